@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libcolimoe.so")
 SOURCES = ["route.hip", "forward.hip", "down_rows.hip", "prefill.hip", "prefill_mx.hip", "layer.hip", "debug.hip",
-           "api.hip"]
+           "api.hip", "mla_append.hip", "mla_gemm.hip", "mla_decode.hip", "mla_prefill.hip", "mla_api.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

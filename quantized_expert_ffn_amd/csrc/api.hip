@@ -156,6 +156,10 @@ bool use_persistent(const coli_moe_dims *d, int S, bool pending) {
 
 namespace coli {
 
+int api_fail(int code, const char *text) { return fail(code, "%s", text); }
+
+int api_check_device() { return check_device(); }
+
 // The kind of the launches the calling thread is making (-1: none).
 thread_local int tl_kind = -1;
 
@@ -664,6 +668,8 @@ int coli_moe_status(void *ws, void *stream) {
     if (s & ST_TIMEOUT)
         return fail(COLI_EHIP, "a kernel's wait for the other workgroups of its launch timed out: not all of them "
                                "were resident (status 0x%x)", s);
+    if (s & ST_BADPAGE)
+        return fail(COLI_EINVAL, "a cache slot, page id, length or row offset is out of range (status 0x%x)", s);
     if (s & ST_BADINDEX) return fail(COLI_EINVAL, "expert index out of range or repeated within a token (status 0x%x)", s);
     if (s & ST_NONFINITE) return fail(COLI_ENONFINITE, "non-finite input or undefined gate weights (status 0x%x)", s);
     return fail(COLI_ENOTRESIDENT, "a routed expert blob was NULL (status 0x%x)", s);

@@ -25,6 +25,7 @@ enum : uint32_t {
     ST_BADINDEX = 2u,      // expert index out of range or repeated in a token
     ST_NOTRESIDENT = 4u,   // routed expert blob pointer is NULL
     ST_TIMEOUT = 8u,       // a wait for other workgroups of the launch gave up (bounded spin)
+    ST_BADPAGE = 16u,      // latent attention: a slot, page id, length or row offset out of range
 };
 
 // Device-scope (all L2 slices) relaxed accesses, for data exchanged between

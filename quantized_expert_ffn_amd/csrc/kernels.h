@@ -199,6 +199,11 @@ inline hipError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t s
 // Raises `kern`'s dynamic-LDS limit to at least `smem` bytes (once per
 // kernel and size, so launches under stream capture only enqueue work).
 hipError_t ensure_dyn_smem(const void *kern, size_t smem);
+
+// For entry points in other files: sets coli_moe_last_error()'s text and
+// returns the code; 0 or COLI_EHIP for the current device.
+int api_fail(int code, const char *text);
+int api_check_device();
 void timing_before(int kind, hipStream_t st);
 void timing_after(int kind, hipStream_t st);
 

@@ -1,0 +1,148 @@
+"""Latent attention: the library exports what include/coli_mla.h declares, and refuses bad arguments on the host,
+before it looks for a device."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import quantized_expert_ffn_amd as q
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P = 1 << 20   # an address that is never followed: every call here is refused first
+
+
+def test_names_match_the_header():
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "coli_mla.h")).read(), flags=re.S)
+    declared = sorted(set(re.findall(r"\b(coli_mla_\w+)\s*\(", text)))
+    assert sorted(q.MLA_EXPORTS) == declared
+    lib = ctypes.CDLL(q.LIB_PATH)
+    for n in declared:
+        assert hasattr(lib, n) and callable(getattr(q, n))
+
+
+def _dims(**kw):
+    base = dict(n_heads=5, rank=512, nope=128, v_dim=128, page_size=48)
+    base.update(kw)
+    return q.make_mla_dims(**base)
+
+
+@pytest.mark.parametrize("field,value", [
+    ("n_heads", 0), ("n_heads", 257), ("rank", 0), ("rank", 384), ("nope", 192), ("v_dim", 64), ("page_size", 0),
+    ("page_size", 65537), ("dtype", 2), ("kv_format", 2), ("kv_format", -1), ("rope_style", 2), ("norm_eps", -1.0),
+    ("norm_eps", float("nan")), ("softmax_scale", 0.0), ("softmax_scale", float("inf"))])
+def test_dims_are_checked(field, value):
+    d = _dims()
+    setattr(d, field, value)
+    assert q.coli_mla_row_bytes(d) == 0
+    assert field.split("_")[0] in q.coli_moe_last_error()
+    with pytest.raises(q.ColiError) as e:
+        q.coli_mla_workspace_bytes(d, 0)
+    assert e.value.code == q.COLI_EINVAL
+
+
+def test_sizes():
+    assert q.coli_mla_row_bytes(_dims()) == 1152
+    assert q.coli_mla_row_bytes(_dims(rank=256, kv_format=q.COLI_KV_E4M3)) == 384
+    assert q.coli_mla_workspace_bytes(_dims()) >= 256
+    for bad in ((-1, 1, 0), (4097, 1, 0), (1, 0, 0), (1, 4000, 5), (1, 1, -1)):
+        with pytest.raises(q.ColiError):
+            q.coli_mla_workspace_bytes(_dims(), *bad)
+    assert q.make_mla_dims(1, 512, 192, 256, 64).softmax_scale == pytest.approx(1 / 16)
+    with pytest.raises(TypeError):
+        q.make_mla_dims(1, 512, 192, 256, 64, dtype=torch.float32)
+
+
+def _ref(d):
+    return ctypes.byref(d)
+
+
+CALLS = {
+    "append": (lambda d, n=3, kv_a=P, g=P, pos=P, slots=P, freq=P, qp=P, qts=320, qhs=64, qo=P, ots=320, ohs=64, pages=P,
+               scale=None, n_pages=4, ws=P, wsb=256:
+               q._lib.coli_mla_append(_ref(d), n, kv_a, g, pos, slots, freq, qp, qts, qhs, qo, ots, ohs, pages, scale,
+                                      n_pages, ws, wsb, None),
+               [dict(n=-1), dict(kv_a=None), dict(pos=None), dict(slots=None), dict(freq=None), dict(qp=None),
+                dict(qo=None), dict(kv_a=P + 8), dict(g=P + 2), dict(qp=P + 4), dict(qo=P + 4), dict(qts=-8),
+                dict(qhs=63), dict(ots=4), dict(ohs=1), dict(pages=None), dict(pages=P + 8), dict(scale=P),
+                dict(n_pages=0), dict(ws=None), dict(ws=P + 4)]),
+    "decode": (lambda d, batch=2, n_q=1, ql=P, qp=P, pages=P, scale=None, n_pages=4, table=P, width=2, lens=P, max_kv=90,
+               out=P, lse=P, ws=P, wsb=1 << 40:
+               q._lib.coli_mla_decode(_ref(d), batch, n_q, ql, qp, pages, scale, n_pages, table, width, lens, max_kv,
+                                      out, lse, ws, wsb, None),
+               [dict(batch=-1), dict(batch=4097), dict(n_q=0), dict(n_q=4000), dict(max_kv=-1), dict(ql=None),
+                dict(qp=None), dict(table=None), dict(lens=None), dict(out=None), dict(ql=P + 2), dict(qp=P + 2),
+                dict(out=P + 2), dict(width=0), dict(width=1), dict(max_kv=97), dict(pages=None), dict(scale=P),
+                dict(n_pages=-1), dict(ws=None)]),
+    "expand": (lambda d, batch=2, rows=7, pages=P, scale=None, n_pages=4, table=P, width=2, cu=P, w=P, kv=P, kp=P, ws=P,
+               wsb=256:
+               q._lib.coli_mla_expand(_ref(d), batch, rows, pages, scale, n_pages, table, width, cu, w, kv, kp, ws, wsb,
+                                      None),
+               [dict(batch=-1), dict(rows=-1), dict(table=None), dict(cu=None), dict(w=None), dict(kv=None),
+                dict(kp=None), dict(w=P + 2), dict(kv=P + 2), dict(kp=P + 2), dict(width=0), dict(pages=None),
+                dict(scale=P), dict(n_pages=0), dict(ws=None)]),
+    "prefill": (lambda d, batch=2, nq=7, nk=9, qq=P, qts=960, qhs=192, kn=P, kts=1280, khs=256, kp=P, v=P, vts=1280,
+                vhs=256, cq=P, ck=P, max_q=5, causal=1, out=P, lse=P, ws=P, wsb=256:
+                q._lib.coli_mla_prefill(_ref(d), batch, nq, nk, qq, qts, qhs, kn, kts, khs, kp, v, vts, vhs, cq, ck,
+                                        max_q, causal, out, lse, ws, wsb, None),
+                [dict(batch=-1), dict(nq=-1), dict(nk=-1), dict(max_q=-1), dict(causal=2), dict(qq=None), dict(kn=None),
+                 dict(kp=None), dict(v=None), dict(cq=None), dict(ck=None), dict(out=None), dict(qq=P + 2),
+                 dict(kn=P + 2), dict(kp=P + 2), dict(v=P + 2), dict(out=P + 2), dict(qts=4), dict(qhs=-8),
+                 dict(kts=1), dict(khs=4), dict(vts=-8), dict(vhs=12), dict(ws=None)]),
+}
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_bad_arguments_are_refused(name):
+    call, bads = CALLS[name]
+    for bad in bads:
+        assert call(_dims(), **bad) == q.COLI_EINVAL, bad
+    assert call(_dims(), wsb=0) == q.COLI_EWORKSPACE
+    d = _dims()
+    d.rank = 100
+    assert call(d) == q.COLI_EINVAL
+    e4m3 = _dims(kv_format=q.COLI_KV_E4M3)
+    if name != "prefill":
+        assert call(e4m3) == q.COLI_EINVAL   # no kv_scale
+
+
+@pytest.mark.parametrize("name,empty", [("append", dict(n=0)), ("decode", dict(batch=0)), ("expand", dict(rows=0)),
+                                        ("expand", dict(batch=0)), ("prefill", dict(nq=0)), ("prefill", dict(max_q=0)),
+                                        ("prefill", dict(batch=0))])
+def test_empty_calls_are_no_ops(name, empty):
+    assert CALLS[name][0](_dims(), **empty) == q.COLI_OK
+
+
+def test_project_arguments():
+    def call(dt=0, n=3, h=5, a=128, b=512, x=P, ts=640, hs=128, w=P, out=P):
+        return q._lib.coli_mla_project(dt, n, h, a, b, x, ts, hs, w, out, None)
+    for bad in (dict(dt=2), dict(n=-1), dict(h=0), dict(h=257), dict(a=96), dict(a=0), dict(a=1088), dict(b=32),
+                dict(b=4160), dict(x=None), dict(w=None), dict(out=None), dict(x=P + 2), dict(w=P + 2),
+                dict(out=P + 2), dict(ts=-8), dict(hs=4)):
+        assert call(**bad) == q.COLI_EINVAL, bad
+    assert call(n=0) == q.COLI_OK
+
+
+def test_binding_refuses_what_does_not_fit():
+    """Types, shapes and devices, on CPU tensors: nothing gets as far as the library."""
+    d = _dims()
+    bf = torch.bfloat16
+    kv_a, ws = torch.zeros(3, 576, dtype=bf), torch.zeros(256, dtype=torch.uint8)
+    pages = torch.zeros(4, 48, 576, dtype=bf)
+    with pytest.raises(ValueError, match="device"):
+        q.coli_mla_append(d, kv_a, None, None, None, None, None, None, pages, None, ws)
+    with pytest.raises(TypeError, match="pages: dtype"):
+        q.coli_mla_append(d, kv_a, None, None, None, None, None, None, pages.half(), None, ws)
+    with pytest.raises(ValueError, match="pages: shape"):
+        q.coli_mla_append(d, kv_a, None, None, None, None, None, None, pages[:, :, :512], None, ws)
+    with pytest.raises(TypeError, match="x: dtype"):
+        q.coli_mla_project(torch.zeros(1, 1, 64), torch.zeros(1, 64, 64), torch.zeros(1, 1, 64))
+    with pytest.raises(ValueError, match="rows for"):
+        q.coli_mla_decode(d, torch.zeros(3, 5, 512, dtype=bf), None, pages, None, None, torch.zeros(2, dtype=torch.int32),
+                          5, None, None, ws)
+    with pytest.raises(ValueError, match="overlap"):
+        q.mla._distinct(torch.zeros(64, dtype=bf).expand(2, 5, 64), (0, 0), "o")
+    q.mla._distinct(torch.zeros(2, 5, 64), (320, 64), "o")
+    q.mla._distinct(torch.zeros(2, 5, 192)[..., 128:], (960, 192), "o")
+    q.mla._distinct(torch.zeros(5, 2, 64).transpose(0, 1), (64, 128), "o")
