@@ -1,0 +1,141 @@
+// Matrix-core operations of the latent-attention kernels on gfx950, in
+// bfloat16 and binary16 with binary32 accumulation, and what feeds them.
+//
+// v_mfma_f32_32x32x16: C[32x32] += A[32x16] B[16x32].  Lane layout:
+//   A: lane l holds A[i][k], i = l % 32, k = 8 (l / 32) + j, in element j;
+//   B: lane l holds B[k][n], n = l % 32, k likewise;
+//   C: register r of lane l holds C[i][n], n = l % 32,
+//      i = 8 (r / 4) + 4 (l / 32) + r % 4.
+// The kernels form transposed scores S^T = K Q^T, so that a lane holds sixteen
+// keys of one query: its softmax needs one exchange between the lane halves.
+// Registers 8 s .. 8 s + 7 are then, as they stand, the B operand of O^T +=
+// V^T P^T if element j of the A operand's lane half h is the value of key
+// 16 s + 8 (j / 4) + 4 h + j % 4: the transposing LDS reads take a row address
+// a lane, so that order costs nothing and P never leaves its registers.
+#pragma once
+
+#include "mla_common.h"
+
+namespace coli {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <class T>
+__device__ __forceinline__ f32x16 mfma32(x8<T> a, x8<T> b, f32x16 c);
+template <>
+__device__ __forceinline__ f32x16 mfma32<__bf16>(x8<__bf16> a, x8<__bf16> b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x16 mfma32<_Float16>(x8<_Float16> a, x8<_Float16> b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// LDS is addressed by byte offset from the start of the workgroup's dynamic
+// allocation, which begins at offset 0 (the kernels declare no static LDS).
+template <class V>
+__device__ __forceinline__ V lds_read(uint32_t off) {
+    return *(const __attribute__((address_space(3))) V *)off;
+}
+template <class V>
+__device__ __forceinline__ void lds_write(uint32_t off, V v) {
+    *(__attribute__((address_space(3))) V *)off = v;
+}
+
+// Transposing reads.  Sixteen lanes read a block of rows of 16 columns and
+// each receives one column: 16-bit elements, four rows, lane x reading columns
+// 4 (x % 4) .. + 3 of row x / 4; bytes, eight rows, lane x reading columns
+// 8 (x % 2) .. + 7 of row x / 2.
+template <class T>
+__device__ __forceinline__ x4<T> lds_read_tr16(uint32_t off) {
+    typedef __attribute__((address_space(3))) s16x4 lds_v;
+    return __builtin_bit_cast(x4<T>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v *)off));
+}
+__device__ __forceinline__ u32x2 lds_read_tr8(uint32_t off) {
+    typedef int i32x2 __attribute__((ext_vector_type(2)));
+    typedef __attribute__((address_space(3))) i32x2 lds_v;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v *)off));
+}
+
+// Eight E4M3 codes as eight values of T: exact in both types (four
+// significant bits, exponents -9 .. 8).
+template <class T>
+__device__ __forceinline__ x8<T> widen8(u32x2 c);
+template <>
+__device__ __forceinline__ x8<__bf16> widen8<__bf16>(u32x2 c) {
+    x8<__bf16> o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const x2<__bf16> a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, false);
+        const x2<__bf16> b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, true);
+        o[4 * i] = a[0];
+        o[4 * i + 1] = a[1];
+        o[4 * i + 2] = b[0];
+        o[4 * i + 3] = b[1];
+    }
+    return o;
+}
+template <>
+__device__ __forceinline__ x8<_Float16> widen8<_Float16>(u32x2 c) {
+    x8<_Float16> o;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const x2<_Float16> a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[i], 1.0f, false);
+        const x2<_Float16> b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[i], 1.0f, true);
+        o[4 * i] = a[0];
+        o[4 * i + 1] = a[1];
+        o[4 * i + 2] = b[0];
+        o[4 * i + 3] = b[1];
+    }
+    return o;
+}
+
+// The larger of a lane's value and the other lane half's.
+__device__ __forceinline__ float half_max(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// 16 bytes of each lane straight into LDS: lane l's land at lds + 16 l (lds
+// uniform over the wavefront).  Done when the wavefront's vmcnt says so.
+// Written in assembly because the compiler otherwise waits for every such
+// load before the next LDS read of any buffer; no register is an output.  The
+// wait state is the one between a write of m0 and a load that reads it; OFF
+// moves both addresses.
+template <int OFF = 0>
+__device__ __forceinline__ void load_to_lds(const void *src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off offset:%2" ::"v"(src), "s"(__builtin_amdgcn_readfirstlane((int)lds)), "n"(OFF)
+                 : "memory");
+}
+
+// A value that is the same in every lane, as a scalar.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    return ((int64_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)v);
+}
+
+// Waits until at most N of the wavefront's vector-memory operations are out.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    static_assert(N < 64, "vmcnt has six bits");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Makes the compiler wait for a value it loaded here, not at its first use.
+template <class V>
+__device__ __forceinline__ void arrived(V &v) {
+    asm volatile("" : "+v"(v));
+}
+
+// A workgroup barrier that waits for this wavefront's LDS accesses, but not
+// for its loads from memory.
+__device__ __forceinline__ void barrier_lds() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+}  // namespace coli
