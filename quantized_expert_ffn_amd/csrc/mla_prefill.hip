@@ -1,55 +1,272 @@
-// Attention of prompts over expanded keys and values.  One pass over the
-// keys with the running maximum and sum of the softmax; a wavefront takes
-// one (query, head).
-#include "mla_common.h"
+// Attention of prompts over expanded keys and values:
+//
+//   s_ij = scale (<q_i, k_j> + <p_i, r_j>),  out_i = sum_j e^{s_ij} v_j / sum_j e^{s_ij}
+//
+// over the keys j that query i sees, in one pass with the running maximum and
+// sum of the softmax.
+#include "kernels.h"
+#include "mla_mfma.h"
 
 namespace coli {
 namespace {
 
-template <class T, int NOPE, int V>
-__global__ __launch_bounds__(256) void k_mla_prefill(MlaPrefillArgs a) {
-    constexpr int KP = NOPE / 64, VP = V / 64;
-    const int lane = threadIdx.x & 63, i = blockIdx.x * 4 + (threadIdx.x >> 6), h = blockIdx.y, b = blockIdx.z;
-    const int q0 = a.cu_q[b], n = a.cu_q[b + 1] - q0, k0 = a.cu_k[b], m_keys = a.cu_k[b + 1] - k0;
-    if (q0 < 0 || n < 0 || q0 + n > a.n_q_rows || n > a.max_q || k0 < 0 || m_keys < 0 || k0 + m_keys > a.n_k_rows) {
-        if (threadIdx.x == 0) raise_status(a.status, ST_BADPAGE);
+constexpr int PRE_TILE = 64;     // keys a tile
+constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
+// The running maximum moves only when a score exceeds it by this many powers
+// of two: weights then reach 2^8, which both types hold, and most tiles spare
+// the pass over the accumulators.
+constexpr float MAX_LAG = 8.0f;
+
+// NW wavefronts of 32 queries each share the tiles of keys and values.
+template <class T_, int NOPE_, int V_, int NW_>
+struct Pre {
+    using T = T_;
+    static constexpr int NOPE = NOPE_, V = V_, NW = NW_;
+    static constexpr int ROWS = 32 * NW;
+    static constexpr int KS = (NOPE + MLA_ROPE) / 16;   // matrix steps of a score
+    static constexpr int KB = (NOPE + MLA_ROPE) / 64;   // blocks of eight 16-byte chunks in a key,
+    static constexpr int VB = V / 64;                   // and in a value
+    static constexpr int CT = V / 32;
+    static constexpr int KTILE = PRE_TILE * 128 * KB, TILE = KTILE + PRE_TILE * 128 * VB;
+    static constexpr int LDS = 2 * TILE;
+};
+
+// As in the decode kernel: LDS holds a tile as [8 tokens][8 chunks] blocks of
+// 1 KiB, chunk c of token t at position c ^ swz(t) of its 128 bytes.
+__device__ __forceinline__ int pre_swz(int t) { return (t & 6) | ((t >> 3) & 1); }
+
+template <class D>
+__global__ __launch_bounds__(64 * D::NW, 1) void k_mla_prefill(MlaPrefillArgs a, int blocks) {
+    using T = typename D::T;
+    constexpr int V = D::V, CT = D::CT, KS = D::KS, THREADS = 64 * D::NW;
+    constexpr float NEG = -__builtin_inff();
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), n = lane & 31, hf = lane >> 5;
+
+    // Workgroups go to the eight XCDs in turn; a run of them on one XCD takes the blocks of one head, whose keys its L2
+    // then holds, the longest first.
+    const int total = gridDim.x, share = (total + 7) / 8, rest = total - (share - 1) * 8;
+    const int xcd = blockIdx.x & 7, nth = blockIdx.x >> 3;
+    const int id = xcd < rest ? xcd * share + nth : rest * share + (xcd - rest) * (share - 1) + nth;
+    const int b = id / (blocks * a.heads), h = id / blocks % a.heads, blk = blocks - 1 - id % blocks;
+
+    const int q0 = uniform(a.cu_q[b]), nq = uniform(a.cu_q[b + 1]) - q0;
+    const int k0 = uniform(a.cu_k[b]), nk = uniform(a.cu_k[b + 1]) - k0;
+    if (q0 < 0 || nq < 0 || nq > a.n_q_rows - q0 || nq > a.max_q || k0 < 0 || nk < 0 || nk > a.n_k_rows - k0) {
+        if (tid == 0) raise_status(a.status, ST_BADPAGE);
         return;
     }
-    if (i >= n) return;
-    const int seen = a.causal ? min(m_keys, i + m_keys - n + 1) : m_keys;
-    const T *q = static_cast<const T *>(a.q) + (q0 + i) * a.q_ts + h * a.q_hs;
-    float qn[KP], o[VP];
-    for (int x = 0; x < KP; ++x) qn[x] = (float)q[64 * x + lane];
-    for (int x = 0; x < VP; ++x) o[x] = 0.0f;
-    const float qp = (float)q[NOPE + lane];
-    float m = -__builtin_inff(), l = 0.0f;
-    for (int t = 0; t < seen; ++t) {
-        const T *k = static_cast<const T *>(a.k_nope) + (k0 + t) * a.k_ts + h * a.k_hs;
-        const T *v = static_cast<const T *>(a.v) + (k0 + t) * a.v_ts + h * a.v_hs;
-        float s = qp * (float)static_cast<const T *>(a.k_pe)[(int64_t)(k0 + t) * MLA_ROPE + lane];
-        for (int x = 0; x < KP; ++x) s = __builtin_fmaf(qn[x], (float)k[64 * x + lane], s);
-        s = wave_sum(s) * a.scale;
-        const float top = fmaxf(m, s), f = expf(m - top), p = expf(s - top);
-        l = l * f + p;
-        for (int x = 0; x < VP; ++x) o[x] = o[x] * f + p * (float)v[64 * x + lane];
-        m = top;
+    const int row0 = blk * D::ROWS, wrow = row0 + 32 * wave, row = wrow + n;
+    if (row0 >= nq) return;
+    const int shift = a.causal ? nk - nq + 1 : nk;            // query i sees shift + i (or all nk) keys
+    auto sees = [&](int i) { return min(nk, max(0, a.causal ? shift + i : nk)); };
+    const int last = min(row0 + D::ROWS, nq) - 1;
+    const int tiles = (sees(last) + PRE_TILE - 1) / PRE_TILE;
+    const int block_seen = sees(row0);                        // keys every query of the block sees,
+    const int wave_seen = sees(min(wrow, nq - 1));            // every query of the wavefront,
+    const int wave_any = wrow < nq ? sees(min(wrow + 31, nq - 1)) : 0;   // any of them
+    const int seen = sees(min(row, nq - 1));
+
+    // ---- lane addresses inside a tile
+    uint32_t ka[4], va[4];
+    {
+        const int f = pre_swz(n);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) ka[v] = (n >> 3) * D::KB * 1024 + (n & 7) * 128 + (((2 * v + hf) ^ f) << 4);
+        const int x = lane & 15, cb = (lane >> 4) & 1, t8 = 4 * hf + (x >> 2);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {   // va[2 e + (ct & 1)], e the token group of a step
+            const int e = v >> 1, fv = pre_swz(8 * e + t8);
+            va[v] = D::KTILE + e * D::VB * 1024 + t8 * 128 + (((4 * (v & 1) + 2 * cb + ((x & 3) >> 1)) ^ fv) << 4) + 8 * (x & 1);
+        }
     }
-    const int64_t row = (int64_t)(q0 + i) * a.heads + h;
-    for (int x = 0; x < VP; ++x) static_cast<T *>(a.out)[row * V + 64 * x + lane] = (T)(seen > 0 ? o[x] / l : 0.0f);
-    if (a.lse && lane == 0) a.lse[row] = seen > 0 ? m + logf(l) : -__builtin_inff();
+
+    // ---- loads: chunk lane % 8 of tokens 8 g + lane / 8, groups g = wave, wave + NW, ..
+    const char *kn = reinterpret_cast<const char *>(static_cast<const T *>(a.k_nope) + k0 * a.k_ts + h * a.k_hs);
+    const char *kp = reinterpret_cast<const char *>(static_cast<const T *>(a.k_pe) + (int64_t)k0 * MLA_ROPE);
+    const char *vv = reinterpret_cast<const char *>(static_cast<const T *>(a.v) + k0 * a.v_ts + h * a.v_hs);
+    auto issue = [&](int tile) {
+        const uint32_t base = (tile & 1) * D::TILE;
+#pragma unroll
+        for (int i = 0; i < 8 / D::NW; ++i) {
+            const int g = wave + i * D::NW, t8 = 8 * g + (lane >> 3);
+            const int64_t t = min(tile * PRE_TILE + t8, nk - 1);   // behind the end: the last again
+            const int chunk = ((lane & 7) ^ pre_swz(t8)) << 4;
+            const char *pn = kn + t * (2 * a.k_ts) + chunk, *pv = vv + t * (2 * a.v_ts) + chunk;
+            const char *pp = kp + t * (2 * MLA_ROPE) + chunk;
+            const uint32_t dk = base + g * D::KB * 1024, dv = base + D::KTILE + g * D::VB * 1024;
+#pragma unroll
+            for (int c = 0; c < D::KB - 1; ++c) load_to_lds(pn + 128 * c, dk + 1024 * c);
+            load_to_lds(pp, dk + 1024 * (D::KB - 1));
+#pragma unroll
+            for (int c = 0; c < D::VB; ++c) load_to_lds(pv + 128 * c, dv + 1024 * c);
+        }
+    };
+    if (tiles > 0) issue(0);
+
+    x8<T> qf[KS];
+    {
+        const T *q = static_cast<const T *>(a.q) + (q0 + min(row, nq - 1)) * a.q_ts + h * a.q_hs + 8 * hf;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qf[s] = *reinterpret_cast<const x8<T> *>(q + 16 * s);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) arrived(qf[s]);
+    }
+    f32x16 o[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[c][r] = 0.0f;
+    float m = NEG, l = 0.0f;
+    const float scale = a.scale * LOG2E;
+    bool odd = false;   // a value that is not finite was set aside
+
+    for (int tile = 0; tile < tiles; ++tile) {
+        const int t0 = tile * PRE_TILE;
+        const uint32_t base = (tile & 1) * D::TILE;
+        wait_vm<0>();
+        barrier_lds();   // the tile is there, and every wavefront is done with the one before
+        if (tile + 1 < tiles) issue(tile + 1);
+        if (block_seen < nk && t0 + PRE_TILE > block_seen) {
+            // A tile that some queries see only in part: values that are not finite would reach those that do not see
+            // them as 0 * NaN.  They are set aside, and added at the end where they are seen.
+            const int from = block_seen > t0 ? block_seen - t0 : 0;
+            for (int i = tid; i < (PRE_TILE - from) * D::VB * 8; i += THREADS) {
+                const int t = from + i / (D::VB * 8), c = i % (D::VB * 8);
+                const uint32_t w = base + D::KTILE + ((t >> 3) * D::VB + (c >> 3)) * 1024 + (t & 7) * 128 + ((c & 7) << 4);
+                x8<T> v = lds_read<x8<T>>(w);
+                bool bad = false;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (!finite_f32((float)v[k])) {
+                        v[k] = (T)0.0f;
+                        bad = true;
+                    }
+                if (bad) lds_write(w, v);
+                odd |= bad;
+            }
+            barrier_lds();
+        }
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh) {
+            const int tw = t0 + 32 * kh;
+            if (tw >= wave_any) break;
+            const uint32_t kb = base + kh * 4 * D::KB * 1024, vb = base + kh * 4 * D::VB * 1024;
+            f32x16 s;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = 0.0f;
+            x8<T> ahead[2][2];   // operands two reads ahead of their products
+            auto fetch = [&](int i) { return lds_read<x8<T>>(kb + ka[i & 3] + (i >> 2) * 1024); };
+            ahead[0][0] = fetch(0);
+            ahead[0][1] = fetch(1);
+#pragma unroll
+            for (int c = 0; c < KS; c += 2) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (c + 2 < KS) {
+                    ahead[(c / 2 + 1) & 1][0] = fetch(c + 2);
+                    ahead[(c / 2 + 1) & 1][1] = fetch(c + 3);
+                }
+                s = mfma32<T>(ahead[(c / 2) & 1][0], qf[c], s);
+                s = mfma32<T>(ahead[(c / 2) & 1][1], qf[c + 1], s);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (tw + 32 > wave_seen) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (tw + 8 * (r >> 2) + 4 * hf + (r & 3) >= seen) s[r] = NEG;
+            }
+            float top = s[0];
+#pragma unroll
+            for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+            top = half_max(top) * scale;
+            if (__ballot(top > m + MAX_LAG)) {
+                const float to = top > m + MAX_LAG ? top : m;
+                const float f = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+                l *= f;
+                m = to;
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[c][r] *= f;
+            }
+            const float ref = m == NEG ? 0.0f : m;
+            float sum = 0.0f;
+            x8<T> p[2];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale, -ref));
+                sum += w;
+                p[r >> 3][r & 7] = (T)w;
+            }
+            l += sum;
+            u32x4 av[2][2];   // a column tile's two matrix steps
+            auto fetch_v = [&](int c, int k) {
+                const uint32_t w = vb + 2 * k * D::VB * 1024 + (c >> 1) * 1024;
+                const u32x2 v0 = __builtin_bit_cast(u32x2, lds_read_tr16<T>(w + va[c & 1]));
+                const u32x2 v1 = __builtin_bit_cast(u32x2, lds_read_tr16<T>(w + va[2 + (c & 1)]));
+                return u32x4{v0[0], v0[1], v1[0], v1[1]};
+            };
+            av[0][0] = fetch_v(0, 0);
+            av[0][1] = fetch_v(0, 1);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (c + 1 < CT) {
+                    av[(c + 1) & 1][0] = fetch_v(c + 1, 0);
+                    av[(c + 1) & 1][1] = fetch_v(c + 1, 1);
+                }
+                o[c] = mfma32<T>(__builtin_bit_cast(x8<T>, av[c & 1][0]), p[0], o[c]);
+                o[c] = mfma32<T>(__builtin_bit_cast(x8<T>, av[c & 1][1]), p[1], o[c]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    l = half_sum(l);
+    if (row < nq) {
+        const int64_t r = (int64_t)(q0 + row) * a.heads + h;
+        const float f = l == 0.0f ? 0.0f : 1.0f / l;
+        T *dst = static_cast<T *>(a.out) + r * V + 4 * hf;
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                x4<T> v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = (T)(o[c][4 * q + i] * f);
+                *reinterpret_cast<x4<T> *>(dst + 32 * c + 8 * q) = v;
+            }
+        if (a.lse && hf == 0) a.lse[r] = l == 0.0f ? NEG : (m + __builtin_amdgcn_logf(l)) * LN2;
+    }
+    if (__syncthreads_or(odd)) {
+        // the values set aside: their column of every query that sees them
+        for (int c = tid; c < V; c += THREADS)
+            for (int t = block_seen; t < sees(last); ++t) {
+                const float x = (float)reinterpret_cast<const T *>(vv)[t * a.v_ts + c];
+                if (finite_f32(x)) continue;
+                for (int i = row0; i <= last; ++i)
+                    if (t < sees(i)) {
+                        T *dst = static_cast<T *>(a.out) + ((int64_t)(q0 + i) * a.heads + h) * V + c;
+                        *dst = (T)((float)*dst + x);
+                    }
+            }
+    }
+}
+
+template <class D>
+hipError_t launch(const MlaPrefillArgs &a, hipStream_t st) {
+    const int blocks = (a.max_q + D::ROWS - 1) / D::ROWS;
+    const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_mla_prefill<D>), D::LDS);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_mla_prefill<D>, dim3((uint32_t)blocks * a.heads * a.batch), dim3(64 * D::NW), D::LDS, st, a, blocks);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_mla_prefill(const MlaPrefillArgs &a, const coli_mla_dims &d, hipStream_t st) {
-    const dim3 grid((a.max_q + 3) / 4, a.heads, a.batch);
     return mla_with_type(d.dtype, [&](auto t) {
         using T = decltype(t);
-        if (d.nope == 128)
-            hipLaunchKernelGGL((k_mla_prefill<T, 128, 128>), grid, dim3(256), 0, st, a);
-        else
-            hipLaunchKernelGGL((k_mla_prefill<T, 192, 256>), grid, dim3(256), 0, st, a);
-        return hipGetLastError();
+        return d.nope == 128 ? launch<Pre<T, 128, 128, 8>>(a, st) : launch<Pre<T, 192, 256, 8>>(a, st);
     });
 }
 
