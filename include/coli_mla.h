@@ -68,10 +68,11 @@ typedef struct coli_mla_dims {
     float softmax_scale; /* > 0, finite */
 } coli_mla_dims;
 
-/* Most query rows of one sequence in one decode call (n_q * n_heads), and
- * most sequences. */
+/* Most query rows of one sequence in one decode call (n_q * n_heads), most
+ * sequences, and most cached tokens (batch * max_kv). */
 #define COLI_MLA_MAX_ROWS 16384
 #define COLI_MLA_MAX_BATCH 4096
+#define COLI_MLA_MAX_TOKENS (1ll << 36)
 
 /* Bytes of one cached token (0 when dims are invalid). */
 size_t coli_mla_row_bytes(const coli_mla_dims *dims);

@@ -31,8 +31,10 @@ FLAGS = [
 
 
 # Per-source additions: the matrix-core kernels keep their products in
-# ordinary VGPRs (their f32 epilogue reads every product once).
-EXTRA = {"prefill.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# ordinary VGPRs (the prefill's f32 epilogue reads every product once, the
+# latent attention's softmax every score).
+_VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+EXTRA = {"prefill.hip": _VGPR_FORM, "mla_decode.hip": _VGPR_FORM, "mla_prefill.hip": _VGPR_FORM}
 
 
 def _compile(src: str) -> str:

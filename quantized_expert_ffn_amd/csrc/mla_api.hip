@@ -94,9 +94,10 @@ size_t coli_mla_row_bytes(const coli_mla_dims *d) {
 size_t coli_mla_workspace_bytes(const coli_mla_dims *d, int32_t batch, int32_t n_q, int32_t max_kv) {
     if (check_mla_dims(d) != COLI_OK) return 0;
     if (batch < 0 || batch > COLI_MLA_MAX_BATCH || n_q < 1 || max_kv < 0 ||
-        (int64_t)n_q * d->n_heads > COLI_MLA_MAX_ROWS) {
+        (int64_t)n_q * d->n_heads > COLI_MLA_MAX_ROWS || (int64_t)batch * max_kv > COLI_MLA_MAX_TOKENS) {
         fail(COLI_EINVAL, "batch=%d, n_q=%d, max_kv=%d: batch in 0..%d, n_q >= 1 with n_q * n_heads <= %d, "
-                          "max_kv >= 0", batch, n_q, max_kv, COLI_MLA_MAX_BATCH, COLI_MLA_MAX_ROWS);
+                          "max_kv >= 0 with batch * max_kv <= %lld", batch, n_q, max_kv, COLI_MLA_MAX_BATCH,
+             COLI_MLA_MAX_ROWS, COLI_MLA_MAX_TOKENS);
         return 0;
     }
     return WS_HEAD + (batch ? mla_decode_part_bytes(*d, batch, n_q, max_kv) : 0);
@@ -176,7 +177,9 @@ int coli_mla_decode(const coli_mla_dims *d, int32_t batch, int32_t n_q, const vo
         return fail(COLI_EINVAL, "batch=%d: must be in 0..%d", batch, COLI_MLA_MAX_BATCH);
     if (n_q < 1 || (int64_t)n_q * d->n_heads > COLI_MLA_MAX_ROWS)
         return fail(COLI_EINVAL, "n_q=%d: must be positive, with n_q * n_heads at most %d", n_q, COLI_MLA_MAX_ROWS);
-    if (max_kv < 0) return fail(COLI_EINVAL, "max_kv=%d < 0", max_kv);
+    if (max_kv < 0 || (int64_t)batch * max_kv > COLI_MLA_MAX_TOKENS)
+        return fail(COLI_EINVAL, "max_kv=%d: must not be negative, with batch * max_kv at most %lld", max_kv,
+                    COLI_MLA_MAX_TOKENS);
     if (batch == 0) return COLI_OK;
     if (!q_lat || !q_pe || !table || !kv_lens || !out)
         return fail(COLI_EINVAL, "coli_mla_decode: NULL pointer argument");

@@ -34,12 +34,19 @@ struct Dec {
     static constexpr int KS = (RANK + MLA_ROPE) / 16; // matrix steps of a score
     static constexpr int CT = RANK / 32 / CG;         // 32-column tiles of a wavefront's output
     static constexpr int TILE = DEC_TILE * ROW;
-    static constexpr int L_OFF = 2 * TILE;                    // int64 [2][64]: row offsets of tiles to come
+    static constexpr int QB = KS / 4;                         // blocks of eight chunks in a query row
+    static constexpr int QUERY = ROWS * 128 * QB;
+    // Queries pass through LDS on their way to registers: through the buffer of the tile before, which plain rows fill
+    // alike, or, with codes, through a region of their own.
+    static constexpr int L_OFF = 2 * TILE + (FP8 ? QUERY : 0);  // int64 [2][64]: row offsets of tiles to come
     static constexpr int L_SCALE = L_OFF + 2 * 8 * DEC_TILE;  // float [2][64]: E4M3 scales
     static constexpr int L_TOP = L_SCALE + 2 * 4 * DEC_TILE;  // float [RG][2][32]: maxima, at the end sums
     static constexpr int L_UNIT = L_TOP + RG * 2 * 32 * 4;    // float [2]: largest scale of a tile
-    static constexpr int L_P = L_UNIT + 16;                   // weights: [RG][2][2][64 lanes] of 16 bytes
-    static constexpr int LDS = L_P + RG * 2 * 2048;
+    static constexpr int L_GROW = L_UNIT + 8;                 // int: the last tile whose maxima had to move, counted from 1
+    // weights: [RG][2][2][64 lanes] of 16 bytes (with codes, in the region of the queries, which are in registers then)
+    static constexpr int L_P = FP8 ? 2 * TILE : L_UNIT + 16;
+    static constexpr int LDS = L_UNIT + 16 + (FP8 ? 0 : RG * 2 * 2048);
+    static_assert(LDS <= 160 * 1024, "the LDS of a CU");
     static constexpr int SLOT = ROWS * RANK + 2 * ROWS;       // floats of a partial result
 };
 
@@ -47,213 +54,272 @@ struct Dec {
 // writes its zeros.
 __device__ __forceinline__ int dec_tiles(int len) { return len > 0 ? (len + DEC_TILE - 1) / DEC_TILE : 1; }
 
-__device__ __forceinline__ int wave_scan(int v, int lane) {
-    for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(v, o);
-        if (lane >= o) v += u;
+// Tiles are shared out evenly: workgroup g of `shares` has `per` of the
+// batch's tiles in order, the first `more` workgroups one more.
+struct Shares {
+    int per, more;
+    __device__ __forceinline__ Shares(int tiles, int shares) : per((uint32_t)tiles / (uint32_t)shares), more(tiles - per * shares) {}
+    __device__ __forceinline__ int first(int g) const { return g * per + min(g, more); }
+    __device__ __forceinline__ int owner(int tile) const {
+        const int t = tile - more * (per + 1);
+        return t < 0 ? (uint32_t)tile / (uint32_t)(per + 1) : more + (uint32_t)t / (uint32_t)per;
     }
-    return v;
-}
-
-// Tiles are shared out evenly: workgroup g of `groups` has tiles
-// first(g) .. first(g + 1) - 1 of the batch's tiles in order.
-__device__ __forceinline__ int64_t dec_first(int64_t tiles, int groups, int g) { return tiles * g / groups; }
-__device__ __forceinline__ int dec_owner(int64_t tiles, int groups, int64_t tile) {
-    return (int)(((tile + 1) * groups - 1) / tiles);
-}
+};
 
 // Swizzle of a token's 16-byte chunks: LDS holds a tile as [8 tokens][8
 // chunks] blocks of 1 KiB, which is what a wavefront's load writes, chunk c of
-// token t at position (c ^ swz(t)) of its 128 bytes.  Sixteen tokens' same
-// chunk, and four tokens' neighbouring ones, then lie in sixteen different
-// groups of banks.
-__device__ __forceinline__ int dec_swz(int t) { return (t & 6) | ((t >> 3) & 1); }
+// token t at position (c ^ swz(t)) of its 128 bytes.  The same chunk of
+// sixteen tokens, and what 32 lanes of a transposing read take (four tokens
+// by four chunks, or eight tokens by two for codes), then lie in sixteen
+// different groups of banks.
+template <bool FP8>
+__device__ __forceinline__ int dec_swz(int t) {
+    const int b1 = (t >> 1) & 1, b2 = (t >> 2) & 1, b3 = (t >> 3) & 1;
+    return FP8 ? 4 * b1 + b2 + 2 * b3 : 4 * b1 + 2 * b2 + b3;
+}
 
+// The tiles of a workgroup form one stream, whatever sequences they belong
+// to: page ids are read three tiles ahead, row offsets stand in LDS two ahead,
+// the tiles' loads run one ahead.
+//
+// A tile takes two barriers: one when it has arrived, one when its weights
+// have.  The weights are formed with the maximum of the tiles before, and
+// formed again (a third barrier) only where a score exceeds that by MAX_LAG.
 template <class D>
 __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int groups) {
     using T = typename D::T;
     constexpr int RANK = D::RANK, CT = D::CT, KS = D::KS;
+    constexpr bool FP8 = D::FP8;
     constexpr float NEG = -__builtin_inff();
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int n = lane & 31, hf = lane >> 5;
     const int rg = wave / D::CG, cg = wave % D::CG, th = cg & 1;
     const int g = blockIdx.x, rows = a.n_q * a.heads;
-    const int block_row = blockIdx.y * D::ROWS, wave_row = block_row + 32 * rg;
+    const int block_row = blockIdx.y * D::ROWS, wave_row = block_row + 32 * rg, row = wave_row + n;
     const bool has_rows = wave_row < rows;
 
     // ---- this workgroup's tiles
-    int64_t tiles = 0;
+    auto tiles_of = [&](int b) { return b < a.batch ? dec_tiles(mla_len(a.kv_lens, b, a.max_kv, a.status)) : 0; };
+    int tiles = 0, mine = 0, incl = 0;
     for (int b = 0; b < a.batch; b += 64) {
-        const int len = b + lane < a.batch ? mla_len(a.kv_lens, b + lane, a.max_kv, a.status) : 0;
-        tiles += uniform(__shfl(wave_scan(b + lane < a.batch ? dec_tiles(len) : 0, lane), 63));
+        mine = tiles_of(b + lane);
+        incl = wave_scan(mine);
+        tiles += __builtin_amdgcn_readlane(incl, 63);
     }
-    const int shares = groups < tiles ? groups : (int)tiles;   // none of them empty
+    const int shares = min(groups, tiles);   // none of them empty
     if (g >= shares) return;
-    int64_t at = dec_first(tiles, shares, g);
-    const int64_t stop = dec_first(tiles, shares, g + 1);
-    int seq = 0;
-    int64_t seq_first = 0;
-    {
-        int64_t base = 0;
-        bool found = false;
-        for (int b = 0; b < a.batch; b += 64) {
-            const int mine = b + lane < a.batch ? dec_tiles(mla_len(a.kv_lens, b + lane, a.max_kv, a.status)) : 0;
-            const int incl = wave_scan(mine, lane);
-            const int64_t f = base + incl - mine;
-            if (g == 0 && blockIdx.y == 0 && wave == 0 && b + lane < a.batch) {   // for the join
-                int32_t *plan = reinterpret_cast<int32_t *>(a.part) + 2 * (b + lane);
-                plan[0] = dec_owner(tiles, shares, f);
-                plan[1] = dec_owner(tiles, shares, f + mine - 1);
-            }
-            const uint64_t hit = __ballot(base + incl > at);
-            if (!found && hit) {
-                const int l = __builtin_ctzll(hit);
-                seq = b + l;
-                seq_first = base + __shfl(incl - mine, l);
-                found = true;
-            }
-            base += __shfl(incl, 63);
+    const Shares share(tiles, shares);
+    const int begin = share.first(g), total = share.first(g + 1) - begin;
+    int seq = -1, tile = 0;
+    for (int b = 0, base = 0; b < a.batch; b += 64) {
+        if (a.batch > 64) {
+            mine = tiles_of(b + lane);
+            incl = wave_scan(mine);
         }
+        const int f = base + incl - mine;
+        if (g == 0 && blockIdx.y == 0 && wave == 0 && b + lane < a.batch) {   // for the join
+            int32_t *plan = reinterpret_cast<int32_t *>(a.part) + 2 * (b + lane);
+            plan[0] = share.owner(f);
+            plan[1] = share.owner(f + mine - 1);
+        }
+        const uint64_t hit = __ballot(base + incl > begin);
+        if (seq < 0 && hit) {
+            const int l = __builtin_ctzll(hit);
+            seq = b + l;
+            tile = begin - __builtin_amdgcn_readlane(f, l);
+        }
+        base += __builtin_amdgcn_readlane(incl, 63);
     }
-    seq = uniform(seq);
-    int left = uniform((int)(stop - at));
-    at = uniform64(at - seq_first);  // from here on in tiles of the sequence
+
+    // ---- the stream of page ids, row offsets and loads: every wavefront carries all of it, a token a lane, in straight
+    // lines that fill the shadows of matrix instructions
+    const uint32_t page_inv = 0xffffffffu / (uint32_t)a.c.page;
+    int lens_from = seq, lens = 0;   // lane i: the length of sequence lens_from + i
+    auto load_lens = [&] {
+        lens_from = seq;
+        lens = min(max(a.kv_lens[min(seq + lane, a.batch - 1)], 0), a.max_kv);
+    };
+    load_lens();
+    int next_seq = seq, next_tile = tile, next_len = __builtin_amdgcn_readlane(lens, 0);
+    bool bad_page = false;
+    struct Page {
+        int id, in;   // of token `lane` of a tile
+    };
+    auto page_ids = [&](Page &p) {
+        const int t = max(0, min(next_tile * DEC_TILE + lane, next_len - 1));   // behind the end: the last again
+        const int pi = div_by(t, a.c.page, page_inv);
+        p.in = t - pi * a.c.page;
+        p.id = a.c.table[(int64_t)next_seq * a.c.width + pi];
+        if (next_len == 0) p.id = 0;
+        const bool cross = (next_tile + 1) * DEC_TILE >= next_len;
+        next_tile = cross ? 0 : next_tile + 1;
+        next_seq = cross ? min(next_seq + 1, a.batch - 1) : next_seq;   // behind the last tile: read and not used
+        next_len = __builtin_amdgcn_readlane(lens, next_seq - lens_from);
+    };
+    float sc_next = 0.0f;
+    auto put_offsets = [&](int it, const Page &p) {
+        const bool bad = (uint32_t)p.id >= (uint32_t)a.c.n_pages;
+        bad_page |= bad;
+        const int64_t slot = (int64_t)(bad ? 0 : p.id) * a.c.page + p.in;
+        lds_write<int64_t>(D::L_OFF + 8 * ((it & 1) * DEC_TILE + lane), slot * D::ROW);
+        if (FP8) sc_next = a.c.scale[slot];
+    };
+    auto put_scales = [&](int it) {
+        lds_write<float>(D::L_SCALE + 4 * ((it & 1) * DEC_TILE + lane), sc_next);
+        lds_write<float>(D::L_UNIT + 4 * (it & 1), wave_max(finite_f32(sc_next) ? fabsf(sc_next) : 0.0f));
+    };
+    // what this thread loads: chunk (lane % 8) of tokens 16 wave + lane / 8 and + 8
+    const int lt0 = 16 * wave + (lane >> 3), lt1 = lt0 + 8;
+    const uint8_t *src0 = a.c.pages + (((lane & 7) ^ dec_swz<FP8>(lt0)) << 4);
+    const uint8_t *src1 = a.c.pages + (((lane & 7) ^ dec_swz<FP8>(lt1)) << 4);
+    auto source = [&](int it, int t) { return lds_read<int64_t>(D::L_OFF + 8 * ((it & 1) * DEC_TILE + t)); };
+    auto issue = [&](int it, int c, const uint8_t *p0, const uint8_t *p1) {
+        const uint32_t d = (it & 1) * D::TILE + 2 * wave * D::CB * 1024;
+        load_to_lds(p0 + 128 * c, d + 1024 * c);
+        load_to_lds(p1 + 128 * c, d + (D::CB + c) * 1024);
+    };
+    // A sequence's queries: whole rows into LDS, as a tile's, then every wavefront's operands out of it.
+    x8<T> qf[KS];
+    auto issue_q = [&](int b, uint32_t to) {
+#pragma unroll
+        for (int i = 0; i < D::RG; ++i) {
+            const int grp = wave * D::RG + i, r8 = 8 * grp + (lane >> 3), r = block_row + r8 < rows ? block_row + r8 : 0;
+            const int chunk = 8 * ((lane & 7) ^ dec_swz<false>(r8));
+            const T *ql = static_cast<const T *>(a.q_lat) + ((int64_t)b * rows + r) * RANK + chunk;
+            const T *qp = static_cast<const T *>(a.q_pe) + ((int64_t)b * rows + r) * MLA_ROPE + chunk;
+#pragma unroll
+            for (int c = 0; c < D::QB; ++c) load_to_lds(c < D::QB - 1 ? ql + 64 * c : qp, to + (grp * D::QB + c) * 1024);
+        }
+    };
+    auto read_q = [&](uint32_t from) {
+        const int r = 32 * rg + n, f = dec_swz<false>(r);
+        uint32_t at[8];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) at[v] = from + (r >> 3) * D::QB * 1024 + (r & 7) * 128 + ((v ^ f) << 4);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            // the chunk of this lane half: codes come sixteen to a read, two matrix steps
+            if (FP8 && s < RANK / 16) {
+                const int c = 4 * (s >> 1) + (s & 1);
+                qf[s] = lds_read<x8<T>>(hf ? at[(c + 2) & 7] : at[c & 7], (c >> 3) * 1024);
+            } else {
+                qf[s] = lds_read<x8<T>>(hf ? at[(2 * s + 1) & 7] : at[2 * s & 7], (s >> 2) * 1024);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s) arrived_acc(qf[s]);
+    };
+    issue_q(seq, FP8 ? 2 * D::TILE : D::TILE);
+    Page pages;
+    {
+        Page p0, p1;
+        page_ids(p0);
+        page_ids(p1);
+        page_ids(pages);
+        put_offsets(0, p0);
+        const float sc0 = sc_next;
+        put_offsets(1, p1);
+        const float sc1 = sc_next;
+        sc_next = sc0;
+        if (FP8) put_scales(0);
+        sc_next = sc1;
+    }
+    if (tid == 0) lds_write<int>(D::L_GROW, 0);
+    barrier_lds();
+    {
+        const uint8_t *p0 = src0 + source(0, lt0), *p1 = src1 + source(0, lt1);
+#pragma unroll
+        for (int c = 0; c < D::CB; ++c) issue(0, c, p0, p1);
+        wait_vm<2 * D::CB>();
+        barrier_lds();   // the queries are there
+        read_q(FP8 ? 2 * D::TILE : D::TILE);
+        wait_vm<0>();
+        arrived(pages.id);
+        arrived(sc_next);
+    }
 
     // ---- lane addresses inside a tile
     uint32_t ka[4], va[4];
     {
-        const int t = 32 * th + n, f = dec_swz(t);
+        const int t = 32 * th + n, f = dec_swz<FP8>(t);
 #pragma unroll
         for (int v = 0; v < 4; ++v)
             ka[v] = (t >> 3) * D::CB * 1024 + (t & 7) * 128 + (((2 * v + hf) ^ f) << 4);
         const int x = lane & 15, cb = (lane >> 4) & 1;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-            if (D::FP8) {   // va[ct & 3], matrix step s at + 2 s groups of tokens
-                const int jr = x >> 1, t8 = 4 * hf + (jr & 3);
-                const int fv = dec_swz(8 * (jr >> 2) + t8);
+            if (FP8) {      // va[ct & 3], matrix step s at + 2 s groups of tokens
+                const int jr = x >> 1, t8 = 4 * hf + (jr & 3), fv = dec_swz<FP8>(8 * (jr >> 2) + t8);
                 va[v] = (jr >> 2) * D::CB * 1024 + t8 * 128 + (((2 * v + cb) ^ fv) << 4) + 8 * (x & 1);
             } else {        // va[2 e + (ct & 1)], e the token group of a step
-                const int e = v >> 1, t8 = 4 * hf + (x >> 2);
-                const int fv = dec_swz(8 * e + t8);
-                va[v] = e * D::CB * 1024 + t8 * 128 +
-                        (((4 * (v & 1) + 2 * cb + ((x & 3) >> 1)) ^ fv) << 4) + 8 * (x & 1);
+                const int e = v >> 1, t8 = 4 * hf + (x >> 2), fv = dec_swz<FP8>(8 * e + t8);
+                va[v] = e * D::CB * 1024 + t8 * 128 + (((4 * (v & 1) + 2 * cb + ((x & 3) >> 1)) ^ fv) << 4) + 8 * (x & 1);
             }
         }
     }
-    // what this thread loads: chunk (lane % 8) of tokens 16 wave + lane / 8 and + 8
-    const int lt0 = 16 * wave + (lane >> 3), lt1 = lt0 + 8;
-    const uint8_t *src0 = a.c.pages + (((lane & 7) ^ dec_swz(lt0)) << 4);
-    const uint8_t *src1 = a.c.pages + (((lane & 7) ^ dec_swz(lt1)) << 4);
 
-    while (left > 0) {
-        const int len = uniform(mla_len(a.kv_lens, seq, a.max_kv, a.status));
-        const int n_tiles = dec_tiles(len);
-        const int lo = (int)at, hi = (int)(left < n_tiles - at ? at + left : n_tiles);
-        const int first_j = block_row / a.heads;
-        const int block_seen = len - a.n_q + 1 + first_j;          // tokens every row here sees
-        const int wave_seen = len - a.n_q + 1 + wave_row / a.heads;
-        const int row = wave_row + n;
-        const int seen = row < rows ? len - a.n_q + 1 + row / a.heads : len;
-
-        // The tiles' loads run one tile ahead, their row offsets two, their page ids three.
-        auto token = [&](int tile) { return min(tile * DEC_TILE + tid, len - 1); };   // behind the end: the last again
-        auto page_of = [&](int tile) -> int {
-            return tid < DEC_TILE && tile < hi && len > 0 ? a.c.table[(int64_t)seq * a.c.width + token(tile) / a.c.page] : 0;
-        };
-        auto slot_of = [&](int tile, int pid) -> int64_t {
-            if ((uint32_t)pid >= (uint32_t)a.c.n_pages) {
-                raise_status(a.status, ST_BADPAGE);
-                pid = 0;
-            }
-            return (int64_t)pid * a.c.page + (len > 0 ? token(tile) % a.c.page : 0);
-        };
-        // Offsets (and scales) of a tile, from its page id; the scales are put down a tile later.
-        float sc_next = 0.0f;
-        auto put_offsets = [&](int tile, int pid) {
-            const int64_t slot = slot_of(tile, pid);
-            lds_write<int64_t>(D::L_OFF + 8 * (((tile - lo) & 1) * DEC_TILE + tid), slot * D::ROW);
-            if (D::FP8) sc_next = a.c.scale[slot];
-        };
-        auto put_scales = [&](int tile) {
-            const int buf = (tile - lo) & 1;
-            lds_write<float>(D::L_SCALE + 4 * (buf * DEC_TILE + tid), sc_next);
-            float top = finite_f32(sc_next) ? fabsf(sc_next) : 0.0f;
-            for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-            if (tid == 0) lds_write<float>(D::L_UNIT + 4 * buf, top);
-        };
-        auto issue = [&](int tile) {
-            const int buf = (tile - lo) & 1;
-            const uint8_t *p0 = src0 + lds_read<int64_t>(D::L_OFF + 8 * (buf * DEC_TILE + lt0));
-            const uint8_t *p1 = src1 + lds_read<int64_t>(D::L_OFF + 8 * (buf * DEC_TILE + lt1));
-            const uint32_t d = buf * D::TILE + 2 * wave * D::CB * 1024;
-#pragma unroll
-            for (int c = 0; c < D::CB; ++c) {
-                load_to_lds(p0 + 128 * c, d + 1024 * c);
-                load_to_lds(p1 + 128 * c, d + (D::CB + c) * 1024);
-            }
-        };
-
-        int pid = page_of(lo), pid2 = page_of(lo + 1);
-        __syncthreads();   // LDS of the segment before is free
-        if (wave == 0) {
-            put_offsets(lo, pid);
-            if (D::FP8) put_scales(lo);
-            if (lo + 1 < hi) put_offsets(lo + 1, pid2);
-        }
-        __syncthreads();
-        issue(lo);
-        pid = page_of(lo + 2);
-        x8<T> qf[KS];
-        {
-            const int64_t r = (int64_t)seq * rows + (row < rows ? row : 0);
-            const T *ql = static_cast<const T *>(a.q_lat) + r * RANK, *qp = static_cast<const T *>(a.q_pe) + r * MLA_ROPE;
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const int k = s < RANK / 16 ? (D::FP8 ? 32 * (s >> 1) + 16 * hf + 8 * (s & 1) : 16 * s + 8 * hf)
-                                            : 16 * (s - RANK / 16) + 8 * hf;
-                qf[s] = *reinterpret_cast<const x8<T> *>((s < RANK / 16 ? ql : qp) + k);
-            }
-#pragma unroll
-            for (int s = 0; s < KS; ++s) arrived(qf[s]);
-        }
+    const float scale = a.scale * LOG2E;
+    const uint32_t top_at = D::L_TOP + 4 * (64 * rg + n), p_at = D::L_P + 4096 * rg + 2048 * th + 16 * lane;
+    const int block_j = block_row / a.heads, wave_j = wave_row / a.heads, row_j = row / a.heads;
+    int it = 0;
+    while (it < total) {
+        // ---- a segment: tiles tile .. of one sequence
+        const int len = __builtin_amdgcn_readlane(lens, seq - lens_from), n_tiles = dec_tiles(len);
+        const int lo = tile, hi = min(n_tiles, lo + total - it);
+        const int block_seen = len - a.n_q + 1 + block_j;          // tokens every row here sees,
+        const int wave_seen = len - a.n_q + 1 + wave_j;            // every row of the wavefront
+        const int seen = row < rows ? len - a.n_q + 1 + row_j : len;
+        const bool works = has_rows && len > 0, scores = works && cg < 2;
         f32x16 o[CT];
 #pragma unroll
         for (int c = 0; c < CT; ++c)
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[c][r] = 0.0f;
-        float m = NEG, l = 0.0f, unit = 0.0f;   // unit: E4M3 accumulators are in units of it
-        const bool works = has_rows && len > 0, scores = works && cg < 2;
-        const uint32_t top_at = D::L_TOP + 4 * (64 * rg + n), p_at = D::L_P + 4096 * rg + 16 * lane;
+        float m = NEG, l = 0.0f;
+        float unit = 0.0f, inv = 0.0f;   // E4M3: the accumulators are in units of the largest scale so far; its inverse
 
-        for (int tile = lo; tile < hi; ++tile) {
-            const int buf = (tile - lo) & 1;
+        for (; tile < hi; ++tile, ++it) {
+            const int buf = it & 1, t0 = tile * DEC_TILE, tw = t0 + 32 * th;
             const uint32_t base = buf * D::TILE;
-            const int t0 = tile * DEC_TILE, tw = t0 + 32 * th;
-            wait_vm<0>();
-            arrived(pid);
-            arrived(sc_next);
+            const bool more = it + 1 < total;
             barrier_lds();   // the tile is there, and every wavefront is done with the one before
-            if (tile + 1 < hi) issue(tile + 1);
-
+            const uint8_t *p0 = src0, *p1 = src1;
+            if (more) {
+                p0 += source(it + 1, lt0);
+                p1 += source(it + 1, lt1);
+            }
             f32x16 s;
-            float sc[16];
+            float sc[16], sum = 0.0f;
+            auto weigh = [&] {
+                const float ref = m == NEG ? 0.0f : m;
+                x8<T> p[2];
+                sum = 0.0f;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale, -ref));
+                    sum += w;
+                    if (FP8) w *= sc[r] * inv;
+                    p[r >> 3][r & 7] = (T)w;
+                }
+                lds_write(p_at, p[0], 0);
+                lds_write(p_at, p[1], 1024);
+            };
             if (scores) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = 0.0f;
-                // operands four reads ahead of their products; no more, or the compiler hoists reads until it spills
+                // operands four reads ahead of their products (no more: the compiler would hoist reads until it spills),
+                // the next tile's loads between them
                 u32x4 ahead[2][4];
-                auto fetch = [&](int i) {
-                    const uint32_t w = D::FP8 && i >= RANK / 32 ? base + ka[i & 3] + D::PE * 1024 : base + ka[i & 3] + (i >> 2) * 1024;
-                    return lds_read<u32x4>(w);
-                };
+                uint32_t kb[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) kb[v] = base + ka[v];
                 constexpr int READS = D::CB * 4;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) ahead[0][i] = fetch(i);
-                if (D::FP8) {
+                for (int i = 0; i < 4; ++i) ahead[0][i] = lds_read<u32x4>(kb[i]);
+                if (FP8) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const f32x4 v = lds_read<f32x4>(D::L_SCALE + 4 * (buf * DEC_TILE + 32 * th + 8 * q + 4 * hf));
+                        const f32x4 v = lds_read<f32x4>(D::L_SCALE + 16 * hf + 4 * (buf * DEC_TILE + 32 * th), 32 * q);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) sc[4 * q + i] = v[i];
                     }
@@ -263,9 +329,10 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                     __builtin_amdgcn_sched_barrier(0);
                     if (c + 4 < READS) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) ahead[(c / 4 + 1) & 1][i] = fetch(c + 4 + i);
+                        for (int i = 0; i < 4; ++i) ahead[(c / 4 + 1) & 1][i] = lds_read<u32x4>(kb[i], (c / 4 + 1) * 1024);
                     }
-                    if (D::FP8 && c == RANK / 32) {
+                    if (more) issue(it + 1, c / 4, p0, p1);
+                    if (FP8 && c == RANK / 32) {
 #pragma unroll
                         for (int r = 0; r < 16; ++r) s[r] *= sc[r];
                     }
@@ -273,82 +340,47 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                     for (int i = 0; i < 4; ++i) {
                         const u32x4 w = ahead[(c / 4) & 1][i];
                         const int k = c + i;
-                        if (D::FP8 && k < RANK / 32) {
+                        if (FP8 && k < RANK / 32) {
                             s = mfma32<T>(widen8<T>(u32x2{w[0], w[1]}), qf[2 * k], s);
                             s = mfma32<T>(widen8<T>(u32x2{w[2], w[3]}), qf[2 * k + 1], s);
                         } else {
-                            s = mfma32<T>(__builtin_bit_cast(x8<T>, w), qf[D::FP8 ? k + RANK / 32 : k], s);
+                            s = mfma32<T>(__builtin_bit_cast(x8<T>, w), qf[FP8 ? k + RANK / 32 : k], s);
                         }
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                const float scale = a.scale * LOG2E;
                 if (tw + 32 > wave_seen) {
+                    const int rem = seen - tw - 4 * hf;
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        s[r] = tw + 8 * (r >> 2) + 4 * hf + (r & 3) < seen ? s[r] * scale : NEG;
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s[r] *= scale;
+                        if (8 * (r >> 2) + (r & 3) >= rem) {
+                            s[r] = NEG;
+                            sc[r] = 0.0f;
+                        }
                 }
                 float top = s[0];
 #pragma unroll
                 for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
-                lds_write<float>(top_at + 128 * th, half_max(top));
-            }
-            if (wave == 0 && tile + 1 < hi) {
-                if (D::FP8) put_scales(tile + 1);
-                if (tile + 2 < hi) {
-                    put_offsets(tile + 2, pid);
-                    pid = page_of(tile + 3);
-                }
-            }
-            barrier_lds();
-            if (works) {
-                const float top = fmaxf(lds_read<float>(top_at), lds_read<float>(top_at + 128));
-                float grown = unit;
-                // the largest scale so far: weights times scales stay in the type's range
-                if (D::FP8) grown = fmaxf(unit, lds_read<float>(D::L_UNIT + 4 * buf));
-                if (__ballot(top > m + MAX_LAG || grown > unit)) {
-                    const float to = top > m + MAX_LAG ? top : m;
-                    float f = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-                    l *= f;
-                    m = to;
-                    if (D::FP8 && grown > unit) {
-                        f *= unit / grown;
-                        unit = grown;
-                    }
+                top = half_max(top) * scale;
+                lds_write<float>(top_at + 128 * th, top);
+                bool grows = top > m + MAX_LAG;
+                if (FP8) grows |= lds_read<float>(D::L_UNIT + 4 * buf) > unit;
+                if (__ballot(grows) && lane == 0) lds_write<int>(D::L_GROW, it + 1);
+            } else if (more) {
 #pragma unroll
-                    for (int c = 0; c < CT; ++c)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) o[c][r] *= f;
-                }
-                if (scores) {
-                    const float ref = m == NEG ? 0.0f : m;
-                    const float inv = D::FP8 ? (unit > 0.0f ? 1.0f / unit : 0.0f) : 1.0f;
-                    float sum = 0.0f;
-                    x8<T> p[2];
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        float w = __builtin_amdgcn_exp2f(s[r] - ref);
-                        sum += w;
-                        if (D::FP8) w = s[r] == NEG ? 0.0f : w * (sc[r] * inv);
-                        p[r >> 3][r & 7] = (T)w;
-                    }
-                    l += sum;
-                    lds_write(p_at + 2048 * th, p[0]);
-                    lds_write(p_at + 2048 * th + 1024, p[1]);
-                }
+                for (int c = 0; c < D::CB; ++c) issue(it + 1, c, p0, p1);
             }
+            if (scores) weigh();
             // A tile that some rows see only in part, though its tokens exist: values that are not finite would reach
             // rows that do not see them as 0 * NaN; a row that does see them has them in its scores already.
             if (block_seen < len && t0 + DEC_TILE > block_seen) {
+                barrier_lds();
                 const int from = block_seen > t0 ? block_seen - t0 : 0;
                 constexpr int CH = (D::CB - 1) * 8;
                 for (int i = tid; i < (DEC_TILE - from) * CH; i += 256) {
                     const int t = from + i / CH, c = i % CH;
                     const uint32_t w = base + ((t >> 3) * D::CB + (c >> 3)) * 1024 + (t & 7) * 128 + ((c & 7) << 4);
-                    if (D::FP8) {
+                    if (FP8) {
                         u32x4 v = lds_read<u32x4>(w);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -365,26 +397,55 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                     }
                 }
             }
-            barrier_lds();
-            if (works) {
-                x8<T> p[4];
+            barrier_lds();   // the weights are there
+            const int grow = lds_read<int>(D::L_GROW);
+            x8<T> p[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) p[k] = lds_read<x8<T>>(p_at + 1024 * k);
-                u32x4 ahead[2][4];   // a column tile's four matrix steps (E4M3: two words each)
-                auto fetch = [&](int c, int k) {
-                    const int col = cg * CT + c;
-                    u32x4 v = {0, 0, 0, 0};
-                    if (D::FP8) {
-                        // CT is 2 or a multiple of 4: where it is 2, the column tile's low bits are not c's
-                        const uint32_t lo_bits = CT % 4 ? va[0] ^ ((col & 3) << 5) : va[c & 3];
-                        const u32x2 w = lds_read_tr8(base + lo_bits + 2 * k * D::CB * 1024 + (col >> 2) * 1024);
-                        v[0] = w[0];
-                        v[1] = w[1];
-                        return v;
+            for (int k = 0; k < 4; ++k) p[k] = lds_read<x8<T>>(p_at - 2048 * th, 1024 * k);
+            if (uniform(grow) == it + 1) {
+                barrier_lds();   // read by all
+                if (works) {
+                    const float top = fmaxf(lds_read<float>(top_at), lds_read<float>(top_at, 128));
+                    const float grown = FP8 ? fmaxf(unit, lds_read<float>(D::L_UNIT + 4 * buf)) : 0.0f;
+                    const float to = top > m + MAX_LAG ? top : m;
+                    float f = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+                    l *= f;
+                    m = to;
+                    if (FP8 && grown > unit) {
+                        f *= unit / grown;
+                        unit = grown;
+                        inv = 1.0f / grown;
                     }
-                    const uint32_t w = base + 2 * k * D::CB * 1024 + (col >> 1) * 1024;
-                    const u32x2 v0 = __builtin_bit_cast(u32x2, lds_read_tr16<T>(w + va[c & 1]));
-                    const u32x2 v1 = __builtin_bit_cast(u32x2, lds_read_tr16<T>(w + va[2 + (c & 1)]));
+#pragma unroll
+                    for (int c = 0; c < CT; ++c)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) o[c][r] *= f;
+                    if (scores) weigh();
+                }
+                barrier_lds();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) p[k] = lds_read<x8<T>>(p_at - 2048 * th, 1024 * k);
+            }
+            l += sum;
+            auto stream = [&](int part) {
+                if (part == 0 && FP8) put_scales(it + 1);
+                if (part == 1) put_offsets(it + 2, pages);
+                if (part == 2) page_ids(pages);
+            };
+            if (works) {
+                u32x4 ahead[2][4];   // a column tile's four matrix steps (E4M3: two words each)
+                uint32_t vb[4];      // E4M3, where a wavefront has two column tiles: their low bits differ from c's
+                const int col0 = cg * CT;
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    vb[v] = base + (FP8 && CT % 4 ? va[0] ^ (((col0 + v) & 3) << 5) : va[v]) + (FP8 ? col0 >> 2 : col0 >> 1) * 1024;
+                auto fetch = [&](int c, int k) {
+                    const int imm = 2 * k * D::CB * 1024 + (FP8 ? c >> 2 : c >> 1) * 1024;
+                    if (FP8) {
+                        const u32x2 w = lds_read_tr8(vb[c & 3], imm);
+                        return u32x4{w[0], w[1], 0, 0};
+                    }
+                    const u32x2 v0 = lds_read_tr16(vb[c & 1], imm), v1 = lds_read_tr16(vb[2 + (c & 1)], imm);
                     return u32x4{v0[0], v0[1], v1[0], v1[1]};
                 };
 #pragma unroll
@@ -399,112 +460,150 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const u32x4 w = ahead[c & 1][k];
-                        const x8<T> v = D::FP8 ? widen8<T>(u32x2{w[0], w[1]}) : __builtin_bit_cast(x8<T>, w);
+                        const x8<T> v = FP8 ? widen8<T>(u32x2{w[0], w[1]}) : __builtin_bit_cast(x8<T>, w);
                         o[c] = mfma32<T>(v, p[k], o[c]);
                     }
+                    if (c < 3) stream(c);
+                    if (CT == 2 && c == 1) stream(2);
                 }
                 __builtin_amdgcn_sched_barrier(0);
+            } else {
+                for (int part = 0; part < 3; ++part) stream(part);
             }
+            wait_vm<0>();
+            arrived(pages.id);
+            arrived(sc_next);
         }
 
         // ---- the segment's result: the sums of both halves of the tokens, then out or a partial result
+        const uint32_t spent = ((it - 1) & 1) * D::TILE, q_at = FP8 ? 2 * D::TILE : spent;
         barrier_lds();
-        if (scores) {
-            l = half_sum(l);
-            lds_write<float>(top_at + 128 * th, l);
-        }
+        if (it < total) issue_q(seq + 1, q_at);
+        if (scores) lds_write<float>(top_at + 128 * th, half_sum(l));
+        wait_vm<0>();
         barrier_lds();
-        l = works ? lds_read<float>(top_at) + lds_read<float>(top_at + 128) : 0.0f;
-        if (D::FP8) {
-#pragma unroll
-            for (int c = 0; c < CT; ++c)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) o[c][r] *= unit;
+        l = works ? lds_read<float>(top_at) + lds_read<float>(top_at, 128) : 0.0f;
+        if (it < total) {
+            read_q(q_at);
+            barrier_lds();
         }
+        const float last_unit = FP8 ? unit : 1.0f;
         if (lo == 0 && hi == n_tiles) {
-            if (row < rows) {
-                const int64_t r = (int64_t)seq * rows + row;
-                const float f = l == 0.0f ? 0.0f : 1.0f / l;
-                T *dst = static_cast<T *>(a.out) + r * RANK + cg * CT * 32 + 4 * hf;
+            // through the buffer of the last tile, 64 columns at a time, so that rows leave in whole lines
+            const float f = l == 0.0f ? 0.0f : last_unit / l;
+            const uint32_t at = spent + wave * 32 * 144;
 #pragma unroll
-                for (int c = 0; c < CT; ++c)
+            for (int c = 0; c < CT; c += 2) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        x4<T> v;
+                for (int i = 0; i < 8; ++i) {
+                    x4<T> v;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = (T)(o[c][4 * q + i] * f);
-                        *reinterpret_cast<x4<T> *>(dst + 32 * c + 8 * q) = v;
-                    }
-                if (a.lse && hf == 0 && cg == 0) a.lse[r] = l == 0.0f ? NEG : (m + __builtin_amdgcn_logf(l)) * LN2;
+                    for (int k = 0; k < 4; ++k) v[k] = (T)(o[c + i / 4][4 * (i % 4) + k] * f);
+                    lds_write(at + n * 144 + 8 * hf, v, 64 * (i / 4) + 16 * (i % 4));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 8 * i + (lane >> 3);
+                    const x8<T> v = lds_read<x8<T>>(at + r * 144 + 16 * (lane & 7));
+                    if (wave_row + r < rows)
+                        *reinterpret_cast<x8<T> *>(static_cast<T *>(a.out) + ((int64_t)seq * rows + wave_row + r) * RANK +
+                                                   (cg * CT + c) * 32 + 8 * (lane & 7)) = v;
+                }
             }
+            if (a.lse && row < rows && hf == 0 && cg == 0)
+                a.lse[(int64_t)seq * rows + row] = l == 0.0f ? NEG : (m + __builtin_amdgcn_logf(l)) * LN2;
         } else if (has_rows) {
             // slot 0: the segment begins inside its sequence, slot 1: with it
             const int64_t slot = ((int64_t)blockIdx.y * groups + g) * 2 + (lo == 0 ? 1 : 0);
             float *dst = a.part + 2 * ((a.batch + 7) & ~7) + slot * D::SLOT;
+            float *at = dst + (rg * (RANK / 32) + cg * CT) * 1024 + 4 * lane;
 #pragma unroll
             for (int c = 0; c < CT; ++c)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     f32x4 v;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = o[c][4 * q + i];
-                    *reinterpret_cast<f32x4 *>(dst + ((rg * (RANK / 32) + cg * CT + c) * 4 + q) * 256 + 4 * lane) = v;
+                    for (int i = 0; i < 4; ++i) v[i] = o[c][4 * q + i] * last_unit;
+                    *reinterpret_cast<f32x4 *>(at + (c * 4 + q) * 256) = v;
                 }
             if (hf == 0 && cg == 0)
                 *reinterpret_cast<float2 *>(dst + D::ROWS * RANK + 2 * (32 * rg + n)) = make_float2(m, l);
         }
-        left -= hi - lo;
-        at = 0;
+        tile = 0;
         ++seq;
+        if (seq + 8 >= lens_from + 64 && it < total) load_lens();
     }
+    if (bad_page) raise_status(a.status, ST_BADPAGE);
 }
 
 // Joins the partial results of a sequence: out = sum_g 2^{m_g - M} o_g / sum_g
-// 2^{m_g - M} l_g, over the workgroups in order.  One workgroup takes 32 rows
-// by 8 columns (of each lane half), its wavefronts every fourth partial.
-template <class T, int RANK, int ROWS>
-__global__ __launch_bounds__(256) void k_mla_join(MlaDecodeArgs a, int groups) {
-    constexpr int SLOT = ROWS * RANK + 2 * ROWS;
+// 2^{m_g - M} l_g, over the workgroups in order, 32 rows by 8 columns a
+// wavefront.  DEEP: a workgroup's sixteen wavefronts take every sixteenth
+// partial each of one such piece, for few sequences in many parts; else they
+// take pieces of their own.
+constexpr int JOIN_WAVES = 16;
+template <class T, int RANK, int ROWS, bool DEEP>
+__global__ __launch_bounds__(64 * JOIN_WAVES) void k_mla_join(MlaDecodeArgs a, int groups) {
+    constexpr int SLOT = ROWS * RANK + 2 * ROWS, EVERY = DEEP ? JOIN_WAVES : 1;
     constexpr float NEG = -__builtin_inff();
     const int b = blockIdx.z, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int32_t *plan = reinterpret_cast<const int32_t *>(a.part) + 2 * b;
     const int g0 = plan[0], g1 = plan[1];
     if (g0 == g1) return;
-    __shared__ f32x4 so[4][64];
-    __shared__ float sm[4][64], sl[4][64];
-    const int rgs = blockIdx.y, rb = rgs / (ROWS / 32), rg = rgs % (ROWS / 32), cq = blockIdx.x, n = lane & 31;
+    __shared__ f32x4 so[DEEP ? JOIN_WAVES : 1][64];
+    __shared__ float sm[DEEP ? JOIN_WAVES : 1][64], sl[DEEP ? JOIN_WAVES : 1][64];
+    const int rgs = blockIdx.y, rb = rgs / (ROWS / 32), rg = rgs % (ROWS / 32), n = lane & 31;
+    const int cq = DEEP ? blockIdx.x : blockIdx.x * JOIN_WAVES + wave;
     const float *part = a.part + 2 * ((a.batch + 7) & ~7) + (int64_t)rb * groups * 2 * SLOT;
-    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto slot = [&](int g) { return part + (int64_t)(2 * g + (g == g0 ? 1 : 0)) * SLOT; };
+    auto weight = [](float m, float to) { return m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to); };
     float m = NEG, l = 0.0f;
-#pragma unroll 4
-    for (int g = g0 + wave; g <= g1; g += 4) {
-        const float *p = part + (int64_t)(2 * g + (g == g0 ? 1 : 0)) * SLOT;
-        const float2 ml = *reinterpret_cast<const float2 *>(p + ROWS * RANK + 2 * (32 * rg + n));
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(p + (rg * (RANK / 32) * 4 + cq) * 256 + 4 * lane);
-        const float to = fmaxf(m, ml.x);
-        const float fa = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-        const float fb = ml.x == to ? 1.0f : __builtin_amdgcn_exp2f(ml.x - to);
-        l = l * fa + ml.y * fb;
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int AHEAD = 8;   // partials read together
+    for (int g = g0 + (DEEP ? wave : 0); g <= g1; g += AHEAD * EVERY) {
+        float2 ml[AHEAD];
+        f32x4 v[AHEAD];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = o[i] * fa + v[i] * fb;
+        for (int i = 0; i < AHEAD; ++i) {
+            const float *p = slot(min(g + i * EVERY, g1));
+            ml[i] = *reinterpret_cast<const float2 *>(p + ROWS * RANK + 2 * (32 * rg + n));
+            v[i] = *reinterpret_cast<const f32x4 *>(p + (rg * (RANK / 32) * 4 + cq) * 256 + 4 * lane);
+        }
+        float to = m;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) to = fmaxf(to, ml[i].x);
+        const float old = weight(m, to);
+        l *= old;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] *= old;
         m = to;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (g + i * EVERY <= g1) {
+                const float f = weight(ml[i].x, m);
+                l = __builtin_fmaf(ml[i].y, f, l);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] = __builtin_fmaf(v[i][k], f, o[k]);
+            }
     }
-    so[wave][lane] = o;
-    sm[wave][lane] = m;
-    sl[wave][lane] = l;
-    __syncthreads();
-    if (wave) return;
+    if (DEEP) {
+        so[wave][lane] = o;
+        sm[wave][lane] = m;
+        sl[wave][lane] = l;
+        __syncthreads();
+        if (wave) return;
 #pragma unroll
-    for (int w = 1; w < 4; ++w) {
-        const float mb = sm[w][lane], lb = sl[w][lane];
-        const f32x4 v = so[w][lane];
-        const float to = fmaxf(m, mb);
-        const float fa = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-        const float fb = mb == to ? 1.0f : __builtin_amdgcn_exp2f(mb - to);
-        l = l * fa + lb * fb;
+        for (int w = 1; w < JOIN_WAVES; ++w) m = fmaxf(m, sm[w][lane]);
+        o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        l = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = o[i] * fa + v[i] * fb;
-        m = to;
+        for (int w = 0; w < JOIN_WAVES; ++w) {
+            const float f = weight(sm[w][lane], m);
+            const f32x4 v = so[w][lane];
+            l = __builtin_fmaf(sl[w][lane], f, l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(v[i], f, o[i]);
+        }
     }
     const int rows = a.n_q * a.heads, row = 32 * rgs + n;
     if (row >= rows) return;
@@ -516,6 +615,9 @@ __global__ __launch_bounds__(256) void k_mla_join(MlaDecodeArgs a, int groups) {
     *reinterpret_cast<x4<T> *>(static_cast<T *>(a.out) + r * RANK + 8 * cq + 4 * (lane >> 5)) = v;
     if (a.lse && cq == 0 && lane < 32) a.lse[r] = l == 0.0f ? NEG : (m + __builtin_amdgcn_logf(l)) * LN2;
 }
+
+// A join of at most this many groups of 32 rows is a deep one.
+constexpr int JOIN_DEEP = 16;
 
 // Rows of a workgroup, and how many workgroups share the batch's tiles: as
 // many as fill the 256 CUs once (a workgroup's LDS and registers take one).
@@ -535,9 +637,15 @@ hipError_t launch(const MlaDecodeArgs &a, hipStream_t st) {
     const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_mla_decode<D>), D::LDS);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k_mla_decode<D>, dim3(groups, blocks), dim3(256), D::LDS, st, a, groups);
-    if (groups > 1)
-        hipLaunchKernelGGL((k_mla_join<typename D::T, D::RANK, D::ROWS>),
-                           dim3(D::RANK / 8, (rows + 31) / 32, a.batch), dim3(256), 0, st, a, groups);
+    if (groups > 1) {
+        const int rgs = (rows + 31) / 32, pieces = D::RANK / 8;
+        if ((int64_t)a.batch * rgs <= JOIN_DEEP)
+            hipLaunchKernelGGL((k_mla_join<typename D::T, D::RANK, D::ROWS, true>), dim3(pieces, rgs, a.batch),
+                               dim3(64 * JOIN_WAVES), 0, st, a, groups);
+        else
+            hipLaunchKernelGGL((k_mla_join<typename D::T, D::RANK, D::ROWS, false>), dim3(pieces / JOIN_WAVES, rgs, a.batch),
+                               dim3(64 * JOIN_WAVES), 0, st, a, groups);
+    }
     return hipGetLastError();
 }
 

@@ -34,28 +34,28 @@ __device__ __forceinline__ f32x16 mfma32<_Float16>(x8<_Float16> a, x8<_Float16> 
 
 // LDS is addressed by byte offset from the start of the workgroup's dynamic
 // allocation, which begins at offset 0 (the kernels declare no static LDS).
+// `imm` is a constant the instruction's offset field takes.
 template <class V>
-__device__ __forceinline__ V lds_read(uint32_t off) {
-    return *(const __attribute__((address_space(3))) V *)off;
+__device__ __forceinline__ V lds_read(uint32_t off, int imm = 0) {
+    return *(const __attribute__((address_space(3))) V *)((const __attribute__((address_space(3))) char *)off + imm);
 }
 template <class V>
-__device__ __forceinline__ void lds_write(uint32_t off, V v) {
-    *(__attribute__((address_space(3))) V *)off = v;
+__device__ __forceinline__ void lds_write(uint32_t off, V v, int imm = 0) {
+    *(__attribute__((address_space(3))) V *)((__attribute__((address_space(3))) char *)off + imm) = v;
 }
 
 // Transposing reads.  Sixteen lanes read a block of rows of 16 columns and
 // each receives one column: 16-bit elements, four rows, lane x reading columns
 // 4 (x % 4) .. + 3 of row x / 4; bytes, eight rows, lane x reading columns
 // 8 (x % 2) .. + 7 of row x / 2.
-template <class T>
-__device__ __forceinline__ x4<T> lds_read_tr16(uint32_t off) {
+__device__ __forceinline__ u32x2 lds_read_tr16(uint32_t off, int imm) {
     typedef __attribute__((address_space(3))) s16x4 lds_v;
-    return __builtin_bit_cast(x4<T>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v *)off));
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v *)((__attribute__((address_space(3))) char *)off + imm)));
 }
-__device__ __forceinline__ u32x2 lds_read_tr8(uint32_t off) {
+__device__ __forceinline__ u32x2 lds_read_tr8(uint32_t off, int imm) {
     typedef int i32x2 __attribute__((ext_vector_type(2)));
     typedef __attribute__((address_space(3))) i32x2 lds_v;
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v *)off));
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v *)((__attribute__((address_space(3))) char *)off + imm)));
 }
 
 // Eight E4M3 codes as eight values of T: exact in both types (four
@@ -101,6 +101,44 @@ __device__ __forceinline__ float half_sum(float v) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// The largest value of the wavefront, in every lane (rotations within 16
+// lanes, then exchanges of rows and halves; no LDS).
+template <int CTRL>
+__device__ __forceinline__ float dpp_max(float v) {
+    const int x = __builtin_bit_cast(int, v);
+    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(x, x, CTRL, 0xf, 0xf, false)));
+}
+__device__ __forceinline__ float wave_max(float v) {
+    v = dpp_max<0x128>(v);
+    v = dpp_max<0x124>(v);
+    v = dpp_max<0x122>(v);
+    v = dpp_max<0x121>(v);
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+
+// Inclusive sums over the wavefront (shifts within 16 lanes, then broadcasts
+// of the rows before).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+    v = dpp_add<0x111, 0xf>(v);
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    v = dpp_add<0x118, 0xf>(v);
+    v = dpp_add<0x142, 0xa>(v);
+    return dpp_add<0x143, 0xc>(v);
+}
+
+// t / d for 0 <= t < 2^31 with inv = (2^32 - 1) / d: the product falls short
+// of the quotient by one at most.
+__device__ __forceinline__ int div_by(int t, int d, uint32_t inv) {
+    const int q = (int)__umulhi((uint32_t)t, inv);
+    return t - q * d >= d ? q + 1 : q;
+}
+
 // 16 bytes of each lane straight into LDS: lane l's land at lds + 16 l (lds
 // uniform over the wavefront).  Done when the wavefront's vmcnt says so.
 // Written in assembly because the compiler otherwise waits for every such
@@ -130,6 +168,13 @@ __device__ __forceinline__ void wait_vm() {
 template <class V>
 __device__ __forceinline__ void arrived(V &v) {
     asm volatile("" : "+v"(v));
+}
+
+// The same for a matrix operand that is to stay in an accumulation register:
+// the matrix instructions read it there.
+template <class V>
+__device__ __forceinline__ void arrived_acc(V &v) {
+    asm volatile("" : "+a"(v));
 }
 
 // A workgroup barrier that waits for this wavefront's LDS accesses, but not

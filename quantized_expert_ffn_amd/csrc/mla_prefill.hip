@@ -33,7 +33,7 @@ struct Pre {
 
 // As in the decode kernel: LDS holds a tile as [8 tokens][8 chunks] blocks of
 // 1 KiB, chunk c of token t at position c ^ swz(t) of its 128 bytes.
-__device__ __forceinline__ int pre_swz(int t) { return (t & 6) | ((t >> 3) & 1); }
+__device__ __forceinline__ int pre_swz(int t) { return 4 * ((t >> 1) & 1) + 2 * ((t >> 2) & 1) + ((t >> 3) & 1); }
 
 template <class D>
 __global__ __launch_bounds__(64 * D::NW, 1) void k_mla_prefill(MlaPrefillArgs a, int blocks) {
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(64 * D::NW, 1) void k_mla_prefill(MlaPrefillArgs a,
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = 0.0f;
             x8<T> ahead[2][2];   // operands two reads ahead of their products
-            auto fetch = [&](int i) { return lds_read<x8<T>>(kb + ka[i & 3] + (i >> 2) * 1024); };
+            auto fetch = [&](int i) { return lds_read<x8<T>>(kb + ka[i & 3], (i >> 2) * 1024); };
             ahead[0][0] = fetch(0);
             ahead[0][1] = fetch(1);
 #pragma unroll
@@ -200,9 +200,8 @@ __global__ __launch_bounds__(64 * D::NW, 1) void k_mla_prefill(MlaPrefillArgs a,
             l += sum;
             u32x4 av[2][2];   // a column tile's two matrix steps
             auto fetch_v = [&](int c, int k) {
-                const uint32_t w = vb + 2 * k * D::VB * 1024 + (c >> 1) * 1024;
-                const u32x2 v0 = __builtin_bit_cast(u32x2, lds_read_tr16<T>(w + va[c & 1]));
-                const u32x2 v1 = __builtin_bit_cast(u32x2, lds_read_tr16<T>(w + va[2 + (c & 1)]));
+                const int imm = 2 * k * D::VB * 1024 + (c >> 1) * 1024;
+                const u32x2 v0 = lds_read_tr16(vb + va[c & 1], imm), v1 = lds_read_tr16(vb + va[2 + (c & 1)], imm);
                 return u32x4{v0[0], v0[1], v1[0], v1[1]};
             };
             av[0][0] = fetch_v(0, 0);
