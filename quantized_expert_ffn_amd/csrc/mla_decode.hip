@@ -54,15 +54,17 @@ struct Dec {
 // writes its zeros.
 __device__ __forceinline__ int dec_tiles(int len) { return len > 0 ? (len + DEC_TILE - 1) / DEC_TILE : 1; }
 
-// Tiles are shared out evenly: workgroup g of `shares` has `per` of the
-// batch's tiles in order, the first `more` workgroups one more.
+// Work is shared out evenly in units: a sequence of n tiles is n + 1 of them,
+// unit 0 standing for its queries and its results, which cost about a tile,
+// unit k > 0 for tile k - 1.  Workgroup g of `shares` has `per` units in order,
+// the first `more` workgroups one more.
 struct Shares {
     int per, more;
-    __device__ __forceinline__ Shares(int tiles, int shares) : per((uint32_t)tiles / (uint32_t)shares), more(tiles - per * shares) {}
+    __device__ __forceinline__ Shares(int units, int shares) : per((uint32_t)units / (uint32_t)shares), more(units - per * shares) {}
     __device__ __forceinline__ int first(int g) const { return g * per + min(g, more); }
-    __device__ __forceinline__ int owner(int tile) const {
-        const int t = tile - more * (per + 1);
-        return t < 0 ? (uint32_t)tile / (uint32_t)(per + 1) : more + (uint32_t)t / (uint32_t)per;
+    __device__ __forceinline__ int owner(int unit) const {
+        const int t = unit - more * (per + 1);
+        return t < 0 ? (uint32_t)unit / (uint32_t)(per + 1) : more + (uint32_t)t / (uint32_t)per;
     }
 };
 
@@ -98,7 +100,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
     const int block_row = blockIdx.y * D::ROWS, wave_row = block_row + 32 * rg, row = wave_row + n;
     const bool has_rows = wave_row < rows;
 
-    // ---- this workgroup's tiles
+    // ---- this workgroup's tiles: `total` of them from tile `tile` of sequence `seq`
     auto tiles_of = [&](int b) { return b < a.batch ? dec_tiles(mla_len(a.kv_lens, b, a.max_kv, a.status)) : 0; };
     int tiles = 0, mine = 0, incl = 0;
     for (int b = 0; b < a.batch; b += 64) {
@@ -106,30 +108,35 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
         incl = wave_scan(mine);
         tiles += __builtin_amdgcn_readlane(incl, 63);
     }
-    const int shares = min(groups, tiles);   // none of them empty
+    const int shares = min(groups, tiles);
     if (g >= shares) return;
-    const Shares share(tiles, shares);
-    const int begin = share.first(g), total = share.first(g + 1) - begin;
-    int seq = -1, tile = 0;
+    const Shares share(tiles + a.batch, shares);
+    const int begin = share.first(g), end = share.first(g + 1);
+    int seq = -1, tile = 0, total = 0;
     for (int b = 0, base = 0; b < a.batch; b += 64) {
         if (a.batch > 64) {
             mine = tiles_of(b + lane);
             incl = wave_scan(mine);
         }
-        const int f = base + incl - mine;
-        if (g == 0 && blockIdx.y == 0 && wave == 0 && b + lane < a.batch) {   // for the join
+        const bool real = b + lane < a.batch;
+        const int f = base + incl - mine + b + lane;   // the sequence's unit 0
+        if (g == 0 && blockIdx.y == 0 && wave == 0 && real) {   // for the join
             int32_t *plan = reinterpret_cast<int32_t *>(a.part) + 2 * (b + lane);
-            plan[0] = share.owner(f);
-            plan[1] = share.owner(f + mine - 1);
+            plan[0] = share.owner(f + 1);
+            plan[1] = share.owner(f + mine);
         }
-        const uint64_t hit = __ballot(base + incl > begin);
+        // its tiles here: those of the units in [begin, end)
+        const int from = min(max(begin - f - 1, 0), mine), to = min(max(end - f - 1, 0), mine);
+        const uint64_t hit = __ballot(real && to > from);
         if (seq < 0 && hit) {
             const int l = __builtin_ctzll(hit);
             seq = b + l;
-            tile = begin - __builtin_amdgcn_readlane(f, l);
+            tile = __builtin_amdgcn_readlane(from, l);
         }
+        total += __builtin_amdgcn_readlane(wave_scan(real ? to - from : 0), 63);
         base += __builtin_amdgcn_readlane(incl, 63);
     }
+    if (total == 0) return;
 
     // ---- the stream of page ids, row offsets and loads: every wavefront carries all of it, a token a lane, in straight
     // lines that fill the shadows of matrix instructions
@@ -209,13 +216,27 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
 #pragma unroll
         for (int s = 0; s < KS; ++s) arrived_acc(qf[s]);
     };
-    issue_q(seq, FP8 ? 2 * D::TILE : D::TILE);
+    // Brings the lines of a sequence's queries into the L2: a word of each, ROWS / 256 threads a row.
+    uint32_t touched[3] = {0, 0, 0};
+    auto touch_q = [&](int b) {
+        constexpr int PER = 256 / D::ROWS, LINES = RANK / 64 / PER;   // threads and latent lines: 4 and 2 or 1, 8 and 1 or 0
+        const int r8 = tid / PER, r = block_row + r8 < rows ? block_row + r8 : 0;
+        const uint8_t *ql = reinterpret_cast<const uint8_t *>(static_cast<const T *>(a.q_lat) + ((int64_t)b * rows + r) * RANK);
+        const uint8_t *qp = reinterpret_cast<const uint8_t *>(static_cast<const T *>(a.q_pe) + ((int64_t)b * rows + r) * MLA_ROPE);
+        touched[0] = *reinterpret_cast<const uint32_t *>(qp);
+        touched[1] = *reinterpret_cast<const uint32_t *>(ql + tid % PER % (RANK / 64) * 128);
+        if (LINES == 2) touched[2] = *reinterpret_cast<const uint32_t *>(ql + (tid % PER + PER) * 128);
+    };
     Page pages;
     {
         Page p0, p1;
         page_ids(p0);
         page_ids(p1);
         page_ids(pages);
+        arrived(p0.id);
+        arrived(p1.id);
+        arrived(pages.id);
+        issue_q(seq, FP8 ? 2 * D::TILE : D::TILE);
         put_offsets(0, p0);
         const float sc0 = sc_next;
         put_offsets(1, p1);
@@ -288,6 +309,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                 p0 += source(it + 1, lt0);
                 p1 += source(it + 1, lt1);
             }
+            if (tile + 1 == hi && it + 1 < total) touch_q(seq + 1);
             f32x16 s;
             float sc[16], sum = 0.0f;
             auto weigh = [&] {
@@ -473,6 +495,8 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
             wait_vm<0>();
             arrived(pages.id);
             arrived(sc_next);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) arrived(touched[i]);
         }
 
         // ---- the segment's result: the sums of both halves of the tokens, then out or a partial result
@@ -541,9 +565,9 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
 // wavefront.  DEEP: a workgroup's sixteen wavefronts take every sixteenth
 // partial each of one such piece, for few sequences in many parts; else they
 // take pieces of their own.
-constexpr int JOIN_WAVES = 16;
+constexpr int JOIN_WAVES = 16;   // of a deep one; else four
 template <class T, int RANK, int ROWS, bool DEEP>
-__global__ __launch_bounds__(64 * JOIN_WAVES) void k_mla_join(MlaDecodeArgs a, int groups) {
+__global__ __launch_bounds__(DEEP ? 64 * JOIN_WAVES : 256) void k_mla_join(MlaDecodeArgs a, int groups) {
     constexpr int SLOT = ROWS * RANK + 2 * ROWS, EVERY = DEEP ? JOIN_WAVES : 1;
     constexpr float NEG = -__builtin_inff();
     const int b = blockIdx.z, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -553,13 +577,13 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void k_mla_join(MlaDecodeArgs a, i
     __shared__ f32x4 so[DEEP ? JOIN_WAVES : 1][64];
     __shared__ float sm[DEEP ? JOIN_WAVES : 1][64], sl[DEEP ? JOIN_WAVES : 1][64];
     const int rgs = blockIdx.y, rb = rgs / (ROWS / 32), rg = rgs % (ROWS / 32), n = lane & 31;
-    const int cq = DEEP ? blockIdx.x : blockIdx.x * JOIN_WAVES + wave;
+    const int cq = DEEP ? blockIdx.x : blockIdx.x * 4 + wave;
     const float *part = a.part + 2 * ((a.batch + 7) & ~7) + (int64_t)rb * groups * 2 * SLOT;
     auto slot = [&](int g) { return part + (int64_t)(2 * g + (g == g0 ? 1 : 0)) * SLOT; };
     auto weight = [](float m, float to) { return m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to); };
     float m = NEG, l = 0.0f;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int AHEAD = 8;   // partials read together
+    constexpr int AHEAD = DEEP ? 8 : 4;   // partials read together
     for (int g = g0 + (DEEP ? wave : 0); g <= g1; g += AHEAD * EVERY) {
         float2 ml[AHEAD];
         f32x4 v[AHEAD];
@@ -643,8 +667,8 @@ hipError_t launch(const MlaDecodeArgs &a, hipStream_t st) {
             hipLaunchKernelGGL((k_mla_join<typename D::T, D::RANK, D::ROWS, true>), dim3(pieces, rgs, a.batch),
                                dim3(64 * JOIN_WAVES), 0, st, a, groups);
         else
-            hipLaunchKernelGGL((k_mla_join<typename D::T, D::RANK, D::ROWS, false>), dim3(pieces / JOIN_WAVES, rgs, a.batch),
-                               dim3(64 * JOIN_WAVES), 0, st, a, groups);
+            hipLaunchKernelGGL((k_mla_join<typename D::T, D::RANK, D::ROWS, false>), dim3(pieces / 4, rgs, a.batch),
+                               dim3(256), 0, st, a, groups);
     }
     return hipGetLastError();
 }
