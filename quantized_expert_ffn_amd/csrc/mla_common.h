@@ -16,7 +16,7 @@ template <class T>
 using x4 = T __attribute__((ext_vector_type(4)));
 template <class T>
 using x2 = T __attribute__((ext_vector_type(2)));
-typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // Row of a cache that holds token t of sequence b; a page id outside the
 // cache raises the status and reads as page 0.

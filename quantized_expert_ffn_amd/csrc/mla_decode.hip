@@ -372,7 +372,8 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 if (tw + 32 > wave_seen) {
-                    const int rem = seen - tw - 4 * hf;
+                    int rem = seen - tw - 4 * hf;
+                    arrived(rem);   // a branch, not selects that every tile would pay for
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
                         if (8 * (r >> 2) + (r & 3) >= rem) {

@@ -10,25 +10,30 @@
 namespace coli {
 namespace {
 
-constexpr int PRE_TILE = 64;     // keys a tile
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 // The running maximum moves only when a score exceeds it by this many powers
 // of two: weights then reach 2^8, which both types hold, and most tiles spare
 // the pass over the accumulators.
 constexpr float MAX_LAG = 8.0f;
 
-// NW wavefronts of 32 queries each share the tiles of keys and values.
-template <class T_, int NOPE_, int V_, int NW_>
+// NW wavefronts share tiles of KT keys and values: NW / KG groups of 32
+// queries, each of KG wavefronts that take 32 keys of a tile each.
+template <class T_, int NOPE_, int V_, int NW_, int KT_, int KG_>
 struct Pre {
     using T = T_;
-    static constexpr int NOPE = NOPE_, V = V_, NW = NW_;
-    static constexpr int ROWS = 32 * NW;
+    static constexpr int NOPE = NOPE_, V = V_, NW = NW_, KT = KT_, KG = KG_;
+    static constexpr int ROWS = 32 * NW / KG;
     static constexpr int KS = (NOPE + MLA_ROPE) / 16;   // matrix steps of a score
     static constexpr int KB = (NOPE + MLA_ROPE) / 64;   // blocks of eight 16-byte chunks in a key,
     static constexpr int VB = V / 64;                   // and in a value
     static constexpr int CT = V / 32;
-    static constexpr int KTILE = PRE_TILE * 128 * KB, TILE = KTILE + PRE_TILE * 128 * VB;
-    static constexpr int LDS = 2 * TILE;
+    static constexpr int KTILE = KT * 128 * KB, TILE = KTILE + KT * 128 * VB;
+    static constexpr int L_ML = NW * (CT / 2) * 4096;   // to join the keys' halves: accumulators, then pairs [NW][32]
+    static_assert(KG == 1 || KT == 64, "two halves of 32 keys");
+    static constexpr int JOIN = KG == 2 ? L_ML + NW * 32 * 8 : 0;
+    static constexpr int STAGES = 3 * TILE <= 160 * 1024 ? 3 : 2;   // tiles in LDS: loads run one or two ahead
+    static constexpr int LDS = STAGES * TILE > JOIN ? STAGES * TILE : JOIN;
+    static constexpr int LOADS = KT / 8 / NW * (KB + VB);            // of a wavefront, for a tile
 };
 
 // As in the decode kernel: LDS holds a tile as [8 tokens][8 chunks] blocks of
@@ -36,18 +41,28 @@ struct Pre {
 __device__ __forceinline__ int pre_swz(int t) { return 4 * ((t >> 1) & 1) + 2 * ((t >> 2) & 1) + ((t >> 3) & 1); }
 
 template <class D>
-__global__ __launch_bounds__(64 * D::NW, 1) void k_mla_prefill(MlaPrefillArgs a, int blocks) {
+__global__ __launch_bounds__(64 * D::NW, 2) void k_mla_prefill(MlaPrefillArgs a, int blocks) {
     using T = typename D::T;
     constexpr int V = D::V, CT = D::CT, KS = D::KS, THREADS = 64 * D::NW;
     constexpr float NEG = -__builtin_inff();
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), n = lane & 31, hf = lane >> 5;
 
-    // Workgroups go to the eight XCDs in turn; a run of them on one XCD takes the blocks of one head, whose keys its L2
-    // then holds, the longest first.
-    const int total = gridDim.x, share = (total + 7) / 8, rest = total - (share - 1) * 8;
-    const int xcd = blockIdx.x & 7, nth = blockIdx.x >> 3;
-    const int id = xcd < rest ? xcd * share + nth : rest * share + (xcd - rest) * (share - 1) + nth;
-    const int b = id / (blocks * a.heads), h = id / blocks % a.heads, blk = blocks - 1 - id % blocks;
+    // Workgroups go to the eight XCDs in turn; the blocks of one head of one sequence stay on one XCD, whose L2 then holds
+    // its keys, the longest first.
+    const int pair = (blockIdx.x & 7) + 8 * ((blockIdx.x >> 3) / blocks), blk = blocks - 1 - (blockIdx.x >> 3) % blocks;
+    if (pair >= a.batch * a.heads) return;
+    const int h = pair % a.heads;
+    int b = pair / a.heads;
+    if (a.batch > 1 && a.batch <= 64) {
+        // the sequences with the most keys first: a long one begun last would leave the other CUs idle
+        const int keys = lane < a.batch ? a.cu_k[lane + 1] - a.cu_k[lane] : -1;
+        int rank = 0;
+        for (int i = 0; i < a.batch; ++i) {
+            const int other = __builtin_amdgcn_readlane(keys, i);
+            rank += other > keys || (other == keys && i < lane);
+        }
+        b = __builtin_ctzll(__ballot(lane < a.batch && rank == b));
+    }
 
     const int q0 = uniform(a.cu_q[b]), nq = uniform(a.cu_q[b + 1]) - q0;
     const int k0 = uniform(a.cu_k[b]), nk = uniform(a.cu_k[b + 1]) - k0;
@@ -55,12 +70,13 @@ __global__ __launch_bounds__(64 * D::NW, 1) void k_mla_prefill(MlaPrefillArgs a,
         if (tid == 0) raise_status(a.status, ST_BADPAGE);
         return;
     }
-    const int row0 = blk * D::ROWS, wrow = row0 + 32 * wave, row = wrow + n;
+    const int group = wave % (D::NW / D::KG), half = wave / (D::NW / D::KG);   // the keys' half with KG = 2
+    const int row0 = blk * D::ROWS, wrow = row0 + 32 * group, row = wrow + n;
     if (row0 >= nq) return;
     const int shift = a.causal ? nk - nq + 1 : nk;            // query i sees shift + i (or all nk) keys
     auto sees = [&](int i) { return min(nk, max(0, a.causal ? shift + i : nk)); };
     const int last = min(row0 + D::ROWS, nq) - 1;
-    const int tiles = (sees(last) + PRE_TILE - 1) / PRE_TILE;
+    const int tiles = (sees(last) + D::KT - 1) / D::KT;
     const int block_seen = sees(row0);                        // keys every query of the block sees,
     const int wave_seen = sees(min(wrow, nq - 1));            // every query of the wavefront,
     const int wave_any = wrow < nq ? sees(min(wrow + 31, nq - 1)) : 0;   // any of them
@@ -85,11 +101,11 @@ __global__ __launch_bounds__(64 * D::NW, 1) void k_mla_prefill(MlaPrefillArgs a,
     const char *kp = reinterpret_cast<const char *>(static_cast<const T *>(a.k_pe) + (int64_t)k0 * MLA_ROPE);
     const char *vv = reinterpret_cast<const char *>(static_cast<const T *>(a.v) + k0 * a.v_ts + h * a.v_hs);
     auto issue = [&](int tile) {
-        const uint32_t base = (tile & 1) * D::TILE;
+        const uint32_t base = tile % D::STAGES * D::TILE;
 #pragma unroll
-        for (int i = 0; i < 8 / D::NW; ++i) {
+        for (int i = 0; i < D::KT / 8 / D::NW; ++i) {
             const int g = wave + i * D::NW, t8 = 8 * g + (lane >> 3);
-            const int64_t t = min(tile * PRE_TILE + t8, nk - 1);   // behind the end: the last again
+            const int64_t t = min(tile * D::KT + t8, nk - 1);   // behind the end: the last again
             const int chunk = ((lane & 7) ^ pre_swz(t8)) << 4;
             const char *pn = kn + t * (2 * a.k_ts) + chunk, *pv = vv + t * (2 * a.v_ts) + chunk;
             const char *pp = kp + t * (2 * MLA_ROPE) + chunk;
@@ -102,6 +118,7 @@ __global__ __launch_bounds__(64 * D::NW, 1) void k_mla_prefill(MlaPrefillArgs a,
         }
     };
     if (tiles > 0) issue(0);
+    if (D::STAGES == 3 && tiles > 1) issue(1);
 
     x8<T> qf[KS];
     {
@@ -121,16 +138,19 @@ __global__ __launch_bounds__(64 * D::NW, 1) void k_mla_prefill(MlaPrefillArgs a,
     bool odd = false;   // a value that is not finite was set aside
 
     for (int tile = 0; tile < tiles; ++tile) {
-        const int t0 = tile * PRE_TILE;
-        const uint32_t base = (tile & 1) * D::TILE;
-        wait_vm<0>();
+        const int t0 = tile * D::KT;
+        const uint32_t base = tile % D::STAGES * D::TILE;
+        if (D::STAGES == 3 && tile + 1 < tiles)
+            wait_vm<D::LOADS>();
+        else
+            wait_vm<0>();
         barrier_lds();   // the tile is there, and every wavefront is done with the one before
-        if (tile + 1 < tiles) issue(tile + 1);
-        if (block_seen < nk && t0 + PRE_TILE > block_seen) {
+        if (tile + D::STAGES - 1 < tiles) issue(tile + D::STAGES - 1);
+        if (block_seen < nk && t0 + D::KT > block_seen) {
             // A tile that some queries see only in part: values that are not finite would reach those that do not see
             // them as 0 * NaN.  They are set aside, and added at the end where they are seen.
             const int from = block_seen > t0 ? block_seen - t0 : 0;
-            for (int i = tid; i < (PRE_TILE - from) * D::VB * 8; i += THREADS) {
+            for (int i = tid; i < (D::KT - from) * D::VB * 8; i += THREADS) {
                 const int t = from + i / (D::VB * 8), c = i % (D::VB * 8);
                 const uint32_t w = base + D::KTILE + ((t >> 3) * D::VB + (c >> 3)) * 1024 + (t & 7) * 128 + ((c & 7) << 4);
                 x8<T> v = lds_read<x8<T>>(w);
@@ -147,8 +167,8 @@ __global__ __launch_bounds__(64 * D::NW, 1) void k_mla_prefill(MlaPrefillArgs a,
             barrier_lds();
         }
 #pragma unroll
-        for (int kh = 0; kh < 2; ++kh) {
-            const int tw = t0 + 32 * kh;
+        for (int k = 0; k < D::KT / 32 / D::KG; ++k) {
+            const int kh = D::KG == 2 ? half : k, tw = t0 + 32 * kh;
             if (tw >= wave_any) break;
             const uint32_t kb = base + kh * 4 * D::KB * 1024, vb = base + kh * 4 * D::VB * 1024;
             f32x16 s;
@@ -170,9 +190,11 @@ __global__ __launch_bounds__(64 * D::NW, 1) void k_mla_prefill(MlaPrefillArgs a,
             }
             __builtin_amdgcn_sched_barrier(0);
             if (tw + 32 > wave_seen) {
+                int rem = seen - tw - 4 * hf;
+                arrived(rem);   // a branch, not selects that every tile would pay for
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (tw + 8 * (r >> 2) + 4 * hf + (r & 3) >= seen) s[r] = NEG;
+                    if (8 * (r >> 2) + (r & 3) >= rem) s[r] = NEG;
             }
             float top = s[0];
 #pragma unroll
@@ -221,12 +243,47 @@ __global__ __launch_bounds__(64 * D::NW, 1) void k_mla_prefill(MlaPrefillArgs a,
     }
 
     l = half_sum(l);
+    int c0 = 0;
+    if (D::KG == 2) {
+        // each wavefront hands half of its columns to the one with the other keys, and both add first half to second
+        barrier_lds();
+        if (hf == 0) lds_write(D::L_ML + 8 * (32 * wave + n), f32x2{m, l});
+#pragma unroll
+        for (int c = 0; c < CT / 2; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                f32x4 v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = half ? o[c][4 * q + i] : o[CT / 2 + c][4 * q + i];
+                lds_write((wave * (CT / 2) + c) * 4096 + 16 * lane, v, q * 1024);
+            }
+        barrier_lds();
+        const int other = wave ^ (D::NW / 2);
+        const f32x2 ml = lds_read<f32x2>(D::L_ML + 8 * (32 * other + n));
+        const float to = fmaxf(m, ml[0]);
+        const float fa = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+        const float fb = ml[0] == to ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - to);
+        l = half ? ml[1] * fb + l * fa : l * fa + ml[1] * fb;
+        m = to;
+#pragma unroll
+        for (int c = 0; c < CT / 2; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f32x4 v = lds_read<f32x4>((other * (CT / 2) + c) * 4096 + 16 * lane, q * 1024);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float own = half ? o[CT / 2 + c][4 * q + i] : o[c][4 * q + i];
+                    o[c][4 * q + i] = own * fa + v[i] * fb;
+                }
+            }
+        c0 = half * (CT / 2);
+    }
     if (row < nq) {
         const int64_t r = (int64_t)(q0 + row) * a.heads + h;
         const float f = l == 0.0f ? 0.0f : 1.0f / l;
-        T *dst = static_cast<T *>(a.out) + r * V + 4 * hf;
+        T *dst = static_cast<T *>(a.out) + r * V + 32 * c0 + 4 * hf;
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
+        for (int c = 0; c < CT / D::KG; ++c)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 x4<T> v;
@@ -234,7 +291,7 @@ __global__ __launch_bounds__(64 * D::NW, 1) void k_mla_prefill(MlaPrefillArgs a,
                 for (int i = 0; i < 4; ++i) v[i] = (T)(o[c][4 * q + i] * f);
                 *reinterpret_cast<x4<T> *>(dst + 32 * c + 8 * q) = v;
             }
-        if (a.lse && hf == 0) a.lse[r] = l == 0.0f ? NEG : (m + __builtin_amdgcn_logf(l)) * LN2;
+        if (a.lse && hf == 0 && half == 0) a.lse[r] = l == 0.0f ? NEG : (m + __builtin_amdgcn_logf(l)) * LN2;
     }
     if (__syncthreads_or(odd)) {
         // the values set aside: their column of every query that sees them
@@ -256,8 +313,18 @@ hipError_t launch(const MlaPrefillArgs &a, hipStream_t st) {
     const int blocks = (a.max_q + D::ROWS - 1) / D::ROWS;
     const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_mla_prefill<D>), D::LDS);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_mla_prefill<D>, dim3((uint32_t)blocks * a.heads * a.batch), dim3(64 * D::NW), D::LDS, st, a, blocks);
+    hipLaunchKernelGGL(k_mla_prefill<D>, dim3((uint32_t)blocks * 8 * ((a.heads * a.batch + 7) / 8)),
+                       dim3(64 * D::NW), D::LDS, st, a, blocks);
     return hipGetLastError();
+}
+
+template <class T, int NOPE, int V>
+hipError_t by_size(const MlaPrefillArgs &a, hipStream_t st) {
+    // Workgroups of 256 queries if they fill the 256 CUs, else of 128 whose keys two wavefronts share: 512 tokens, 64
+    // heads, widths 192 + 64 and 256: 41 against 33 us; 1024 tokens: 66 against 83 us; 8192: 1.94 against 2.16 ms.
+    const int64_t by_max = (int64_t)a.batch * ((a.max_q + 255) / 256), by_rows = (a.n_q_rows + 255) / 256 + a.batch - 1;
+    if (a.heads * (by_max < by_rows ? by_max : by_rows) < 256) return launch<Pre<T, NOPE, V, 8, 64, 2>>(a, st);
+    return launch<Pre<T, NOPE, V, 8, 64, 1>>(a, st);
 }
 
 }  // namespace
@@ -265,7 +332,7 @@ hipError_t launch(const MlaPrefillArgs &a, hipStream_t st) {
 hipError_t launch_mla_prefill(const MlaPrefillArgs &a, const coli_mla_dims &d, hipStream_t st) {
     return mla_with_type(d.dtype, [&](auto t) {
         using T = decltype(t);
-        return d.nope == 128 ? launch<Pre<T, 128, 128, 8>>(a, st) : launch<Pre<T, 192, 256, 8>>(a, st);
+        return d.nope == 128 ? by_size<T, 128, 128>(a, st) : by_size<T, 192, 256>(a, st);
     });
 }
 
