@@ -3,122 +3,162 @@
 // gathered out of the paged cache).
 //
 // Both keep their reduction dimension contiguous in both operands, so one
-// tiled product serves them: a workgroup of four wavefronts takes TM output
-// features by TN tokens, w as the A operand, so that a lane's results are four
-// consecutive features of one token.  Steps of 32 along k go through a ring
-// of three LDS stages, loaded straight from memory two steps ahead; the
-// results go through LDS once more, to leave in whole rows.
+// tiled product serves them: a workgroup takes tiles of TM output features by
+// its TN tokens, w as the A operand, so that a lane's results are four
+// consecutive features of one token.  Steps of 64 along k, a line of 128 bytes
+// of every row, form one stream over a workgroup's tiles, through a ring of
+// LDS stages loaded straight from memory; results pass through the stage that
+// was used last, to leave in whole lines.
 #include "kernels.h"
 #include "mla_mfma.h"
 
 namespace coli {
 namespace {
 
-constexpr int STAGES = 3;
-
-template <class T_, bool FP8_, int TM_, int TN_, int WM_>
+// NW wavefronts in WM x NW / WM pieces of a tile; WGS workgroups fit a CU.
+template <class T_, bool FP8_, int TM_, int TN_, int NW_, int WM_, int STAGES_, int WGS_>
 struct Gemm {
     using T = T_;
     static constexpr bool FP8 = FP8_;
-    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = 4 / WM_;
+    static constexpr int TM = TM_, TN = TN_, NW = NW_, WM = WM_, WN = NW_ / WM_, STAGES = STAGES_, WGS = WGS_;
     static constexpr int FM = TM / WM / 32, FN = TN / WN / 32;       // 32 x 32 tiles of a wavefront
-    static constexpr int BROW = FP8 ? 32 : 64;                       // bytes of a token's step
-    static constexpr int ASTAGE = TM * 64, STAGE = ASTAGE + TN * BROW;
-    static constexpr int LA = TM / 64;                               // 1 KiB loads a wavefront and step
-    static constexpr int LB_ALL = TN * BROW / 1024, LB = LB_ALL < 4 ? 1 : LB_ALL / 4;
-    static constexpr int OROW = 2 * TM + 16;                         // bytes of a result row in LDS
-    static constexpr int LDS = STAGES * STAGE > TN * OROW ? STAGES * STAGE : TN * OROW;
+    static constexpr int BROW = FP8 ? 64 : 128;                      // bytes of a token's step
+    static constexpr int ASTAGE = TM * 128, STAGE = ASTAGE + TN * BROW;
+    static constexpr int LA = TM / 8 / NW;                           // 1 KiB loads a wavefront and step
+    static constexpr int LB_ALL = TN * BROW / 1024, LB = LB_ALL < NW ? 1 : LB_ALL / NW;
+    static constexpr int OF = FM < 2 ? 1 : 2;                        // 32-feature tiles that leave together
+    static constexpr int OROW = 64 * OF + 16, OUT = NW * 32 * OROW;  // bytes of a token's, of the wavefronts'
+    static constexpr int LDS = STAGES * STAGE;
+    static_assert(OUT <= STAGE && LDS * WGS <= 160 * 1024, "LDS");
 };
 
-// The product of one tile.  wp, xp: this lane's sources of its A and B loads
-// at k = 0; dst: the tile's first feature of each token.
+// Lane's place in a 1 KiB load: eight rows of eight chunks (sixteen of four
+// for codes), swizzled so that sixteen rows' same chunk lies in sixteen groups
+// of banks.
+__device__ __forceinline__ int swz(int r) { return 4 * ((r >> 1) & 1) + 2 * ((r >> 2) & 1) + ((r >> 3) & 1); }
+__device__ __forceinline__ int swz8(int r) { return (r >> 2) & 3; }
+
+// The products of the tiles mt .. mt_end - 1 of TM features.  w: [features]
+// [64 steps]; xp: this lane's sources of its B loads at k = 0; row_of: where a
+// token's features go, or null.
 template <class D, class Row>
-__device__ __forceinline__ void gemm_tile(const uint8_t *const (&wp)[D::LA], const uint8_t *const (&xp)[D::LB], int steps,
-                                          int features, const float (&scale)[D::FN], Row row_of) {
+__device__ __forceinline__ void gemm_tiles(const typename D::T *w, int features, const uint8_t *const (&xp)[D::LB], int steps,
+                                           int mt, int mt_end, const float (&scale)[D::FN], Row row_of) {
     using T = typename D::T;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), n = lane & 31, hf = lane >> 5;
     const int wm = wave % D::WM, wn = wave / D::WM;
-    auto issue = [&](int step) {
-        const uint32_t base = step % STAGES * D::STAGE;
+    // ---- the stream of loads
+    const uint8_t *wp[D::LA];
+    int load_mt = mt, load_k = 0, load_slot = 0;
+    auto aim = [&] {
 #pragma unroll
-        for (int i = 0; i < D::LA; ++i) load_to_lds(wp[i] + step * 64, base + (wave * D::LA + i) * 1024);
+        for (int i = 0; i < D::LA; ++i) {
+            const int r = (wave * D::LA + i) * 8 + (lane >> 3), o = min(load_mt * D::TM + r, features - 1);
+            wp[i] = reinterpret_cast<const uint8_t *>(w + (int64_t)o * (64 * steps)) + (((lane & 7) ^ swz(r)) << 4);
+        }
+    };
+    auto issue = [&] {
+        if (load_mt >= mt_end) return;
+        const uint32_t base = load_slot * D::STAGE;
+#pragma unroll
+        for (int i = 0; i < D::LA; ++i) load_to_lds(wp[i] + load_k * 128, base + (wave * D::LA + i) * 1024);
 #pragma unroll
         for (int i = 0; i < D::LB; ++i)   // fewer loads than wavefronts: some load the same once more
-            load_to_lds(xp[i] + step * D::BROW, base + D::ASTAGE + (wave * D::LB + i) % D::LB_ALL * 1024);
+            load_to_lds(xp[i] + load_k * D::BROW, base + D::ASTAGE + (wave * D::LB + i) % D::LB_ALL * 1024);
+        load_slot = load_slot == D::STAGES - 1 ? 0 : load_slot + 1;
+        if (++load_k == steps) {
+            load_k = 0;
+            ++load_mt;
+            aim();
+        }
     };
-    f32x16 acc[D::FM][D::FN];
+    aim();
 #pragma unroll
-    for (int i = 0; i < D::FM; ++i)
+    for (int i = 0; i < D::STAGES - 1; ++i) issue();
+    // Matrix step e of a stage takes k = 32 (e / 2) + 16 hf + 8 (e % 2) + 0..7 on both sides: 16 bytes of codes then hold
+    // two steps.
+    uint32_t aa[4], ba[4];
 #pragma unroll
-        for (int j = 0; j < D::FN; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-    const int f = (n >> 2) & 3;
-    const uint32_t a_at = (wm * D::FM * 32 + n) * 64, b_at = D::ASTAGE + (wn * D::FN * 32 + n) * D::BROW;
-    // Matrix step e of a stage takes k = 16 hf + 8 e + 0..7 on both sides: 16 bytes of codes then hold both steps.
-    const uint32_t c0 = ((2 * hf) ^ f) << 4, c1 = ((2 * hf + 1) ^ f) << 4, c8 = (hf ^ ((n >> 3) & 1)) << 4;
-    issue(0);
-    if (steps > 1) issue(1);
-    for (int step = 0; step < steps; ++step) {
-        if (step + 1 < steps)
-            wait_vm<D::LA + D::LB>();
-        else
-            wait_vm<0>();
-        barrier_lds();
-        if (step + 2 < steps) issue(step + 2);
-        const uint32_t base = step % STAGES * D::STAGE;
-        x8<T> av[2][D::FM], bv[2][D::FN];
-#pragma unroll
-        for (int j = 0; j < D::FN; ++j) {
-            if (D::FP8) {
-                const u32x4 c = lds_read<u32x4>(base + b_at + j * 32 * D::BROW + c8);
-                bv[0][j] = widen8<T>(u32x2{c[0], c[1]});
-                bv[1][j] = widen8<T>(u32x2{c[2], c[3]});
-            } else {
-                bv[0][j] = lds_read<x8<T>>(base + b_at + j * 32 * D::BROW + c0);
-                bv[1][j] = lds_read<x8<T>>(base + b_at + j * 32 * D::BROW + c1);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < D::FM; ++i) {
-            av[0][i] = lds_read<x8<T>>(base + a_at + i * 2048 + c0);
-            av[1][i] = lds_read<x8<T>>(base + a_at + i * 2048 + c1);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int i = 0; i < D::FM; ++i)
-#pragma unroll
-                for (int j = 0; j < D::FN; ++j) acc[i][j] = mfma32<T>(av[e][i], bv[e][j], acc[i][j]);
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t c = ((4 * (e >> 1) + 2 * hf + (e & 1)) ^ swz(n)) << 4, r = (n >> 3) * 1024 + (n & 7) * 128;
+        aa[e] = wm * D::FM * 4096 + r + c;
+        ba[e] = D::ASTAGE + wn * D::FN * 32 * D::BROW + (D::FP8 ? n * 64 + (((e & 2) + hf) ^ swz8(n)) * 16 : r + c);
     }
-    barrier_lds();
-#pragma unroll
-    for (int j = 0; j < D::FN; ++j)
+    int slot = 0, ready = 0;   // steps whose loads are known to have arrived
+    for (; mt < mt_end; ++mt) {
+        f32x16 acc[D::FM][D::FN];
 #pragma unroll
         for (int i = 0; i < D::FM; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                x4<T> v;
+            for (int j = 0; j < D::FN; ++j)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = (T)(acc[i][j][4 * q + k] * scale[j]);
-                lds_write(((wn * D::FN + j) * 32 + n) * D::OROW + 2 * ((wm * D::FM + i) * 32 + 8 * q + 4 * hf), v);
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+        uint32_t base = 0;
+        for (int k = 0; k < steps; ++k) {
+            if (ready > 0)
+                --ready;
+            else if (D::STAGES > 2 && (mt + 1 < mt_end || k + 1 < steps))
+                wait_vm<(D::STAGES - 2) * (D::LA + D::LB)>();
+            else
+                wait_vm<0>();
+            barrier_lds();
+            issue();
+            base = slot * D::STAGE;
+            slot = slot == D::STAGES - 1 ? 0 : slot + 1;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {   // two matrix steps at a time
+                x8<T> av[2][D::FM], bv[2][D::FN];
+#pragma unroll
+                for (int j = 0; j < D::FN; ++j) {
+                    if (D::FP8) {
+                        const u32x4 c = lds_read<u32x4>(base + ba[2 * h], j * 32 * D::BROW);
+                        bv[0][j] = widen8<T>(u32x2{c[0], c[1]});
+                        bv[1][j] = widen8<T>(u32x2{c[2], c[3]});
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) bv[e][j] = lds_read<x8<T>>(base + ba[2 * h + e], j * 32 * D::BROW);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < D::FM; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) av[e][i] = lds_read<x8<T>>(base + aa[2 * h + e], i * 4096);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int i = 0; i < D::FM; ++i)
+#pragma unroll
+                        for (int j = 0; j < D::FN; ++j) acc[i][j] = mfma32<T>(av[e][i], bv[e][j], acc[i][j]);
             }
-    barrier_lds();
-    constexpr int CH = D::TM / 8;
-#pragma unroll 4
-    for (int i = tid; i < D::TN * CH; i += 256) {
-        const int t = i / CH, c = i % CH;
-        T *dst = row_of(t);
-        if (dst && 8 * c < features) *reinterpret_cast<x8<T> *>(dst + 8 * c) = lds_read<x8<T>>(t * D::OROW + 16 * c);
+        }
+        // The loads that are out, before the stores: a later count of loads must not wait for those.
+        wait_vm<0>();
+        ready = D::STAGES - 1;
+        barrier_lds();
+        const uint32_t at = base + wave * 32 * D::OROW;
+        constexpr int PER = 4 * D::OF;   // lanes a token's run of features
+#pragma unroll
+        for (int j = 0; j < D::FN; ++j)
+#pragma unroll
+            for (int i = 0; i < D::FM; i += D::OF) {
+#pragma unroll
+                for (int q = 0; q < 4 * D::OF; ++q) {
+                    x4<T> v;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = (T)(acc[i + q / 4][j][4 * (q % 4) + k] * scale[j]);
+                    lds_write(at + n * D::OROW + 8 * hf, v, 16 * q);
+                }
+                const int o = mt * D::TM + (wm * D::FM + i) * 32 + 8 * (lane % PER);
+#pragma unroll
+                for (int p = 0; p < PER / 2; ++p) {
+                    const int t = p * (64 / PER) + lane / PER;
+                    const x8<T> v = lds_read<x8<T>>(at + t * D::OROW + 16 * (lane % PER));
+                    T *dst = row_of((wn * D::FN + j) * 32 + t);
+                    if (dst && o < features) *reinterpret_cast<x8<T> *>(dst + o) = v;
+                }
+            }
     }
 }
-
-// Lane's place in a 1 KiB load: 16 rows of four chunks (32 of two for
-// codes), swizzled so that sixteen rows' same chunk lies in sixteen bank groups.
-__device__ __forceinline__ int load_row(int lane) { return lane >> 2; }
-__device__ __forceinline__ int load_chunk(int lane) { return ((lane & 3) ^ ((lane >> 4) & 3)) << 4; }
-__device__ __forceinline__ int load_row8(int lane) { return lane >> 1; }
-__device__ __forceinline__ int load_chunk8(int lane) { return ((lane & 1) ^ ((lane >> 4) & 1)) << 4; }
 
 // Work items to XCDs: workgroups go to the eight XCDs in turn; each XCD takes
 // a contiguous run of items.
@@ -128,40 +168,37 @@ __device__ __forceinline__ int xcd_item(int block, int total) {
 }
 
 template <class D>
-__global__ __launch_bounds__(256, 2) void k_mla_project(MlaProjectArgs a, int m_tiles, int n_tiles) {
+__global__ __launch_bounds__(64 * D::NW, 2) void k_mla_project(MlaProjectArgs a, int m_tiles, int parts, int n_tiles) {
     using T = typename D::T;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int id = xcd_item(blockIdx.x, gridDim.x);
-    const int h = id / (m_tiles * n_tiles), mt = id / n_tiles % m_tiles, nt = id % n_tiles;
-    const int o0 = mt * D::TM, t0 = nt * D::TN;
-    const uint8_t *wp[D::LA], *xp[D::LB];
-#pragma unroll
-    for (int i = 0; i < D::LA; ++i) {
-        const int o = min(o0 + (wave * D::LA + i) * 16 + load_row(lane), a.n_out - 1);
-        wp[i] = reinterpret_cast<const uint8_t *>(static_cast<const T *>(a.w) + ((int64_t)h * a.n_out + o) * a.n_in) + load_chunk(lane);
-    }
+    const int h = id / (parts * n_tiles), part = id / n_tiles % parts, t0 = id % n_tiles * D::TN;
+    const uint8_t *xp[D::LB];
 #pragma unroll
     for (int i = 0; i < D::LB; ++i) {
-        const int64_t t = min(t0 + (wave * D::LB + i) % D::LB_ALL * 16 + load_row(lane), a.tokens - 1);
-        xp[i] = reinterpret_cast<const uint8_t *>(static_cast<const T *>(a.x) + t * a.x_ts + h * a.x_hs) + load_chunk(lane);
+        const int r = (wave * D::LB + i) % D::LB_ALL * 8 + (lane >> 3);
+        const int64_t t = min(t0 + r, a.tokens - 1);
+        xp[i] = reinterpret_cast<const uint8_t *>(static_cast<const T *>(a.x) + t * a.x_ts + h * a.x_hs) +
+                (((lane & 7) ^ swz(r)) << 4);
     }
     float scale[D::FN];
 #pragma unroll
     for (int j = 0; j < D::FN; ++j) scale[j] = 1.0f;
-    gemm_tile<D>(wp, xp, a.n_in / 32, a.n_out - o0, scale, [&](int t) -> T * {
-        return t0 + t < a.tokens ? static_cast<T *>(a.out) + ((int64_t)(t0 + t) * a.heads + h) * a.n_out + o0 : nullptr;
-    });
+    gemm_tiles<D>(static_cast<const T *>(a.w) + (int64_t)h * a.n_out * a.n_in, a.n_out, xp, a.n_in / 64,
+                  part * m_tiles / parts, (part + 1) * m_tiles / parts, scale, [&](int t) -> T * {
+                      return t0 + t < a.tokens ? static_cast<T *>(a.out) + ((int64_t)(t0 + t) * a.heads + h) * a.n_out : nullptr;
+                  });
 }
 
+// A workgroup keeps its tokens and goes through the feature tiles of its part:
+// the rows are looked up once, and the workgroups of an XCD, which mostly have
+// one part, meet at the same weights in its L2.
 template <class D>
-__global__ __launch_bounds__(256, 2) void k_mla_expand(MlaExpandArgs a, int rank, int m_tiles, int n_tiles) {
+__global__ __launch_bounds__(64 * D::NW, 2) void k_mla_expand(MlaExpandArgs a, int rank, int m_tiles, int parts, int n_tiles) {
     using T = typename D::T;
-    constexpr int GROUP = 8;   // feature tiles of a group: their weights stay in an XCD's L2 while the tokens pass
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int id = xcd_item(blockIdx.x, gridDim.x);
-    const int group = id / (GROUP * n_tiles), width = min(GROUP, m_tiles - group * GROUP);
-    const int mt = group * GROUP + (id - group * GROUP * n_tiles) % width, nt = (id - group * GROUP * n_tiles) / width;
-    const int o0 = mt * D::TM, t0 = nt * D::TN;
+    const int part = id / n_tiles, t0 = id % n_tiles * D::TN;
     const int rows = min(a.rows, a.cu_k[a.batch]);
     if (t0 >= rows) return;
     const int row_bytes = D::FP8 ? rank + 2 * MLA_ROPE : 2 * (rank + MLA_ROPE);
@@ -180,48 +217,63 @@ __global__ __launch_bounds__(256, 2) void k_mla_expand(MlaExpandArgs a, int rank
         }
         return mla_slot(a.c, b, at, a.status);
     };
-    const uint8_t *wp[D::LA], *xp[D::LB];
-#pragma unroll
-    for (int i = 0; i < D::LA; ++i) {
-        const int o = min(o0 + (wave * D::LA + i) * 16 + load_row(lane), a.n_out - 1);
-        wp[i] = reinterpret_cast<const uint8_t *>(static_cast<const T *>(a.w) + (int64_t)o * rank) + load_chunk(lane);
-    }
+    const uint8_t *xp[D::LB];
 #pragma unroll
     for (int i = 0; i < D::LB; ++i) {
         const int l = (wave * D::LB + i) % D::LB_ALL;
-        xp[i] = D::FP8 ? a.c.pages + slot_of(l * 32 + load_row8(lane)) * row_bytes + load_chunk8(lane)
-                       : a.c.pages + slot_of(l * 16 + load_row(lane)) * row_bytes + load_chunk(lane);
+        const int r = D::FP8 ? l * 16 + (lane >> 2) : l * 8 + (lane >> 3);
+        xp[i] = a.c.pages + slot_of(r) * row_bytes + ((D::FP8 ? (lane & 3) ^ swz8(r) : (lane & 7) ^ swz(r)) << 4);
     }
     float scale[D::FN];
 #pragma unroll
     for (int j = 0; j < D::FN; ++j)
         scale[j] = D::FP8 ? a.c.scale[slot_of((wave / D::WM * D::FN + j) * 32 + (lane & 31))] : 1.0f;
-    if (mt == 0)   // one tile of features also copies the keys
-        for (int i = tid; i < D::TN * 8; i += 256)
+    if (part == 0)   // one part also copies the keys
+        for (int i = tid; i < D::TN * 8; i += 64 * D::NW)
             if (t0 + i / 8 < rows)
                 *reinterpret_cast<x8<T> *>(static_cast<T *>(a.k_pe) + (int64_t)(t0 + i / 8) * MLA_ROPE + i % 8 * 8) =
                     *reinterpret_cast<const x8<T> *>(a.c.pages + slot_of(i / 8) * row_bytes + row_bytes - 2 * MLA_ROPE + i % 8 * 16);
-    gemm_tile<D>(wp, xp, rank / 32, a.n_out - o0, scale, [&](int t) -> T * {
-        return t0 + t < rows ? static_cast<T *>(a.kv) + (int64_t)(t0 + t) * a.n_out + o0 : nullptr;
-    });
+    gemm_tiles<D>(static_cast<const T *>(a.w), a.n_out, xp, rank / 64, part * m_tiles / parts, (part + 1) * m_tiles / parts, scale,
+                  [&](int t) -> T * { return t0 + t < rows ? static_cast<T *>(a.kv) + (int64_t)(t0 + t) * a.n_out : nullptr; });
+}
+
+// Parts the feature tiles of `items` token tiles are cut into: workgroups
+// enough to fill the 256 CUs once, if there are tiles enough.
+template <class D>
+int gemm_parts(int64_t items, int m_tiles) {
+    const int64_t parts = 256 * D::WGS / items;
+    return (int)(parts < 1 ? 1 : parts < m_tiles ? parts : m_tiles);
 }
 
 template <class D>
 hipError_t project(const MlaProjectArgs &a, hipStream_t st) {
     const int mt = (a.n_out + D::TM - 1) / D::TM, nt = (a.tokens + D::TN - 1) / D::TN;
+    const int parts = gemm_parts<D>((int64_t)nt * a.heads, mt);
     const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_mla_project<D>), D::LDS);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_mla_project<D>, dim3((uint32_t)mt * nt * a.heads), dim3(256), D::LDS, st, a, mt, nt);
+    hipLaunchKernelGGL(k_mla_project<D>, dim3((uint32_t)parts * nt * a.heads), dim3(64 * D::NW), D::LDS, st, a, mt, parts, nt);
     return hipGetLastError();
 }
 
 template <class D>
 hipError_t expand(const MlaExpandArgs &a, int rank, hipStream_t st) {
-    const int mt = (a.n_out + D::TM - 1) / D::TM, nt = (a.rows + D::TN - 1) / D::TN;
+    const int mt = (a.n_out + D::TM - 1) / D::TM, nt = (a.rows + D::TN - 1) / D::TN, parts = gemm_parts<D>(nt, mt);
     const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_mla_expand<D>), D::LDS);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_mla_expand<D>, dim3((uint32_t)mt * nt), dim3(256), D::LDS, st, a, rank, mt, nt);
+    hipLaunchKernelGGL(k_mla_expand<D>, dim3((uint32_t)parts * nt), dim3(64 * D::NW), D::LDS, st, a, rank, mt, parts, nt);
     return hipGetLastError();
+}
+
+template <class T, bool FP8>
+hipError_t expand_by_size(const MlaExpandArgs &a, int rank, hipStream_t st) {
+    if (a.rows <= 32) return expand<Gemm<T, FP8, 128, 32, 4, 4, 3, 2>>(a, rank, st);
+    // rounds of 256 workgroups, in tokens
+    auto rounds = [&](int tn) {
+        const int64_t mt = (a.n_out + 255) / 256, nt = (a.rows + tn - 1) / tn, parts = nt < 256 ? 256 / nt : 1;
+        return (mt + parts - 1) / parts * ((nt * parts + 255) / 256) * tn;
+    };
+    if (rounds(128) < rounds(256)) return expand<Gemm<T, FP8, 256, 128, 8, 4, 3, 1>>(a, rank, st);
+    return expand<Gemm<T, FP8, 256, 256, 8, 2, 2, 1>>(a, rank, st);
 }
 
 }  // namespace
@@ -229,19 +281,16 @@ hipError_t expand(const MlaExpandArgs &a, int rank, hipStream_t st) {
 hipError_t launch_mla_project(const MlaProjectArgs &a, int dtype, hipStream_t st) {
     return mla_with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        if (a.tokens <= 32) return project<Gemm<T, false, 128, 32, 4>>(a, st);
-        if (a.n_out <= 128 || a.tokens <= 512) return project<Gemm<T, false, 128, 128, 2>>(a, st);
-        return project<Gemm<T, false, 256, 128, 2>>(a, st);
+        if (a.tokens <= 32) return project<Gemm<T, false, 128, 32, 4, 4, 3, 2>>(a, st);
+        if (a.n_out <= 128 || a.tokens <= 512) return project<Gemm<T, false, 128, 128, 4, 2, 2, 2>>(a, st);
+        return project<Gemm<T, false, 256, 256, 8, 2, 2, 1>>(a, st);
     });
 }
 
 hipError_t launch_mla_expand(const MlaExpandArgs &a, const coli_mla_dims &d, hipStream_t st) {
     return mla_with_type(d.dtype, [&](auto t) {
         using T = decltype(t);
-        const bool fp8 = d.kv_format == COLI_KV_E4M3;
-        if (a.rows <= 32)
-            return fp8 ? expand<Gemm<T, true, 128, 32, 4>>(a, d.rank, st) : expand<Gemm<T, false, 128, 32, 4>>(a, d.rank, st);
-        return fp8 ? expand<Gemm<T, true, 256, 128, 2>>(a, d.rank, st) : expand<Gemm<T, false, 256, 128, 2>>(a, d.rank, st);
+        return d.kv_format == COLI_KV_E4M3 ? expand_by_size<T, true>(a, d.rank, st) : expand_by_size<T, false>(a, d.rank, st);
     });
 }
 
