@@ -16,10 +16,12 @@ namespace coli {
 namespace {
 
 // NW wavefronts in WM x NW / WM pieces of a tile; WGS workgroups fit a CU.
-template <class T_, bool FP8_, int TM_, int TN_, int NW_, int WM_, int STAGES_, int WGS_>
+// STREAM: results go past the L2, which keeps the operands (8192 rows, 64
+// heads, 470 MB of results: 275 us without, 240 us with).
+template <class T_, bool FP8_, int TM_, int TN_, int NW_, int WM_, int STAGES_, int WGS_, bool STREAM_ = false>
 struct Gemm {
     using T = T_;
-    static constexpr bool FP8 = FP8_;
+    static constexpr bool FP8 = FP8_, STREAM = STREAM_;
     static constexpr int TM = TM_, TN = TN_, NW = NW_, WM = WM_, WN = NW_ / WM_, STAGES = STAGES_, WGS = WGS_;
     static constexpr int FM = TM / WM / 32, FN = TN / WN / 32;       // 32 x 32 tiles of a wavefront
     static constexpr int BROW = FP8 ? 64 : 128;                      // bytes of a token's step
@@ -154,7 +156,12 @@ __device__ __forceinline__ void gemm_tiles(const typename D::T *w, int features,
                     const int t = p * (64 / PER) + lane / PER;
                     const x8<T> v = lds_read<x8<T>>(at + t * D::OROW + 16 * (lane % PER));
                     T *dst = row_of((wn * D::FN + j) * 32 + t);
-                    if (dst && o < features) *reinterpret_cast<x8<T> *>(dst + o) = v;
+                    if (dst && o < features) {
+                        if (D::STREAM)
+                            __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4 *>(dst + o));
+                        else
+                            *reinterpret_cast<x8<T> *>(dst + o) = v;
+                    }
                 }
             }
     }
@@ -190,15 +197,18 @@ __global__ __launch_bounds__(64 * D::NW, 2) void k_mla_project(MlaProjectArgs a,
                   });
 }
 
-// A workgroup keeps its tokens and goes through the feature tiles of its part:
-// the rows are looked up once, and the workgroups of an XCD, which mostly have
-// one part, meet at the same weights in its L2.
+// A workgroup keeps its tokens and goes through the feature tiles of its part,
+// so the rows are looked up once.  An XCD has all parts of few token tiles: its
+// L2 keeps those rows while the weights pass through it once (8192 rows, 64
+// heads: 302 us with one part of all tokens an XCD, whose rows its L2 does not
+// hold).
 template <class D>
 __global__ __launch_bounds__(64 * D::NW, 2) void k_mla_expand(MlaExpandArgs a, int rank, int m_tiles, int parts, int n_tiles) {
     using T = typename D::T;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int id = xcd_item(blockIdx.x, gridDim.x);
-    const int part = id / n_tiles, t0 = id % n_tiles * D::TN;
+    const int across = 4 * parts, run = id / across, wide = min(4, n_tiles - 4 * run);
+    const int part = (id - run * across) / wide, t0 = (4 * run + (id - run * across) % wide) * D::TN;
     const int rows = min(a.rows, a.cu_k[a.batch]);
     if (t0 >= rows) return;
     const int row_bytes = D::FP8 ? rank + 2 * MLA_ROPE : 2 * (rank + MLA_ROPE);
@@ -272,8 +282,8 @@ hipError_t expand_by_size(const MlaExpandArgs &a, int rank, hipStream_t st) {
         const int64_t mt = (a.n_out + 255) / 256, nt = (a.rows + tn - 1) / tn, parts = nt < 256 ? 256 / nt : 1;
         return (mt + parts - 1) / parts * ((nt * parts + 255) / 256) * tn;
     };
-    if (rounds(128) < rounds(256)) return expand<Gemm<T, FP8, 256, 128, 8, 4, 3, 1>>(a, rank, st);
-    return expand<Gemm<T, FP8, 256, 256, 8, 2, 2, 1>>(a, rank, st);
+    if (rounds(128) < rounds(256)) return expand<Gemm<T, FP8, 256, 128, 8, 4, 3, 1, true>>(a, rank, st);
+    return expand<Gemm<T, FP8, 256, 256, 8, 2, 2, 1, true>>(a, rank, st);
 }
 
 }  // namespace
@@ -282,8 +292,8 @@ hipError_t launch_mla_project(const MlaProjectArgs &a, int dtype, hipStream_t st
     return mla_with_type(dtype, [&](auto t) {
         using T = decltype(t);
         if (a.tokens <= 32) return project<Gemm<T, false, 128, 32, 4, 4, 3, 2>>(a, st);
-        if (a.n_out <= 128 || a.tokens <= 512) return project<Gemm<T, false, 128, 128, 4, 2, 2, 2>>(a, st);
-        return project<Gemm<T, false, 256, 256, 8, 2, 2, 1>>(a, st);
+        if (a.n_out <= 128 || a.tokens <= 512) return project<Gemm<T, false, 128, 128, 4, 2, 2, 2, true>>(a, st);
+        return project<Gemm<T, false, 256, 256, 8, 2, 2, 1, true>>(a, st);
     });
 }
 

@@ -72,36 +72,36 @@ def _check(rc, where):
         raise ColiError(rc, where)
 
 
+# The checks below run on every call of kernels that take a few microseconds:
+# one expression that passes, the reasons only where it does not.
 def _arg(t, dtype, shape, what):
-    """Address of a contiguous device tensor of this type and shape (None: any size there)."""
+    """Address of a contiguous device tensor of this type and shape."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, dtype, shape, what)
+    raise ValueError(f"{what}: must be contiguous")
+
+
+def _refuse(t, dtype, shape, what):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what}: expected a torch tensor")
     if t.dtype != dtype:
         raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{what}: must be a device tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: must be contiguous")
-    return t.data_ptr()
 
 
 def _strided(t, dtype, shape, what):
     """Address and the first two strides of a device tensor [tokens, heads, width] whose last dimension is dense."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what}: expected a torch tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
-    if t.dim() != 3 or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: must be a device tensor")
-    s = t.stride()
-    if s[2] != 1:
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda):
+        _refuse(t, dtype, shape, what)
+    a, b, c = t.stride()
+    if c != 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
     # the stride of a dimension of one element is never used
-    return t.data_ptr(), s[0] if t.shape[0] > 1 else 0, s[1] if t.shape[1] > 1 else 0
+    return t.data_ptr(), a if shape[0] > 1 else 0, b if shape[1] > 1 else 0
 
 
 def _distinct(t, strides, what):
@@ -114,21 +114,35 @@ def _distinct(t, strides, what):
 
 
 def _ws(ws):
-    return _arg(ws, torch.uint8, (None,), "ws"), ws.numel()
+    n = ws.numel()
+    return _arg(ws, torch.uint8, (n,), "ws"), n
 
 
-def _stream(stream, device):
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream(stream, t):
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(t.get_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _columns(t, what):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{what}: expected a tensor of two dimensions")
+    return t.shape[1]
+
+
 def _pages(d, pages, kv_scale):
-    row = d.rank + (2 * COLI_MLA_ROPE if d.kv_format == COLI_KV_E4M3 else COLI_MLA_ROPE)
-    at = _arg(pages, torch.uint8 if d.kv_format == COLI_KV_E4M3 else _OF[d.dtype], (None, d.page_size, row), "pages")
+    if d.kv_format == COLI_KV_E4M3:
+        dtype, row = torch.uint8, d.rank + 2 * COLI_MLA_ROPE
+    else:
+        dtype, row = _OF[d.dtype], d.rank + COLI_MLA_ROPE
+    n, page = pages.shape[0], d.page_size
+    at = _arg(pages, dtype, (n, page, row), "pages")
     if kv_scale is not None:
-        kv_scale = _arg(kv_scale, torch.float32, (pages.shape[0] * d.page_size,), "kv_scale")
-    return at, kv_scale, pages.shape[0]
+        kv_scale = _arg(kv_scale, torch.float32, (n * page,), "kv_scale")
+    return at, kv_scale, n
 
 
 # ---------------------------------------------------------------- entry points
@@ -161,7 +175,7 @@ def coli_mla_append(dims, kv_a, norm_w, positions, slots, inv_freq, q_pe, q_pe_o
         None if norm_w is None else _arg(norm_w, dt, (d.rank,), "norm_w"),
         _arg(positions, torch.int32, (n,), "positions"), _arg(slots, torch.int64, (n,), "slots"),
         _arg(inv_freq, torch.float64, (COLI_MLA_ROPE // 2,), "inv_freq"), *q, *o, at, scale, n_pages, *_ws(ws),
-        _stream(stream, kv_a.device)), "coli_mla_append")
+        _stream(stream, kv_a)), "coli_mla_append")
 
 
 def coli_mla_project(x, w, out, stream=None):
@@ -174,7 +188,7 @@ def coli_mla_project(x, w, out, stream=None):
     _check(_lib.coli_mla_project(
         _TYPES[x.dtype], n, heads, n_in, n_out, *_strided(x, x.dtype, (n, heads, n_in), "x"),
         _arg(w, x.dtype, (heads, n_out, n_in), "w"), _arg(out, x.dtype, (n, heads, n_out), "out"),
-        _stream(stream, x.device)), "coli_mla_project")
+        _stream(stream, x)), "coli_mla_project")
 
 
 def coli_mla_decode(dims, q_lat, q_pe, pages, kv_scale, table, kv_lens, max_kv, out, lse, ws, stream=None):
@@ -183,24 +197,26 @@ def coli_mla_decode(dims, q_lat, q_pe, pages, kv_scale, table, kv_lens, max_kv, 
     if batch and (rows % batch or not rows):
         raise ValueError(f"q_lat: {rows} rows for {batch} sequences")
     at, scale, n_pages = _pages(d, pages, kv_scale)
+    width = _columns(table, "table")
     _check(_lib.coli_mla_decode(
         ctypes.byref(d), batch, rows // batch if batch else 1, _arg(q_lat, dt, (rows, d.n_heads, d.rank), "q_lat"),
         _arg(q_pe, dt, (rows, d.n_heads, COLI_MLA_ROPE), "q_pe"), at, scale, n_pages,
-        _arg(table, torch.int32, (batch, None), "table"), table.shape[1], _arg(kv_lens, torch.int32, (batch,), "kv_lens"),
+        _arg(table, torch.int32, (batch, width), "table"), width, _arg(kv_lens, torch.int32, (batch,), "kv_lens"),
         max_kv, _arg(out, dt, (rows, d.n_heads, d.rank), "out"),
         None if lse is None else _arg(lse, torch.float32, (rows, d.n_heads), "lse"), *_ws(ws),
-        _stream(stream, q_lat.device)), "coli_mla_decode")
+        _stream(stream, q_lat)), "coli_mla_decode")
 
 
 def coli_mla_expand(dims, pages, kv_scale, table, cu_k, w, kv, k_pe, ws, stream=None):
     d, dt, n, wide = dims, _OF[dims.dtype], kv.shape[0], dims.nope + dims.v_dim
     batch = cu_k.shape[0] - 1
     at, scale, n_pages = _pages(d, pages, kv_scale)
+    width = _columns(table, "table")
     _check(_lib.coli_mla_expand(
-        ctypes.byref(d), batch, n, at, scale, n_pages, _arg(table, torch.int32, (batch, None), "table"),
-        table.shape[1], _arg(cu_k, torch.int32, (batch + 1,), "cu_k"), _arg(w, dt, (d.n_heads, wide, d.rank), "w"),
+        ctypes.byref(d), batch, n, at, scale, n_pages, _arg(table, torch.int32, (batch, width), "table"),
+        width, _arg(cu_k, torch.int32, (batch + 1,), "cu_k"), _arg(w, dt, (d.n_heads, wide, d.rank), "w"),
         _arg(kv, dt, (n, d.n_heads, wide), "kv"), _arg(k_pe, dt, (n, COLI_MLA_ROPE), "k_pe"), *_ws(ws),
-        _stream(stream, kv.device)), "coli_mla_expand")
+        _stream(stream, kv)), "coli_mla_expand")
 
 
 def coli_mla_prefill(dims, q, k_nope, k_pe, v, cu_q, cu_k, max_q, causal, out, lse, ws, stream=None):
@@ -215,4 +231,4 @@ def coli_mla_prefill(dims, q, k_nope, k_pe, v, cu_q, cu_k, max_q, causal, out, l
         _arg(cu_k, torch.int32, (batch + 1,), "cu_k"), max_q, int(bool(causal)),
         _arg(out, dt, (n, d.n_heads, d.v_dim), "out"),
         None if lse is None else _arg(lse, torch.float32, (n, d.n_heads), "lse"), *_ws(ws),
-        _stream(stream, q.device)), "coli_mla_prefill")
+        _stream(stream, q)), "coli_mla_prefill")
