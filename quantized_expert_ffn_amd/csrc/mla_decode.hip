@@ -18,6 +18,8 @@ constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 // of two: weights then reach 2^8, which every type here holds, and most tiles
 // spare the pass over the accumulators.
 constexpr float MAX_LAG = 8.0f;
+// As little does the unit of E4M3 scales move: weights times scales reach 2^12.
+constexpr float UNIT_LAG = 16.0f;
 
 // Four wavefronts: RG groups of 32 rows, each of CG = 4 / RG wavefronts that
 // share the output's columns.  Wavefronts 0 and 1 of a group score half of a
@@ -180,10 +182,23 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
     const uint8_t *src0 = a.c.pages + (((lane & 7) ^ dec_swz<FP8>(lt0)) << 4);
     const uint8_t *src1 = a.c.pages + (((lane & 7) ^ dec_swz<FP8>(lt1)) << 4);
     auto source = [&](int it, int t) { return lds_read<int64_t>(D::L_OFF + 8 * ((it & 1) * DEC_TILE + t)); };
+    auto lds_line = [](int c, const uint8_t *p, uint32_t d) {   // line c of a row, its block c
+        switch (c) {
+        case 0: load_to_lds<0>(p, d); break;
+        case 1: load_to_lds<128>(p, d, 1024); break;
+        case 2: load_to_lds<256>(p, d, 2048); break;
+        case 3: load_to_lds<384>(p, d, 3 * 1024); break;
+        case 4: load_to_lds<512>(p, d, 4 * 1024); break;
+        case 5: load_to_lds<640>(p, d, 5 * 1024); break;
+        case 6: load_to_lds<768>(p, d, 6 * 1024); break;
+        case 7: load_to_lds<896>(p, d, 7 * 1024); break;
+        default: load_to_lds<1024>(p, d, 8 * 1024); break;
+        }
+    };
     auto issue = [&](int it, int c, const uint8_t *p0, const uint8_t *p1) {
         const uint32_t d = (it & 1) * D::TILE + 2 * wave * D::CB * 1024;
-        load_to_lds(p0 + 128 * c, d + 1024 * c);
-        load_to_lds(p1 + 128 * c, d + (D::CB + c) * 1024);
+        lds_line(c, p0, d);
+        lds_line(c, p1, d + D::CB * 1024);
     };
     // A sequence's queries: whole rows into LDS, as a tile's, then every wavefront's operands out of it.
     x8<T> qf[KS];
@@ -381,19 +396,19 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                             sc[r] = 0.0f;
                         }
                 }
-                float top = s[0];
+                float top = fmaxf(fmaxf(s[0], s[1]), s[2]);
 #pragma unroll
-                for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
-                top = half_max(top) * scale;
+                for (int r = 3; r < 15; r += 2) top = fmaxf(fmaxf(top, s[r]), s[r + 1]);
+                top = half_max(fmaxf(top, s[15])) * scale;
                 lds_write<float>(top_at + 128 * th, top);
                 bool grows = top > m + MAX_LAG;
-                if (FP8) grows |= lds_read<float>(D::L_UNIT + 4 * buf) > unit;
+                if (FP8) grows |= lds_read<float>(D::L_UNIT + 4 * buf) > UNIT_LAG * unit;
                 if (__ballot(grows) && lane == 0) lds_write<int>(D::L_GROW, it + 1);
             } else if (more) {
 #pragma unroll
                 for (int c = 0; c < D::CB; ++c) issue(it + 1, c, p0, p1);
             }
-            if (scores) weigh();
+            if (scores && tile > lo) weigh();   // a segment's first maximum moves: its weights come below
             // A tile that some rows see only in part, though its tokens exist: values that are not finite would reach
             // rows that do not see them as 0 * NaN; a row that does see them has them in its scores already.
             if (block_seen < len && t0 + DEC_TILE > block_seen) {
@@ -425,7 +440,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
             x8<T> p[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) p[k] = lds_read<x8<T>>(p_at - 2048 * th, 1024 * k);
-            if (uniform(grow) == it + 1) {
+            if (tile == lo || uniform(grow) == it + 1) {
                 barrier_lds();   // read by all
                 if (works) {
                     const float top = fmaxf(lds_read<float>(top_at), lds_read<float>(top_at, 128));

@@ -139,16 +139,18 @@ __device__ __forceinline__ int div_by(int t, int d, uint32_t inv) {
     return t - q * d >= d ? q + 1 : q;
 }
 
-// 16 bytes of each lane straight into LDS: lane l's land at lds + 16 l (lds
-// uniform over the wavefront).  Done when the wavefront's vmcnt says so.
-// Written in assembly because the compiler otherwise waits for every such
-// load before the next LDS read of any buffer; no register is an output.  The
-// wait state is the one between a write of m0 and a load that reads it; OFF
-// moves both addresses.
+// 16 bytes of each lane straight into LDS: from src + OFF, lane l's to lds +
+// lds_off + 16 l (lds uniform over the wavefront).  Done when the wavefront's
+// vmcnt says so.  Written in assembly because the compiler otherwise waits for
+// every such load before the next LDS read of any buffer; no register is an
+// output.  The instruction's offset counts on both sides, hence the
+// subtraction; the wait state is the one between a write of m0 and a load that
+// reads it.
 template <int OFF = 0>
-__device__ __forceinline__ void load_to_lds(const void *src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off offset:%2" ::"v"(src), "s"(__builtin_amdgcn_readfirstlane((int)lds)), "n"(OFF)
-                 : "memory");
+__device__ __forceinline__ void load_to_lds(const void *src, uint32_t lds, int lds_off = 0) {
+    asm volatile("s_add_u32 m0, %1, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off offset:%3" ::"v"(src),
+                 "s"(__builtin_amdgcn_readfirstlane((int)lds)), "i"(lds_off - OFF), "n"(OFF)
+                 : "memory", "scc");
 }
 
 // A value that is the same in every lane, as a scalar.
