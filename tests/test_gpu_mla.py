@@ -181,7 +181,7 @@ def test_append_keeps_a_nan_visible():
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("n,heads,n_in,n_out", [
     (1, 1, 64, 64), (1, 5, 192, 512), (3, 64, 512, 128), (5, 16, 128, 256), (16, 7, 192, 512), (17, 5, 512, 256),
-    (33, 3, 128, 512), (64, 2, 256, 128), (133, 9, 512, 128), (300, 5, 192, 512), (257, 1, 1024, 320), (129, 2, 64, 4096)])
+    (33, 3, 128, 512), (64, 2, 256, 128), (600, 2, 192, 512), (513, 3, 64, 192), (133, 9, 512, 128), (300, 5, 192, 512), (257, 1, 1024, 320), (129, 2, 64, 4096)])
 def test_project(dtype, n, heads, n_in, n_out):
     say("project", dtype, n, heads, n_in, n_out)
     g = gen(n * heads)
@@ -242,6 +242,16 @@ def test_decode_many_splits(fp8, heads, n_q):
     lens = [20011, 1, 0, 640, 64, 63, 9000, 129]
     say("decode splits", fp8, heads, n_q)
     run_decode(gen(3), lens, n_q, heads, 512, BF, fp8, 64)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("batch,n_q,heads,top", [(100, 1, 3, 200), (62, 33, 256, 40), (300, 2, 20, 70)])
+def test_decode_many_sequences(fp8, batch, n_q, heads, top):
+    """More sequences than a wavefront has lanes, and so many rows that one workgroup goes through all sequences."""
+    say("decode many", fp8, batch, n_q, heads)
+    g = torch.Generator().manual_seed(batch)
+    lens = [int(v) for v in torch.randint(0, top + 1, (batch,), generator=g)]
+    run_decode(gen(batch), lens, n_q, heads, 256, BF, fp8, 16)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -364,7 +374,7 @@ def test_decode_reports_bad_pages_and_lengths(fp8):
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("rank,fp8", [(512, False), (512, True), (256, False), (256, True)])
 @pytest.mark.parametrize("lens,heads,page,nope", [([1], 1, 1, 128), ([0, 3, 0, 70, 1], 5, 16, 192), ([333, 1, 0, 700], 3, 48, 192),
-                                                  ([130], 32, 64, 128), ([257, 255], 1, 128, 192)])
+                                                  ([130], 32, 64, 128), ([257, 255], 1, 128, 192), ([2000, 48], 16, 64, 192)])
 def test_expand(dtype, rank, fp8, lens, heads, page, nope):
     say("expand", dtype, rank, fp8, lens, heads, page, nope)
     g = gen(sum(lens) + heads)
@@ -385,6 +395,35 @@ def test_expand(dtype, rank, fp8, lens, heads, page, nope):
     ref.close(kv[:n], want, 1.01 * ref.U[dtype] * want.abs() + (rank + 4) * ref.U32 * mag + ref.TINY[dtype], "kv")
     assert torch.equal(k_pe[:n].double(), key[at])
     assert (kv[n:] == 7).all() and (k_pe[n:] == 7).all(), "written behind the last row"
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_expand_and_prefill_of_many_sequences(fp8):
+    """A hundred sequences, every third of them empty."""
+    say("expand many", fp8)
+    g = gen(6)
+    lens = [0 if i % 3 == 1 else 1 + 7 * i % 23 for i in range(100)]
+    heads, rank, page, n = 3, 256, 16, sum(lens)
+    pages, scale, table = cache(g, lens, rank, BF, fp8, page)
+    d = dims(heads, rank, BF, fp8, page)
+    w = (randn(g, heads, 256, rank) / 16).to(BF)
+    kv, k_pe = torch.full((n, heads, 256), NAN, dtype=BF, device="cuda"), torch.full((n, 64), NAN, dtype=BF, device="cuda")
+    ws, cu = workspace(d), ref.cumulative(lens, "cuda")
+    q().coli_mla_expand(d, pages, scale, table, cu, w, kv, k_pe, ws)
+    lat, key = ref.rows_of(pages, scale, rank, BF)
+    at = torch.cat([ref.slots_of(table, b, m, page) for b, m in enumerate(lens)])
+    wf = w.double().flatten(0, 1).t()
+    want, mag = (lat[at] @ wf).view(n, heads, -1), (lat[at].abs() @ wf.abs()).view(n, heads, -1)
+    ref.close(kv, want, 1.01 * ref.U[BF] * want.abs() + (rank + 4) * ref.U32 * mag, "kv")
+    assert torch.equal(k_pe.double(), key[at])
+    qq = randn(g, n, heads, 192, dtype=BF)
+    out, lse = torch.full((n, heads, 128), NAN, dtype=BF, device="cuda"), torch.full((n, heads), NAN, device="cuda")
+    q().coli_mla_prefill(d, qq, kv[..., :128], k_pe, kv[..., 128:], cu, cu, max(lens), True, out, lse, ws)
+    ok(ws)
+    want, wl, mag, smag = ref.prefill(qq, kv[..., :128], k_pe, kv[..., 128:], lens, lens, True, d.softmax_scale)
+    tol, tl = ref.attend_tol(want, mag, smag, 192, max(lens), BF)
+    ref.close(out, want, tol, "out")
+    ref.close(lse, wl, tl, "lse")
 
 
 def test_expand_reports_bad_pages_and_offsets():
@@ -434,7 +473,8 @@ def run_prefill(g, q_lens, k_lens, heads, nope, dtype, causal, spread=1.0, poiso
 
 PREFILL = [  # q_lens, k_lens, heads
     ([1], [1], 1), ([2, 0, 5], [2, 0, 5], 5), ([1, 77, 300], [1, 200, 300], 3), ([64, 65, 63], [64, 65, 63], 2),
-    ([33], [1000], 5), ([130, 5], [129, 0], 3), ([513, 1, 128], [513, 700, 131], 1), ([700], [64], 2)]
+    ([33], [1000], 5), ([130, 5], [129, 0], 3), ([513, 1, 128], [513, 700, 131], 1), ([700], [64], 2),
+    ([300, 77], [300, 200], 128)]
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
@@ -453,29 +493,29 @@ def test_prefill_strides_and_peaked_scores(nope):
     run_prefill(gen(2), [700], [900], 2, nope, FP, True, spread=12.0)
 
 
-@pytest.mark.parametrize("nope", [128, 192])
-def test_prefill_masked_keys_may_hold_anything(nope):
+@pytest.mark.parametrize("nope,heads", [(128, 2), (192, 2), (128, 256), (192, 256)])
+def test_prefill_masked_keys_may_hold_anything(nope, heads):
     """Keys and values that a query does not see are NaN or infinite: inside its own tile and behind it."""
     n = 200
     for value in (NAN, float("inf"), -float("inf")):
         for at in (199, 130, 70):
-            say("prefill poisoned", nope, value, at)
+            say("prefill poisoned", nope, heads, value, at)
 
             def poison(k_nope, k_pe, v):
                 k_nope[at] = value
                 v[at] = value
-            out, lse = run_prefill(gen(at), [n], [n], 2, nope, BF, True, poison=poison)
+            out, lse = run_prefill(gen(at), [n], [n], heads, nope, BF, True, poison=poison)
             assert out[:at].isfinite().all() and lse[:at].isfinite().all()
 
 
-@pytest.mark.parametrize("nope", [128, 192])
-def test_prefill_keeps_a_seen_nan_visible(nope):
+@pytest.mark.parametrize("nope,heads", [(128, 2), (192, 2), (128, 256), (192, 256)])
+def test_prefill_keeps_a_seen_nan_visible(nope, heads):
     """A value that is not finite reaches exactly the queries that see it, and its own column only."""
     def poison(k_nope, k_pe, v):
         v[70, 0, 5] = NAN
         v[90, 1, 7] = float("inf")
     say("prefill seen nan", nope)
-    out, _ = run_prefill(gen(5), [200], [200], 2, nope, FP, True, poison=poison)
+    out, _ = run_prefill(gen(5), [200], [200], heads, nope, FP, True, poison=poison)
     assert out[70:, 0, 5].isnan().all() and out[90:, 1, 7].isinf().all()
 
 
