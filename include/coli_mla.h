@@ -73,6 +73,8 @@ typedef struct coli_mla_dims {
 #define COLI_MLA_MAX_ROWS 16384
 #define COLI_MLA_MAX_BATCH 4096
 #define COLI_MLA_MAX_TOKENS (1ll << 36)
+/* Largest token stride of prefill's keys and values, in elements. */
+#define COLI_MLA_MAX_STRIDE (1 << 23)
 
 /* Bytes of one cached token (0 when dims are invalid). */
 size_t coli_mla_row_bytes(const coli_mla_dims *dims);

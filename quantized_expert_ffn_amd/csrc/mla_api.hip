@@ -155,6 +155,8 @@ int coli_mla_project(int32_t dtype, int32_t n_tokens, int32_t n_heads, int32_t n
         return fail(COLI_EINVAL, "n_in=%d: must be a multiple of 64 in 64..1024", n_in);
     if (n_out < 64 || n_out > 4096 || n_out % 64)
         return fail(COLI_EINVAL, "n_out=%d: must be a multiple of 64 in 64..4096", n_out);
+    if ((int64_t)n_heads * n_tokens >= (int64_t)1 << 30)
+        return fail(COLI_EINVAL, "n_tokens=%d: too many for %d heads", n_tokens, n_heads);
     if (n_tokens == 0) return COLI_OK;
     if (!x || !w || !out) return fail(COLI_EINVAL, "coli_mla_project: NULL pointer argument");
     if (!aligned16(x) || !aligned16(w) || !aligned16(out))
@@ -259,6 +261,10 @@ int coli_mla_prefill(const coli_mla_dims *d, int32_t batch, int32_t n_q_rows, in
     if (bad_stride(q_token_stride) || bad_stride(q_head_stride) || bad_stride(k_token_stride) ||
         bad_stride(k_head_stride) || bad_stride(v_token_stride) || bad_stride(v_head_stride))
         return fail(COLI_EINVAL, "coli_mla_prefill: strides must be non-negative multiples of 8");
+    if (k_token_stride > COLI_MLA_MAX_STRIDE || v_token_stride > COLI_MLA_MAX_STRIDE)
+        return fail(COLI_EINVAL, "coli_mla_prefill: token strides of k_nope and v must be at most %d", COLI_MLA_MAX_STRIDE);
+    if ((int64_t)batch * d->n_heads * ((max_q + 127) / 128) >= (int64_t)1 << 28)
+        return fail(COLI_EINVAL, "coli_mla_prefill: batch=%d, max_q=%d: too many blocks of queries", batch, max_q);
     if ((rc = check_ws(ws, ws_bytes, WS_HEAD, "coli_mla_prefill"))) return rc;
     if ((rc = api_check_device())) return rc;
     MlaPrefillArgs a{};

@@ -212,37 +212,46 @@ __global__ __launch_bounds__(64 * D::NW, 2) void k_mla_expand(MlaExpandArgs a, i
     const int rows = min(a.rows, a.cu_k[a.batch]);
     if (t0 >= rows) return;
     const int row_bytes = D::FP8 ? rank + 2 * MLA_ROPE : 2 * (rank + MLA_ROPE);
-    // the sequence of the tile's first row: how many end at or before it
-    int first = 0;
-    for (int b = 0; b < a.batch; b += 64)
-        first += __popcll(__ballot(b + lane < a.batch && a.cu_k[min(b + lane, a.batch - 1) + 1] <= t0));
-    auto slot_of = [&](int t) -> int64_t {
-        const int r = min(t0 + t, rows - 1);
-        int b = min(first, a.batch - 1);
-        while (b + 1 < a.batch && a.cu_k[b + 1] <= r) ++b;
-        const int at = r - a.cu_k[b];
-        if (at < 0 || at >= (int64_t)a.c.width * a.c.page) {
-            raise_status(a.status, ST_BADPAGE);
-            return 0;
+    // Where the tile's rows are, a thread a row, in the stage that is loaded last: int64 row offsets, then scales.
+    constexpr uint32_t AT = (D::STAGES - 1) * D::STAGE, SCALES = AT + 8 * D::TN;
+    {
+        // the sequence of the tile's first row: how many end at or before it
+        int first = 0;
+        for (int b = 0; b < a.batch; b += 64)
+            first += __popcll(__ballot(b + lane < a.batch && a.cu_k[min(b + lane, a.batch - 1) + 1] <= t0));
+        for (int t = tid; t < D::TN; t += 64 * D::NW) {
+            const int r = min(t0 + t, rows - 1);
+            int b = min(first, a.batch - 1);
+            while (b + 1 < a.batch && a.cu_k[b + 1] <= r) ++b;
+            const int at = r - a.cu_k[b];
+            int64_t slot = 0;
+            if (at < 0 || at >= (int64_t)a.c.width * a.c.page)
+                raise_status(a.status, ST_BADPAGE);
+            else
+                slot = mla_slot(a.c, b, at, a.status);
+            lds_write<int64_t>(AT + 8 * t, slot * row_bytes);
+            if (D::FP8) lds_write<float>(SCALES + 4 * t, a.c.scale[slot]);
         }
-        return mla_slot(a.c, b, at, a.status);
-    };
+        __syncthreads();
+    }
     const uint8_t *xp[D::LB];
 #pragma unroll
     for (int i = 0; i < D::LB; ++i) {
         const int l = (wave * D::LB + i) % D::LB_ALL;
         const int r = D::FP8 ? l * 16 + (lane >> 2) : l * 8 + (lane >> 3);
-        xp[i] = a.c.pages + slot_of(r) * row_bytes + ((D::FP8 ? (lane & 3) ^ swz8(r) : (lane & 7) ^ swz(r)) << 4);
+        xp[i] = a.c.pages + lds_read<int64_t>(AT + 8 * r) + ((D::FP8 ? (lane & 3) ^ swz8(r) : (lane & 7) ^ swz(r)) << 4);
     }
     float scale[D::FN];
 #pragma unroll
     for (int j = 0; j < D::FN; ++j)
-        scale[j] = D::FP8 ? a.c.scale[slot_of((wave / D::WM * D::FN + j) * 32 + (lane & 31))] : 1.0f;
+        scale[j] = D::FP8 ? lds_read<float>(SCALES + 4 * ((wave / D::WM * D::FN + j) * 32 + (lane & 31))) : 1.0f;
     if (part == 0)   // one part also copies the keys
         for (int i = tid; i < D::TN * 8; i += 64 * D::NW)
             if (t0 + i / 8 < rows)
                 *reinterpret_cast<x8<T> *>(static_cast<T *>(a.k_pe) + (int64_t)(t0 + i / 8) * MLA_ROPE + i % 8 * 8) =
-                    *reinterpret_cast<const x8<T> *>(a.c.pages + slot_of(i / 8) * row_bytes + row_bytes - 2 * MLA_ROPE + i % 8 * 16);
+                    *reinterpret_cast<const x8<T> *>(a.c.pages + lds_read<int64_t>(AT + 8 * (i / 8)) + row_bytes - 2 * MLA_ROPE +
+                                                     i % 8 * 16);
+    barrier_lds();   // the offsets are read: the stage is free
     gemm_tiles<D>(static_cast<const T *>(a.w), a.n_out, xp, rank / 64, part * m_tiles / parts, (part + 1) * m_tiles / parts, scale,
                   [&](int t) -> T * { return t0 + t < rows ? static_cast<T *>(a.kv) + (int64_t)(t0 + t) * a.n_out : nullptr; });
 }

@@ -33,7 +33,7 @@ struct Pre {
     static constexpr int JOIN = KG == 2 ? L_ML + NW * 32 * 8 : 0;
     static constexpr int STAGES = 3 * TILE <= 160 * 1024 ? 3 : 2;   // tiles in LDS: loads run one or two ahead
     static constexpr int LDS = STAGES * TILE > JOIN ? STAGES * TILE : JOIN;
-    static constexpr int LOADS = KT / 8 / NW * (KB + VB);            // of a wavefront, for a tile
+    static constexpr int LOADS = KB + VB;                            // of a wavefront, for a tile
 };
 
 // As in the decode kernel: LDS holds a tile as [8 tokens][8 chunks] blocks of
@@ -96,26 +96,47 @@ __global__ __launch_bounds__(64 * D::NW, 2) void k_mla_prefill(MlaPrefillArgs a,
         }
     }
 
-    // ---- loads: chunk lane % 8 of tokens 8 g + lane / 8, groups g = wave, wave + NW, ..
+    // ---- loads: a wavefront takes chunk lane % 8 of tokens 8 wave + lane / 8 of a tile, keys and values apart
+    static_assert(D::KT == 8 * D::NW, "one group of eight tokens a wavefront");
     const char *kn = reinterpret_cast<const char *>(static_cast<const T *>(a.k_nope) + k0 * a.k_ts + h * a.k_hs);
     const char *kp = reinterpret_cast<const char *>(static_cast<const T *>(a.k_pe) + (int64_t)k0 * MLA_ROPE);
     const char *vv = reinterpret_cast<const char *>(static_cast<const T *>(a.v) + k0 * a.v_ts + h * a.v_hs);
-    auto issue = [&](int tile) {
-        const uint32_t base = tile % D::STAGES * D::TILE;
-#pragma unroll
-        for (int i = 0; i < D::KT / 8 / D::NW; ++i) {
-            const int g = wave + i * D::NW, t8 = 8 * g + (lane >> 3);
-            const int64_t t = min(tile * D::KT + t8, nk - 1);   // behind the end: the last again
-            const int chunk = ((lane & 7) ^ pre_swz(t8)) << 4;
-            const char *pn = kn + t * (2 * a.k_ts) + chunk, *pv = vv + t * (2 * a.v_ts) + chunk;
-            const char *pp = kp + t * (2 * MLA_ROPE) + chunk;
-            const uint32_t dk = base + g * D::KB * 1024, dv = base + D::KTILE + g * D::VB * 1024;
-#pragma unroll
-            for (int c = 0; c < D::KB - 1; ++c) load_to_lds(pn + 128 * c, dk + 1024 * c);
-            load_to_lds(pp, dk + 1024 * (D::KB - 1));
-#pragma unroll
-            for (int c = 0; c < D::VB; ++c) load_to_lds(pv + 128 * c, dv + 1024 * c);
+    const int my_token = 8 * wave + (lane >> 3);
+    const uint32_t my_chunk = ((lane & 7) ^ pre_swz(my_token)) << 4;
+    const uint32_t k_step = 2 * (uint32_t)a.k_ts, v_step = 2 * (uint32_t)a.v_ts;
+    uint32_t k_off = my_token * k_step + my_chunk, p_off = my_token * (2 * MLA_ROPE) + my_chunk, v_off = my_token * v_step + my_chunk;
+    // Tiles come in order, so the last, where tokens behind the end are the last token again, can change the offsets.
+    auto clamp = [&](int tile) {
+        const int end = nk - tile * D::KT;
+        if (end < D::KT) {
+            const int t = min(my_token, end - 1);
+            k_off = t * k_step + my_chunk;
+            p_off = t * (2 * MLA_ROPE) + my_chunk;
+            v_off = t * v_step + my_chunk;
         }
+    };
+    auto issue_k = [&](int tile) {
+        clamp(tile);
+        const uint32_t d = tile % D::STAGES * D::TILE + wave * D::KB * 1024;
+        const char *n0 = kn + (int64_t)tile * D::KT * (2 * a.k_ts), *p0 = kp + (int64_t)tile * (D::KT * 2 * MLA_ROPE);
+        load_to_lds_from<0>(n0, k_off, d, 0);
+        load_to_lds_from<128>(n0, k_off, d, 1024);
+        if (D::KB == 4) load_to_lds_from<256>(n0, k_off, d, 2048);
+        load_to_lds_from<0>(p0, p_off, d, (D::KB - 1) * 1024);
+    };
+    auto issue_v = [&](int tile) {
+        const uint32_t d = tile % D::STAGES * D::TILE + D::KTILE + wave * D::VB * 1024;
+        const char *v0 = vv + (int64_t)tile * D::KT * (2 * a.v_ts);
+        load_to_lds_from<0>(v0, v_off, d, 0);
+        load_to_lds_from<128>(v0, v_off, d, 1024);
+        if (D::VB == 4) {
+            load_to_lds_from<256>(v0, v_off, d, 2048);
+            load_to_lds_from<384>(v0, v_off, d, 3 * 1024);
+        }
+    };
+    auto issue = [&](int tile) {
+        issue_k(tile);
+        issue_v(tile);
     };
     if (tiles > 0) issue(0);
     if (D::STAGES == 3 && tiles > 1) issue(1);
@@ -145,7 +166,16 @@ __global__ __launch_bounds__(64 * D::NW, 2) void k_mla_prefill(MlaPrefillArgs a,
         else
             wait_vm<0>();
         barrier_lds();   // the tile is there, and every wavefront is done with the one before
-        if (tile + D::STAGES - 1 < tiles) issue(tile + D::STAGES - 1);
+        // With two stages the values' loads follow the first scores: a burst of all of them would hold up the products.
+        const int coming = tile + D::STAGES - 1;
+        bool v_due = coming < tiles;
+        if (v_due) {
+            issue_k(coming);
+            if (D::STAGES == 3) {
+                issue_v(coming);
+                v_due = false;
+            }
+        }
         if (block_seen < nk && t0 + D::KT > block_seen) {
             // A tile that some queries see only in part: values that are not finite would reach those that do not see
             // them as 0 * NaN.  They are set aside, and added at the end where they are seen.
@@ -220,6 +250,10 @@ __global__ __launch_bounds__(64 * D::NW, 2) void k_mla_prefill(MlaPrefillArgs a,
                 p[r >> 3][r & 7] = (T)w;
             }
             l += sum;
+            if (v_due) {
+                issue_v(coming);
+                v_due = false;
+            }
             u32x4 av[2][2];   // a column tile's two matrix steps
             auto fetch_v = [&](int c, int k) {
                 const int imm = 2 * k * D::VB * 1024 + (c >> 1) * 1024;
@@ -240,6 +274,7 @@ __global__ __launch_bounds__(64 * D::NW, 2) void k_mla_prefill(MlaPrefillArgs a,
             }
             __builtin_amdgcn_sched_barrier(0);
         }
+        if (v_due) issue_v(coming);
     }
 
     l = half_sum(l);

@@ -46,7 +46,7 @@ def test_sizes():
     assert q.coli_mla_row_bytes(_dims()) == 1152
     assert q.coli_mla_row_bytes(_dims(rank=256, kv_format=q.COLI_KV_E4M3)) == 384
     assert q.coli_mla_workspace_bytes(_dims()) >= 256
-    for bad in ((-1, 1, 0), (4097, 1, 0), (1, 0, 0), (1, 4000, 5), (1, 1, -1)):
+    for bad in ((-1, 1, 0), (4097, 1, 0), (1, 0, 0), (1, 4000, 5), (1, 1, -1), (4000, 1, 1 << 30)):
         with pytest.raises(q.ColiError):
             q.coli_mla_workspace_bytes(_dims(), *bad)
     assert q.make_mla_dims(1, 512, 192, 256, 64).softmax_scale == pytest.approx(1 / 16)
@@ -71,7 +71,8 @@ CALLS = {
                out=P, lse=P, ws=P, wsb=1 << 40:
                q._lib.coli_mla_decode(_ref(d), batch, n_q, ql, qp, pages, scale, n_pages, table, width, lens, max_kv,
                                       out, lse, ws, wsb, None),
-               [dict(batch=-1), dict(batch=4097), dict(n_q=0), dict(n_q=4000), dict(max_kv=-1), dict(ql=None),
+               [dict(batch=-1), dict(batch=4097), dict(n_q=0), dict(n_q=4000), dict(max_kv=-1),
+                dict(batch=4000, max_kv=1 << 30), dict(ql=None),
                 dict(qp=None), dict(table=None), dict(lens=None), dict(out=None), dict(ql=P + 2), dict(qp=P + 2),
                 dict(out=P + 2), dict(width=0), dict(width=1), dict(max_kv=97), dict(pages=None), dict(scale=P),
                 dict(n_pages=-1), dict(ws=None)]),
@@ -89,7 +90,8 @@ CALLS = {
                 [dict(batch=-1), dict(nq=-1), dict(nk=-1), dict(max_q=-1), dict(causal=2), dict(qq=None), dict(kn=None),
                  dict(kp=None), dict(v=None), dict(cq=None), dict(ck=None), dict(out=None), dict(qq=P + 2),
                  dict(kn=P + 2), dict(kp=P + 2), dict(v=P + 2), dict(out=P + 2), dict(qts=4), dict(qhs=-8),
-                 dict(kts=1), dict(khs=4), dict(vts=-8), dict(vhs=12), dict(ws=None)]),
+                 dict(kts=1), dict(khs=4), dict(vts=-8), dict(vhs=12), dict(ws=None), dict(kts=(1 << 23) + 8),
+                 dict(vts=1 << 40), dict(batch=4096, max_q=1 << 30)]),
 }
 
 
@@ -117,7 +119,7 @@ def test_empty_calls_are_no_ops(name, empty):
 def test_project_arguments():
     def call(dt=0, n=3, h=5, a=128, b=512, x=P, ts=640, hs=128, w=P, out=P):
         return q._lib.coli_mla_project(dt, n, h, a, b, x, ts, hs, w, out, None)
-    for bad in (dict(dt=2), dict(n=-1), dict(h=0), dict(h=257), dict(a=96), dict(a=0), dict(a=1088), dict(b=32),
+    for bad in (dict(dt=2), dict(n=-1), dict(n=1 << 30), dict(h=0), dict(h=257), dict(a=96), dict(a=0), dict(a=1088), dict(b=32),
                 dict(b=4160), dict(x=None), dict(w=None), dict(out=None), dict(x=P + 2), dict(w=P + 2),
                 dict(out=P + 2), dict(ts=-8), dict(hs=4)):
         assert call(**bad) == q.COLI_EINVAL, bad
