@@ -4,14 +4,20 @@ Argument marshalling only: each function has the name of the C entry point
 it calls, takes sizes and strides from the tensors, checks that they fit each
 other, and raises ColiError on a non-zero return.  coli_moe_status() reads
 the workspace's device status.
+
+The checks and the call itself run in a CPython module (csrc/mla_bind.cpp),
+since most of these kernels take less time than the same checks here; what
+does not fit there comes back here, where the checks say what it is.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 
 import torch
 
-from . import _lib, ColiError
+from . import _lib, LIB_PATH, ColiError
 
 COLI_BF16, COLI_FP16 = 0, 1
 COLI_KV_PLAIN, COLI_KV_E4M3 = 0, 1
@@ -72,8 +78,6 @@ def _check(rc, where):
         raise ColiError(rc, where)
 
 
-# The checks below run on every call of kernels that take a few microseconds:
-# one expression that passes, the reasons only where it does not.
 def _arg(t, dtype, shape, what):
     """Address of a contiguous device tensor of this type and shape."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
@@ -118,13 +122,26 @@ def _ws(ws):
     return _arg(ws, torch.uint8, (n,), "ws"), n
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _load_bind():
+    path = os.path.join(os.path.dirname(LIB_PATH), "_mla_bind.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with `python -m quantized_expert_ffn_amd.build`")
+    spec = importlib.util.spec_from_file_location("_mla_bind", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+_bind = _load_bind()
+_at = ctypes.addressof
+
+
+def _handle(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def _stream(stream, t):
-    if stream is None:
-        return _raw_stream(t.get_device())
-    return stream if isinstance(stream, int) else stream.cuda_stream
+    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else _handle(stream)
 
 
 def _columns(t, what):
@@ -161,6 +178,9 @@ def coli_mla_workspace_bytes(dims, batch: int = 0, n_q: int = 1, max_kv: int = 0
 def coli_mla_append(dims, kv_a, norm_w, positions, slots, inv_freq, q_pe, q_pe_out, pages, kv_scale, ws, stream=None):
     """norm_w None: the latent is stored as it is.  q_pe and q_pe_out (both may be None): [n, n_heads, 64] views with
     strides of their own; they may be the same tensor."""
+    rc = _bind.append(_at(dims), kv_a, norm_w, positions, slots, inv_freq, q_pe, q_pe_out, pages, kv_scale, ws, _handle(stream))
+    if rc != 1:
+        return _check(rc, "coli_mla_append")
     d, n = dims, kv_a.shape[0]
     dt = _OF[d.dtype]
     q = o = (None, 0, 0)
@@ -181,6 +201,9 @@ def coli_mla_append(dims, kv_a, norm_w, positions, slots, inv_freq, q_pe, q_pe_o
 def coli_mla_project(x, w, out, stream=None):
     """out[t, h] = w[h] x[t, h]: x [n, heads, n_in] (a view with strides of its own), w [heads, n_out, n_in], out
     [n, heads, n_out]."""
+    rc = _bind.project(x, w, out, _handle(stream))
+    if rc != 1:
+        return _check(rc, "coli_mla_project")
     if x.dtype not in _TYPES:
         raise TypeError(f"x: dtype {x.dtype}, expected torch.bfloat16 or torch.float16")
     n, heads, n_in = x.shape
@@ -193,6 +216,9 @@ def coli_mla_project(x, w, out, stream=None):
 
 def coli_mla_decode(dims, q_lat, q_pe, pages, kv_scale, table, kv_lens, max_kv, out, lse, ws, stream=None):
     """q_lat [batch * n_q, n_heads, rank]; the batch is kv_lens'.  lse may be None."""
+    rc = _bind.decode(_at(dims), q_lat, q_pe, pages, kv_scale, table, kv_lens, max_kv, out, lse, ws, _handle(stream))
+    if rc != 1:
+        return _check(rc, "coli_mla_decode")
     d, dt, batch, rows = dims, _OF[dims.dtype], kv_lens.shape[0], q_lat.shape[0]
     if batch and (rows % batch or not rows):
         raise ValueError(f"q_lat: {rows} rows for {batch} sequences")
@@ -208,6 +234,9 @@ def coli_mla_decode(dims, q_lat, q_pe, pages, kv_scale, table, kv_lens, max_kv, 
 
 
 def coli_mla_expand(dims, pages, kv_scale, table, cu_k, w, kv, k_pe, ws, stream=None):
+    rc = _bind.expand(_at(dims), pages, kv_scale, table, cu_k, w, kv, k_pe, ws, _handle(stream))
+    if rc != 1:
+        return _check(rc, "coli_mla_expand")
     d, dt, n, wide = dims, _OF[dims.dtype], kv.shape[0], dims.nope + dims.v_dim
     batch = cu_k.shape[0] - 1
     at, scale, n_pages = _pages(d, pages, kv_scale)
@@ -222,6 +251,9 @@ def coli_mla_expand(dims, pages, kv_scale, table, cu_k, w, kv, k_pe, ws, stream=
 def coli_mla_prefill(dims, q, k_nope, k_pe, v, cu_q, cu_k, max_q, causal, out, lse, ws, stream=None):
     """q, k_nope and v are views with strides of their own (k_nope and v as coli_mla_expand leaves them: kv[..., :nope]
     and kv[..., nope:]).  lse may be None."""
+    rc = _bind.prefill(_at(dims), q, k_nope, k_pe, v, cu_q, cu_k, max_q, causal, out, lse, ws, _handle(stream))
+    if rc != 1:
+        return _check(rc, "coli_mla_prefill")
     d, dt, n, m = dims, _OF[dims.dtype], q.shape[0], k_nope.shape[0]
     batch = cu_q.shape[0] - 1
     _check(_lib.coli_mla_prefill(

@@ -535,6 +535,29 @@ def test_prefill_reports_bad_offsets():
 
 
 # ---------------------------------------------------------------- together
+def test_calls_run_on_the_current_stream_or_the_given_one():
+    """Inputs that a stream writes late are seen by a call on that stream."""
+    say("streams")
+    g = gen(31)
+    real, w = randn(g, 9, 4, 128, dtype=BF), randn(g, 4, 64, 128, dtype=BF)
+    want = torch.empty(9, 4, 64, dtype=BF, device="cuda")
+    q().coli_mla_project(real, w, want)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for given in (False, True):
+        x, out = torch.zeros_like(real), torch.zeros_like(want)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+            x.copy_(real)
+            if not given:
+                q().coli_mla_project(x, w, out)
+        if given:
+            q().coli_mla_project(x, w, out, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), given
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_absorbed_form_is_the_expanded_form(fp8):
     """A prompt's last queries through project, decode, project equal the expanded form's: one cache, two ways."""
