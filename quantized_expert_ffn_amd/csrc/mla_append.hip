@@ -8,6 +8,10 @@
 // reduced to a turn in 64 bits: a position of 1e5 times a frequency near one
 // has no fraction left in binary32.  All wavefronts then rotate the queries,
 // sixteen values (eight pairs) a thread.
+//
+// What bounds it: bytes, of which the queries' are the most: 8191 tokens, 64
+// heads, E4M3 latents: 27 us and 149 MB, 5.5 TB/s, from a warm cache, 36 us
+// from a cold one; one token: 2.9 us.
 #include "mla_common.h"
 
 namespace coli {

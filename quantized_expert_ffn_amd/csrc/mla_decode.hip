@@ -6,6 +6,15 @@
 // latents, so a sequence is one product [rows x (rank + 64)] x [tokens] and
 // one [tokens] x [rank], of the same cached tile: read from memory once, used
 // twice from LDS.
+//
+// What bounds it: up to 64 rows the cached bytes (131071 tokens, 64 heads,
+// rank 512, bf16: 151 MB; 34.4 us and 9.8 us for the join, 4.4 TB/s in the
+// first); from 128 rows on a tile's own chain of scores, softmax and values,
+// which one wavefront a SIMD runs through without overlap (registers: 144 of
+// queries and 128 of accumulators): a four-token verify of 64 heads over
+// 115700 E4M3 tokens takes 81 us and 9.4 us, 0.70 PFLOP/s, matrix cores 35%
+// busy; reads from LDS, widening, softmax, loads and page bookkeeping each
+// account for 5 to 7 us of it.
 #include "kernels.h"
 #include "mla_mfma.h"
 
@@ -23,7 +32,10 @@ constexpr float UNIT_LAG = 16.0f;
 
 // Four wavefronts: RG groups of 32 rows, each of CG = 4 / RG wavefronts that
 // share the output's columns.  Wavefronts 0 and 1 of a group score half of a
-// tile's tokens each and hand their weights to the others through LDS.
+// tile's tokens each and hand their weights to the others through LDS.  Whole
+// columns for a wavefront would spare that exchange, but 256 registers of
+// accumulators beside 144 of queries spilled 330 and more; one row group of 64
+// columns' quarters would read every tile from LDS four times.
 template <class T_, int RANK_, bool FP8_, int RG_>
 struct Dec {
     using T = T_;
@@ -656,11 +668,16 @@ __global__ __launch_bounds__(DEEP ? 64 * JOIN_WAVES : 256) void k_mla_join(MlaDe
     if (a.lse && cq == 0 && lane < 32) a.lse[r] = l == 0.0f ? NEG : (m + __builtin_amdgcn_logf(l)) * LN2;
 }
 
-// A join of at most this many groups of 32 rows is a deep one.
-constexpr int JOIN_DEEP = 16;
+// A join of at most this many groups of 32 rows is a deep one (131071 tokens,
+// 64 heads: 44.5 against 92 us for the whole call; 8 x 4096 tokens, 32 heads:
+// 25.0 against 26.2; 16 x 2000 tokens, 16 heads: 28.6 against 23.2; the uneven
+// batch of 64, 128 heads: 86 against 49).
+constexpr int JOIN_DEEP = 8;
 
-// Rows of a workgroup, and how many workgroups share the batch's tiles: as
-// many as fill the 256 CUs once (a workgroup's LDS and registers take one).
+// Rows of a workgroup: 32 where they suffice (16 heads, 131071 tokens: 38.4 us
+// against 40.6 with 64; 1023 tokens: 13.6 against 14.2), and how many
+// workgroups share the batch's tiles: as many as fill the 256 CUs once (a
+// workgroup's LDS and registers take one).
 int dec_rows(int rows) { return rows <= 32 ? 32 : 64; }
 int dec_groups(int batch, int rows, int max_kv) {
     const int per = dec_rows(rows), blocks = (rows + per - 1) / per;

@@ -9,6 +9,14 @@
 // of every row, form one stream over a workgroup's tiles, through a ring of
 // LDS stages loaded straight from memory; results pass through the stage that
 // was used last, to leave in whole lines.
+//
+// What bounds it: expand of 8192 rows, 64 heads, rank 512, 192 + 256 features,
+// bf16: 239 us, 1.0 PFLOP/s and 470 MB written; without its loads it takes 174
+// us, without its stores 216, without most of its products 167: a step's loads
+// are out for about one step, and LDS serves them beside 0.75 KiB of operands
+// a product (128 x 128 a wavefront would read 0.5, and spills; 128 x 96 takes
+// 300 us).  Project is bound by its bytes: 133 tokens, 128 heads, 512 -> 128,
+// fp16: 8.2 us, 4.7 TB/s; one token, 64 heads, 192 -> 512, bf16: 4.0 us.
 #include "kernels.h"
 #include "mla_mfma.h"
 

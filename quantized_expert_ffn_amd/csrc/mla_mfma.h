@@ -154,7 +154,8 @@ __device__ __forceinline__ void load_to_lds(const void *src, uint32_t lds, int l
 }
 
 // The same from a base all lanes share and an offset of each.  Five wait
-// states would have to pass if a vector instruction had just written the base.
+// states pass before the load, what it needs if a vector instruction has just
+// written the base.
 template <int OFF>
 __device__ __forceinline__ void load_to_lds_from(const void *base, uint32_t at, uint32_t lds, int lds_off) {
     asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1 offset:%4" ::"v"(at), "s"(base),
