@@ -12,7 +12,7 @@
 // first); from 128 rows on a tile's own chain of scores, softmax and values,
 // which one wavefront a SIMD runs through without overlap (registers: 144 of
 // queries and 128 of accumulators): a four-token verify of 64 heads over
-// 115700 E4M3 tokens takes 81 us and 9.4 us, 0.70 PFLOP/s, matrix cores 35%
+// 115700 E4M3 tokens takes 82 us and 9.4 us, 0.70 PFLOP/s, matrix cores 35%
 // busy; reads from LDS, widening, softmax, loads and page bookkeeping each
 // account for 5 to 7 us of it.
 #include "kernels.h"

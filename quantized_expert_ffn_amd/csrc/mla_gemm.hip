@@ -12,10 +12,10 @@
 //
 // What bounds it: expand of 8192 rows, 64 heads, rank 512, 192 + 256 features,
 // bf16: 239 us, 1.0 PFLOP/s and 470 MB written; without its loads it takes 174
-// us, without its stores 216, without most of its products 167: a step's loads
-// are out for about one step, and LDS serves them beside 0.75 KiB of operands
-// a product (128 x 128 a wavefront would read 0.5, and spills; 128 x 96 takes
-// 300 us).  Project is bound by its bytes: 133 tokens, 128 heads, 512 -> 128,
+// us, with one product in eight 167: a step's loads are out for about one
+// step, and LDS serves them beside 0.75 KiB of operands a product (128 x 128 a
+// wavefront would read 0.5, and spills; 128 x 96 takes 300 us).  Stores that
+// pass L2 by took it there from 275 us, 216 of them without any store.  Project is bound by its bytes: 133 tokens, 128 heads, 512 -> 128,
 // fp16: 8.2 us, 4.7 TB/s; one token, 64 heads, 192 -> 512, bf16: 4.0 us.
 #include "kernels.h"
 #include "mla_mfma.h"
@@ -272,6 +272,14 @@ int gemm_parts(int64_t items, int m_tiles) {
     return (int)(parts < 1 ? 1 : parts < m_tiles ? parts : m_tiles);
 }
 
+// How many m x n tiles cover features x tokens.
+int64_t gemm_tile_count(int64_t features, int64_t tokens, int m, int n) {
+    return (features + m - 1) / m * ((tokens + n - 1) / n);
+}
+// 128 x 32 tiles of three stages, two workgroups a CU, start soonest: they are
+// taken where all run at once.
+constexpr int64_t SMALL_TILES = 512;
+
 template <class D>
 hipError_t project(const MlaProjectArgs &a, hipStream_t st) {
     const int mt = (a.n_out + D::TM - 1) / D::TM, nt = (a.tokens + D::TN - 1) / D::TN;
@@ -291,9 +299,14 @@ hipError_t expand(const MlaExpandArgs &a, int rank, hipStream_t st) {
     return hipGetLastError();
 }
 
+// Which tiles, at rank 512, bf16.  128 x 32 against 256 x 128: 16 heads of 256
+// features, 512 rows (512 tiles): 9.1 us against 12.8; 64 heads of 448, 64 rows
+// (448): 9.4 against 13.1; 160 rows of those (1120): 21.5 against 14.7.  256 x
+// 128 against 256 x 256, 64 heads of 448, where the fuller last round decides:
+// 1034 rows: 44.2 against 53.3; 8192 rows: 286 against 249.
 template <class T, bool FP8>
 hipError_t expand_by_size(const MlaExpandArgs &a, int rank, hipStream_t st) {
-    if (a.rows <= 32) return expand<Gemm<T, FP8, 128, 32, 4, 4, 3, 2>>(a, rank, st);
+    if (a.rows <= 32 || gemm_tile_count(a.n_out, a.rows, 128, 32) <= SMALL_TILES) return expand<Gemm<T, FP8, 128, 32, 4, 4, 3, 2>>(a, rank, st);
     // rounds of 256 workgroups, in tokens
     auto rounds = [&](int tn) {
         const int64_t mt = (a.n_out + 255) / 256, nt = (a.rows + tn - 1) / tn, parts = nt < 256 ? 256 / nt : 1;
@@ -305,11 +318,21 @@ hipError_t expand_by_size(const MlaExpandArgs &a, int rank, hipStream_t st) {
 
 }  // namespace
 
+// Which tiles, bf16.  128 x 32 against 128 x 128: 16 heads, 512 -> 128, 300
+// tokens (160 tiles): 6.7 us against 8.5; 64 heads, 512 -> 256, 100 tokens
+// (512): 8.2 against 8.7, 200 tokens (896): 12.6 against 9.7.  256 x 256 needs
+// long sums and tiles for most CUs: 64 heads, 512 -> 256, 600 tokens (192
+// tiles): 19.8 against 21.8, 4096 tokens: 103 against 131; 16 heads of those,
+// 2048 tokens (128 tiles): 19.1 against 13.9; 64 heads, 192 -> 512, 4096
+// tokens: 130 against 100.  128 heads, 128 -> 512 gain by it at 8000 tokens
+// (395 against 376) and lose at 8192 (353 against 437).
 hipError_t launch_mla_project(const MlaProjectArgs &a, int dtype, hipStream_t st) {
     return mla_with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        if (a.tokens <= 32) return project<Gemm<T, false, 128, 32, 4, 4, 3, 2>>(a, st);
-        if (a.n_out <= 128 || a.tokens <= 512) return project<Gemm<T, false, 128, 128, 4, 2, 2, 2, true>>(a, st);
+        if (a.tokens <= 32 || gemm_tile_count(a.n_out, a.tokens, 128, 32) * a.heads <= SMALL_TILES)
+            return project<Gemm<T, false, 128, 32, 4, 4, 3, 2>>(a, st);
+        if (a.n_in <= 192 || a.n_out <= 128 || gemm_tile_count(a.n_out, a.tokens, 256, 256) * a.heads < 192)
+            return project<Gemm<T, false, 128, 128, 4, 2, 2, 2, true>>(a, st);
         return project<Gemm<T, false, 256, 256, 8, 2, 2, 1, true>>(a, st);
     });
 }

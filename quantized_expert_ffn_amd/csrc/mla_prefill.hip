@@ -8,11 +8,12 @@
 // What bounds it: the matrix cores at the clock they are left with.  8192
 // tokens, 64 heads, widths 192 + 64 and 256, bf16, causal: 1.91 ms, 1.15
 // PFLOP/s, 0.82 of what a large library product of the same type reaches on
-// the card; counters: matrix cores 63% busy at 1.74 GHz, LDS 32%, no bank
-// conflicts.  Without its loads the kernel takes 1.72 ms, without its
-// exponentials 1.85 ms.  Short calls are bound by the chain of a tile: ragged
-// prompts of up to 513 queries over 1500 keys, 32 heads, widths 128 + 64 and
-// 128, fp16: 41 us, 24 tiles in a row for the longest.
+// the card; counters: matrix cores 63% busy at 1.74 GHz, LDS 32%, hardly a
+// bank conflict.  An earlier 1.94 ms became 1.72 without the loads after the
+// first tiles and 1.85 without the exponentials.  Short calls are bound by the
+// chain of a tile: ragged prompts of up to 513 queries over 1500 keys, 32
+// heads, widths 128 + 64 and 128, fp16: 41 us, 24 tiles in a row for the
+// longest.
 #include "kernels.h"
 #include "mla_mfma.h"
 
@@ -28,8 +29,8 @@ constexpr float MAX_LAG = 8.0f;
 // NW wavefronts share tiles of KT keys and values: NW / KG groups of 32
 // queries, each of KG wavefronts that take 32 keys of a tile each.  Eight
 // wavefronts of 256 registers are two a SIMD, so that one's softmax runs under
-// the other's products (four on tiles of 32 keys, two workgroups a CU: 1.97
-// ms against 1.94).
+// the other's products (four on tiles of 32 keys took 1.97 and 2.38 ms in two
+// builds in which eight on 64 took 1.94).
 template <class T_, int NOPE_, int V_, int NW_, int KT_, int KG_>
 struct Pre {
     using T = T_;

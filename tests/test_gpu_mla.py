@@ -196,6 +196,14 @@ def test_project(dtype, n, heads, n_in, n_out):
     assert (out[n] == 7).all(), "written behind the last token"
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n,heads,n_in,n_out", [(300, 20, 192, 512), (517, 37, 64, 192), (259, 67, 512, 64), (513, 33, 512, 320),
+                                                (770, 48, 256, 192), (40, 150, 1024, 320), (257, 96, 320, 512)])
+def test_project_of_many_heads(dtype, n, heads, n_in, n_out):
+    """Products of more tiles than run at once, whose last tokens and features do not fill a tile."""
+    test_project(dtype, n, heads, n_in, n_out)
+
+
 # ---------------------------------------------------------------- decode
 def run_decode(g, lens, n_q, heads, rank, dtype, fp8, page, poison=None, spread=1.0, max_kv=None, with_lse=True):
     pages, scale, table = cache(g, lens, rank, dtype, fp8, page)
@@ -395,6 +403,15 @@ def test_expand(dtype, rank, fp8, lens, heads, page, nope):
     ref.close(kv[:n], want, 1.01 * ref.U[dtype] * want.abs() + (rank + 4) * ref.U32 * mag + ref.TINY[dtype], "kv")
     assert torch.equal(k_pe[:n].double(), key[at])
     assert (kv[n:] == 7).all() and (k_pe[n:] == 7).all(), "written behind the last row"
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("rank,fp8", [(512, False), (512, True), (256, False), (256, True)])
+@pytest.mark.parametrize("lens,heads,page,nope", [([333, 1, 0, 700], 37, 48, 192), ([129, 62], 64, 16, 128), ([300], 64, 64, 192),
+                                                  ([2000, 49, 0], 33, 1, 128), ([95, 2], 128, 64, 128)])
+def test_expand_of_many_heads(dtype, rank, fp8, lens, heads, page, nope):
+    """Products of more tiles than run at once."""
+    test_expand(dtype, rank, fp8, lens, heads, page, nope)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
