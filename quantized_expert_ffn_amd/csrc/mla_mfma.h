@@ -33,7 +33,8 @@ __device__ __forceinline__ f32x16 mfma32<_Float16>(x8<_Float16> a, x8<_Float16> 
 }
 
 // LDS is addressed by byte offset from the start of the workgroup's dynamic
-// allocation, which begins at offset 0 (the kernels declare no static LDS).
+// allocation, which begins at offset 0: the kernels declare no static LDS and
+// call nothing that has some (a barrier that carries a value does).
 // `imm` is a constant the instruction's offset field takes.
 template <class V>
 __device__ __forceinline__ V lds_read(uint32_t off, int imm = 0) {

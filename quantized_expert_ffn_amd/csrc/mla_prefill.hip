@@ -45,7 +45,9 @@ struct Pre {
     static_assert(KG == 1 || KT == 64, "two halves of 32 keys");
     static constexpr int JOIN = KG == 2 ? L_ML + NW * 32 * 8 : 0;
     static constexpr int STAGES = 3 * TILE <= 160 * 1024 ? 3 : 2;   // tiles in LDS: loads run one or two ahead
-    static constexpr int LDS = STAGES * TILE > JOIN ? STAGES * TILE : JOIN;
+    static constexpr int L_ODD = STAGES * TILE > JOIN ? STAGES * TILE : JOIN;   // int: a wavefront set a value aside
+    static constexpr int LDS = L_ODD + 16;
+    static_assert(LDS <= 160 * 1024, "the LDS of a CU");
     static constexpr int LOADS = KB + VB;                            // of a wavefront, for a tile
 };
 
@@ -151,6 +153,9 @@ __global__ __launch_bounds__(64 * D::NW, 2) void k_mla_prefill(MlaPrefillArgs a,
         issue_k(tile);
         issue_v(tile);
     };
+    // Cleared before the first tile's barrier, set after it.  A word of the kernel's own: a barrier that carries a value
+    // would take one of the device library's, at the byte where the dynamic allocation is addressed from.
+    if (tid == 0) lds_write<int>(D::L_ODD, 0);
     if (tiles > 0) issue(0);
     if (D::STAGES == 3 && tiles > 1) issue(1);
 
@@ -341,7 +346,11 @@ __global__ __launch_bounds__(64 * D::NW, 2) void k_mla_prefill(MlaPrefillArgs a,
             }
         if (a.lse && hf == 0 && half == 0) a.lse[r] = l == 0.0f ? NEG : (m + __builtin_amdgcn_logf(l)) * LN2;
     }
-    if (__syncthreads_or(odd)) {
+    if (__ballot(odd) && lane == 0) lds_write<int>(D::L_ODD, 1);
+    barrier_lds();
+    if (lds_read<int>(D::L_ODD)) {
+        wait_vm<0>();   // the results are there for the others to add to
+        barrier_lds();
         // the values set aside: their column of every query that sees them
         for (int c = tid; c < V; c += THREADS)
             for (int t = block_seen; t < sees(last); ++t) {
