@@ -151,7 +151,7 @@ template <int OFF = 0>
 __device__ __forceinline__ void load_to_lds(const void *src, uint32_t lds, int lds_off = 0) {
     asm volatile("s_add_u32 m0, %1, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off offset:%3" ::"v"(src),
                  "s"(__builtin_amdgcn_readfirstlane((int)lds)), "i"(lds_off - OFF), "n"(OFF)
-                 : "memory", "scc");
+                 : "memory", "scc", "m0");
 }
 
 // The same from a base all lanes share and an offset of each.  Five wait
@@ -161,7 +161,7 @@ template <int OFF>
 __device__ __forceinline__ void load_to_lds_from(const void *base, uint32_t at, uint32_t lds, int lds_off) {
     asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1 offset:%4" ::"v"(at), "s"(base),
                  "s"(__builtin_amdgcn_readfirstlane((int)lds)), "i"(lds_off - OFF), "n"(OFF)
-                 : "memory", "scc");
+                 : "memory", "scc", "m0");
 }
 
 // A value that is the same in every lane, as a scalar.

@@ -50,3 +50,17 @@ def test_dynamic_lds_begins_at_zero(name, count, tmp_path):
     found = {k: v for k, v in kernels(name, tmp_path).items() if "k_mla_join" not in k}
     assert len(found) >= count and all("k_mla_" in k for k in found), sorted(found)
     assert not {k: v for k, v in found.items() if v}
+
+
+def test_assembly_names_what_it_writes():
+    """Every assembly text that writes m0 or the condition code says so to the compiler."""
+    csrc = os.path.join(ROOT, "quantized_expert_ffn_amd", "csrc")
+    seen = 0
+    for name in sorted(os.listdir(csrc)):
+        for text in re.findall(r"\basm\s+volatile\s*\((.*?)\);", open(os.path.join(csrc, name)).read(), re.S):
+            if re.search(r"\bs_\w+\s+m0\b", text):
+                seen += 1
+                clobbers = text.rsplit(":", 1)[1]
+                assert '"m0"' in clobbers and '"memory"' in clobbers, (name, text)
+                assert "s_add" not in text or '"scc"' in clobbers, (name, text)
+    assert seen
