@@ -27,7 +27,9 @@
  *
  * Arithmetic: inputs of 16 bits, products and sums in binary32, softmax
  * statistics in binary32, results rounded once to 16 bits.  The weights of a
- * softmax are rounded to 16 bits before their product with the values.
+ * softmax are rounded to 16 bits before their product with the values (over
+ * an E4M3 cache, weight times the token's scale is, relative to the largest such
+ * product that the query sees, whatever the scales).
  * Results do not depend on timing: no sum runs through an atomic.
  */
 #ifndef COLI_MLA_H

@@ -27,8 +27,13 @@ constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 // of two: weights then reach 2^8, which every type here holds, and most tiles
 // spare the pass over the accumulators.
 constexpr float MAX_LAG = 8.0f;
-// As little does the unit of E4M3 scales move: weights times scales reach 2^12.
-constexpr float UNIT_LAG = 16.0f;
+//
+// E4M3 tokens have a scale each, f 2^e with 1/2 <= |f| < 1, and what is rounded
+// to 16 bits is weight times scale.  That product has a reference of its own,
+// the row's largest 2^{score + e} so far, lagging alike: a token whose scale is
+// far above the others' takes their bits only as far as its weight lets it
+// count, and one that a row does not see takes none.  f stays outside the
+// exponent and the reference is a whole number, so that e costs no precision.
 
 // Four wavefronts: RG groups of 32 rows, each of CG = 4 / RG wavefronts that
 // share the output's columns.  Wavefronts 0 and 1 of a group score half of a
@@ -54,12 +59,13 @@ struct Dec {
     // alike, or, with codes, through a region of their own.
     static constexpr int L_OFF = 2 * TILE + (FP8 ? QUERY : 0);  // int64 [2][64]: row offsets of tiles to come
     static constexpr int L_SCALE = L_OFF + 2 * 8 * DEC_TILE;  // float [2][64]: E4M3 scales
-    static constexpr int L_TOP = L_SCALE + 2 * 4 * DEC_TILE;  // float [RG][2][32]: maxima, at the end sums
-    static constexpr int L_UNIT = L_TOP + RG * 2 * 32 * 4;    // float [2]: largest scale of a tile
-    static constexpr int L_GROW = L_UNIT + 8;                 // int: the last tile whose maxima had to move, counted from 1
+    static constexpr int L_EXP = L_SCALE + 2 * 4 * DEC_TILE;  // float [2][64]: their exponents
+    static constexpr int L_TOP = L_EXP + (FP8 ? 2 * 4 * DEC_TILE : 0);   // float [RG][2][32]: maxima, at the end sums
+    static constexpr int TOPS = RG * 2 * 32 * 4;              // bytes of them; with codes, as many of score + exponent follow
+    static constexpr int L_GROW = L_TOP + (FP8 ? 2 : 1) * TOPS;   // int: the last tile whose maxima had to move, counted from 1
     // weights: [RG][2][2][64 lanes] of 16 bytes (with codes, in the region of the queries, which are in registers then)
-    static constexpr int L_P = FP8 ? 2 * TILE : L_UNIT + 16;
-    static constexpr int LDS = L_UNIT + 16 + (FP8 ? 0 : RG * 2 * 2048);
+    static constexpr int L_P = FP8 ? 2 * TILE : L_GROW + 16;
+    static constexpr int LDS = L_GROW + 16 + (FP8 ? 0 : RG * 2 * 2048);
     static_assert(LDS <= 160 * 1024, "the LDS of a CU");
     static constexpr int SLOT = ROWS * RANK + 2 * ROWS;       // floats of a partial result
 };
@@ -186,8 +192,9 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
         if (FP8) sc_next = a.c.scale[slot];
     };
     auto put_scales = [&](int it) {
-        lds_write<float>(D::L_SCALE + 4 * ((it & 1) * DEC_TILE + lane), sc_next);
-        lds_write<float>(D::L_UNIT + 4 * (it & 1), wave_max(finite_f32(sc_next) ? fabsf(sc_next) : 0.0f));
+        const uint32_t at = 4 * ((it & 1) * DEC_TILE + lane);
+        lds_write<float>(D::L_SCALE + at, sc_next);
+        lds_write<float>(D::L_EXP + at, sc_next == 0.0f ? NEG : (float)__builtin_amdgcn_frexp_expf(sc_next));
     };
     // what this thread loads: chunk (lane % 8) of tokens 16 wave + lane / 8 and + 8
     const int lt0 = 16 * wave + (lane >> 3), lt1 = lt0 + 8;
@@ -324,7 +331,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[c][r] = 0.0f;
         float m = NEG, l = 0.0f;
-        float unit = 0.0f, inv = 0.0f;   // E4M3: the accumulators are in units of the largest scale so far; its inverse
+        float mv = NEG;   // E4M3: the reference of weights times scales, and of the accumulators
 
         for (; tile < hi; ++tile, ++it) {
             const int buf = it & 1, t0 = tile * DEC_TILE, tw = t0 + 32 * th;
@@ -338,17 +345,24 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
             }
             if (tile + 1 == hi && it + 1 < total) touch_q(seq + 1);
             f32x16 s;
-            float sc[16], sum = 0.0f;
+            float sc[16], sum = 0.0f;   // E4M3: scales, from the scores on their fractions
+            auto exponents = [&](int q) { return lds_read<f32x4>(D::L_EXP + 16 * hf + 4 * (buf * DEC_TILE + 32 * th), 32 * q); };
             auto weigh = [&] {
-                const float ref = m == NEG ? 0.0f : m;
+                const float ref = m == NEG ? 0.0f : m, refv = mv == NEG ? 0.0f : mv;
                 x8<T> p[2];
                 sum = 0.0f;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale, -ref));
-                    sum += w;
-                    if (FP8) w *= sc[r] * inv;
-                    p[r >> 3][r & 7] = (T)w;
+                for (int q = 0; q < 4; ++q) {
+                    f32x4 e;
+                    if (FP8) e = exponents(q);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 4 * q + i;
+                        float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale, -ref));
+                        sum += w;
+                        if (FP8) w = sc[r] * __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale, e[i] - refv));
+                        p[r >> 3][r & 7] = (T)w;
+                    }
                 }
                 lds_write(p_at, p[0], 0);
                 lds_write(p_at, p[1], 1024);
@@ -383,7 +397,10 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                     if (more) issue(it + 1, c / 4, p0, p1);
                     if (FP8 && c == RANK / 32) {
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) s[r] *= sc[r];
+                        for (int r = 0; r < 16; ++r) {
+                            s[r] *= sc[r];
+                            sc[r] = __builtin_amdgcn_frexp_mantf(sc[r]);
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -414,7 +431,20 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                 top = half_max(fmaxf(top, s[15])) * scale;
                 lds_write<float>(top_at + 128 * th, top);
                 bool grows = top > m + MAX_LAG;
-                if (FP8) grows |= lds_read<float>(D::L_UNIT + 4 * buf) > UNIT_LAG * unit;
+                if (FP8) {
+                    float topv = NEG;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4 e = exponents(q);
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2)
+                            topv = fmaxf(fmaxf(topv, __builtin_fmaf(s[4 * q + i], scale, e[i])),
+                                         __builtin_fmaf(s[4 * q + i + 1], scale, e[i + 1]));
+                    }
+                    topv = half_max(topv);
+                    lds_write<float>(top_at + D::TOPS + 128 * th, topv);
+                    grows |= topv > mv + MAX_LAG;
+                }
                 if (__ballot(grows) && lane == 0) lds_write<int>(D::L_GROW, it + 1);
             } else if (more) {
 #pragma unroll
@@ -456,15 +486,15 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                 barrier_lds();   // read by all
                 if (works) {
                     const float top = fmaxf(lds_read<float>(top_at), lds_read<float>(top_at, 128));
-                    const float grown = FP8 ? fmaxf(unit, lds_read<float>(D::L_UNIT + 4 * buf)) : 0.0f;
                     const float to = top > m + MAX_LAG ? top : m;
                     float f = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
                     l *= f;
                     m = to;
-                    if (FP8 && grown > unit) {
-                        f *= unit / grown;
-                        unit = grown;
-                        inv = 1.0f / grown;
+                    if (FP8) {
+                        const float topv = fmaxf(lds_read<float>(top_at + D::TOPS), lds_read<float>(top_at + D::TOPS, 128));
+                        const float tov = topv > mv + MAX_LAG ? rintf(topv) : mv;
+                        f = mv == tov ? 1.0f : __builtin_amdgcn_exp2f(mv - tov);
+                        mv = tov;
                     }
 #pragma unroll
                     for (int c = 0; c < CT; ++c)
@@ -539,10 +569,13 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
             read_q(q_at);
             barrier_lds();
         }
-        const float last_unit = FP8 ? unit : 1.0f;
+        // Results leave divided by the segment's sum; the difference of the references may pass binary32's exponents, half
+        // of it does not.
+        const float half_off = FP8 && l != 0.0f ? __builtin_amdgcn_exp2f(0.5f * (mv - m)) : 1.0f;
+        const float f = l == 0.0f ? 0.0f : half_off / l;
+        auto result = [&](int c, int r) { return FP8 ? o[c][r] * f * half_off : o[c][r] * f; };
         if (lo == 0 && hi == n_tiles) {
             // through the buffer of the last tile, 64 columns at a time, so that rows leave in whole lines
-            const float f = l == 0.0f ? 0.0f : last_unit / l;
             const uint32_t at = spent + wave * 32 * 144;
 #pragma unroll
             for (int c = 0; c < CT; c += 2) {
@@ -550,7 +583,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                 for (int i = 0; i < 8; ++i) {
                     x4<T> v;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] = (T)(o[c + i / 4][4 * (i % 4) + k] * f);
+                    for (int k = 0; k < 4; ++k) v[k] = (T)result(c + i / 4, 4 * (i % 4) + k);
                     lds_write(at + n * 144 + 8 * hf, v, 64 * (i / 4) + 16 * (i % 4));
                 }
 #pragma unroll
@@ -575,7 +608,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                 for (int q = 0; q < 4; ++q) {
                     f32x4 v;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = o[c][4 * q + i] * last_unit;
+                    for (int i = 0; i < 4; ++i) v[i] = result(c, 4 * q + i);
                     *reinterpret_cast<f32x4 *>(at + (c * 4 + q) * 256) = v;
                 }
             if (hf == 0 && cg == 0)
@@ -588,9 +621,9 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
     if (bad_page) raise_status(a.status, ST_BADPAGE);
 }
 
-// Joins the partial results of a sequence: out = sum_g 2^{m_g - M} o_g / sum_g
-// 2^{m_g - M} l_g, over the workgroups in order, 32 rows by 8 columns a
-// wavefront.  DEEP: a workgroup's sixteen wavefronts take every sixteenth
+// Joins the partial results of a sequence, each divided by its own sum: out =
+// sum_g 2^{m_g - M} l_g o_g / sum_g 2^{m_g - M} l_g, over the workgroups in
+// order, 32 rows by 8 columns a wavefront.  DEEP: a workgroup's sixteen wavefronts take every sixteenth
 // partial each of one such piece, for few sequences in many parts; else they
 // take pieces of their own.
 constexpr int JOIN_WAVES = 16;   // of a deep one; else four
@@ -632,8 +665,8 @@ __global__ __launch_bounds__(DEEP ? 64 * JOIN_WAVES : 256) void k_mla_join(MlaDe
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
             if (g + i * EVERY <= g1) {
-                const float f = weight(ml[i].x, m);
-                l = __builtin_fmaf(ml[i].y, f, l);
+                const float f = ml[i].y * weight(ml[i].x, m);
+                l += f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[k] = __builtin_fmaf(v[i][k], f, o[k]);
             }

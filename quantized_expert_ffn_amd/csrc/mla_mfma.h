@@ -102,22 +102,6 @@ __device__ __forceinline__ float half_sum(float v) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// The largest value of the wavefront, in every lane (rotations within 16
-// lanes, then exchanges of rows and halves; no LDS).
-template <int CTRL>
-__device__ __forceinline__ float dpp_max(float v) {
-    const int x = __builtin_bit_cast(int, v);
-    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(x, x, CTRL, 0xf, 0xf, false)));
-}
-__device__ __forceinline__ float wave_max(float v) {
-    v = dpp_max<0x128>(v);
-    v = dpp_max<0x124>(v);
-    v = dpp_max<0x122>(v);
-    v = dpp_max<0x121>(v);
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
-}
-
 // Inclusive sums over the wavefront (shifts within 16 lanes, then broadcasts
 // of the rows before).
 template <int CTRL, int ROWS>

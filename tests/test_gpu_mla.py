@@ -303,6 +303,99 @@ def test_decode_scales_far_apart():
     run_decode(gen(9), [400, 90], 1, 64, 512, BF, True, 16, poison)
 
 
+def _outlier(at, rank, page, lens, times, down, dtype):
+    """Token `at` of each sequence: a scale of `times` and a latent of one column, which it has alone and no query looks
+    at, and a key that lowers its score by about `down`."""
+    def change(pages, scale, table):
+        flat = pages.view(-1, pages.shape[-1])
+        flat[:, 0] = 0
+        for b, n in enumerate(lens):
+            s = int(ref.slots_of(table, b, n, page)[at])
+            flat[s, 1:rank] = 0
+            flat[s, 0] = 0x7e   # 448
+            scale[s] = times / 448
+            flat[s, rank:].view(dtype)[:] = -down / (64 * 192 ** -0.5)
+    return change
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("heads,n_q", [(16, 1), (64, 1), (16, 4)])
+@pytest.mark.parametrize("times,down", [(2.0 ** 16, 60.0), (2.0 ** 26, 60.0), (2.0 ** 26, 18.0), (2.0 ** 100, 800.0),
+                                        (2.0 ** 100, 104.0), (2.0 ** -40, 0.0), (0.0, -5.0)])
+def test_decode_scale_of_one_token(dtype, heads, n_q, times, down):
+    """One token's scale far from the others': a token of no weight takes nothing from them, one whose small weight times
+    its scale counts is counted, one whose weight times its scale is nothing leaves the others their precision."""
+    say("decode scale of one", dtype, heads, n_q, times, down)
+    rank, page, lens = 256, 16, [70, 333]
+    for at in (3, 66):   # in a sequence's first tile, in a later one
+        g = gen(heads)
+        pages, scale, table = cache(g, lens, rank, dtype, True, page)
+        _outlier(at, rank, page, lens, times, down, dtype)(pages, scale, table)
+        n = len(lens) * n_q
+        q_lat, q_pe = randn(g, n, heads, rank, dtype=dtype), torch.ones(n, heads, 64, dtype=dtype, device="cuda")
+        q_lat[..., 0] = 0
+        _decode_and_compare(q_lat, q_pe, pages, scale, table, lens, n_q, page, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("heads,n_q", [(5, 4), (64, 2)])
+def test_decode_scale_of_an_unseen_token(dtype, heads, n_q):
+    """The last draft token's scale is 2^26 times the others': the queries before it have the bits they have without."""
+    say("decode unseen scale", dtype, heads, n_q)
+    rank, page, lens = 512, 16, [77, 300]
+    outs = []
+    for times in (1.0, 2.0 ** 26):
+        g = gen(7)
+        pages, scale, table = cache(g, lens, rank, dtype, True, page)
+        for b, n in enumerate(lens):
+            scale[ref.slots_of(table, b, n, page)[-1]] *= times
+        n = len(lens) * n_q
+        q_lat, q_pe = randn(g, n, heads, rank, dtype=dtype), randn(g, n, heads, 64, dtype=dtype)
+        d = dims(heads, rank, dtype, True, page, scale=192 ** -0.5)
+        ws = workspace(d, len(lens), n_q, max(lens))
+        out, lse = torch.full((n, heads, rank), NAN, dtype=dtype, device="cuda"), torch.full((n, heads), NAN, device="cuda")
+        q().coli_mla_decode(d, q_lat, q_pe, pages, scale, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), max(lens),
+                            out, lse, ws)
+        ok(ws)
+        outs.append((out.view(len(lens), n_q, heads, rank)[:, :-1], lse.view(len(lens), n_q, heads)[:, :-1]))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("power", [-134, -120, 60])
+@pytest.mark.parametrize("lens,heads,n_q", [([40, 333], 5, 2), ([9000], 64, 1)])
+def test_decode_small_and_large_scales(power, lens, heads, n_q):
+    """All scales at the ends of binary32's range, below its normal numbers too; keys alone make the scores."""
+    say("decode scales at the ends", power, lens, heads)
+    rank, page = 512, 64
+    g = gen(heads)
+    pages, scale, table = cache(g, lens, rank, BF, True, page)
+    scale *= 2.0 ** (power / 2)
+    scale *= 2.0 ** (power / 2)
+    n = len(lens) * n_q
+    q_lat, q_pe = torch.zeros(n, heads, rank, dtype=BF, device="cuda"), randn(g, n, heads, 64, dtype=BF)
+    _decode_and_compare(q_lat, q_pe, pages, scale, table, lens, n_q, page, BF)
+
+
+def _decode_and_compare(q_lat, q_pe, pages, scale, table, lens, n_q, page, dtype):
+    n, heads, rank = q_lat.shape
+    d = dims(heads, rank, dtype, scale is not None, page, scale=192 ** -0.5)
+    ws = workspace(d, len(lens), n_q, max(lens))
+    ws[256:] = 0xff   # stale partial results
+    out, lse = torch.full((n, heads, rank), NAN, dtype=dtype, device="cuda"), torch.full((n, heads), NAN, device="cuda")
+    q().coli_mla_decode(d, q_lat, q_pe, pages, scale, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), max(lens),
+                        out, lse, ws)
+    ok(ws)
+    lat, key = ref.rows_of(pages, scale, rank, dtype)
+    want, wl, mag, smag = ref.decode(q_lat, q_pe, lat, key, table, lens, n_q, page, d.softmax_scale)
+    tol, tl = ref.attend_tol(want, mag, smag, rank + 64, max(lens), dtype)
+    # a weight below the least normal number of binary16 is off by up to half a step of it, 2^-25 of the row's largest
+    # weight times scale (which is at least 2^-2 of the unit), times a code of up to 448
+    if scale is not None and dtype == FP:
+        tol = tol + sum(lens) * 2.0 ** -23 * mag.amax(-1, keepdim=True)
+    ref.close(out, want, tol, "out")
+    ref.close(lse, wl, tl, "lse")
+
+
 def test_decode_far_pages():
     """Byte offsets past 32 bits in a long cache."""
     say("decode far pages")
