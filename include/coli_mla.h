@@ -29,7 +29,8 @@
  * statistics in binary32, results rounded once to 16 bits.  The weights of a
  * softmax are rounded to 16 bits before their product with the values (over
  * an E4M3 cache, weight times the token's scale is, relative to the largest such
- * product that the query sees, whatever the scales).
+ * product that the query sees, whatever the scales).  In binary16 a weight below
+ * 2^-19 of the row's largest has fewer than eleven bits, one below 2^-30 none.
  * Results do not depend on timing: no sum runs through an atomic.
  */
 #ifndef COLI_MLA_H

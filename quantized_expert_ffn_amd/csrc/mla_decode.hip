@@ -24,8 +24,8 @@ namespace {
 constexpr int DEC_TILE = 64;     // tokens a tile
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 // The running maximum moves only when a score exceeds it by this many powers
-// of two: weights then reach 2^8, which every type here holds, and most tiles
-// spare the pass over the accumulators.
+// of two: weights then reach 2^8 (binary16, lifted by 2^7: 2^15), which both
+// types hold, and most tiles spare the pass over the accumulators.
 constexpr float MAX_LAG = 8.0f;
 //
 // E4M3 tokens have a scale each, f 2^e with 1/2 <= |f| < 1, and what is rounded
@@ -330,7 +330,8 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
         for (int c = 0; c < CT; ++c)
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[c][r] = 0.0f;
-        float m = NEG, l = 0.0f;
+        constexpr float LIFT = WEIGHT_LIFT<T>, LAG = LIFT + MAX_LAG;
+        float m = NEG, l = 0.0f;   // m: the running maximum less LIFT
         float mv = NEG;   // E4M3: the reference of weights times scales, and of the accumulators
 
         for (; tile < hi; ++tile, ++it) {
@@ -430,7 +431,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                 for (int r = 3; r < 15; r += 2) top = fmaxf(fmaxf(top, s[r]), s[r + 1]);
                 top = half_max(fmaxf(top, s[15])) * scale;
                 lds_write<float>(top_at + 128 * th, top);
-                bool grows = top > m + MAX_LAG;
+                bool grows = top > m + LAG;
                 if (FP8) {
                     float topv = NEG;
 #pragma unroll
@@ -443,7 +444,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                     }
                     topv = half_max(topv);
                     lds_write<float>(top_at + D::TOPS + 128 * th, topv);
-                    grows |= topv > mv + MAX_LAG;
+                    grows |= topv > mv + LAG;
                 }
                 if (__ballot(grows) && lane == 0) lds_write<int>(D::L_GROW, it + 1);
             } else if (more) {
@@ -486,13 +487,13 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                 barrier_lds();   // read by all
                 if (works) {
                     const float top = fmaxf(lds_read<float>(top_at), lds_read<float>(top_at, 128));
-                    const float to = top > m + MAX_LAG ? top : m;
+                    const float to = top > m + LAG ? top - LIFT : m;
                     float f = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
                     l *= f;
                     m = to;
                     if (FP8) {
                         const float topv = fmaxf(lds_read<float>(top_at + D::TOPS), lds_read<float>(top_at + D::TOPS, 128));
-                        const float tov = topv > mv + MAX_LAG ? rintf(topv) : mv;
+                        const float tov = topv > mv + LAG ? rintf(topv) - LIFT : mv;
                         f = mv == tov ? 1.0f : __builtin_amdgcn_exp2f(mv - tov);
                         mv = tov;
                     }

@@ -102,6 +102,15 @@ __device__ __forceinline__ float half_sum(float v) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// Softmax weights are rounded to T in units of 2^-LIFT of the running maximum's.
+// binary16 has no normal number below 2^-14 and none below 2^-24: relative to
+// the maximum itself, 10^5 keys of 2^-26 each would vanish, 2^-9 of the sum.
+// Lifted by 2^7 they do from 2^-32 on, and the maximum's lag still fits.
+template <class T>
+inline constexpr float WEIGHT_LIFT = 0.0f;
+template <>
+inline constexpr float WEIGHT_LIFT<_Float16> = 7.0f;
+
 // Inclusive sums over the wavefront (shifts within 16 lanes, then broadcasts
 // of the rows before).
 template <int CTRL, int ROWS>

@@ -22,8 +22,8 @@ namespace {
 
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 // The running maximum moves only when a score exceeds it by this many powers
-// of two: weights then reach 2^8, which both types hold, and most tiles spare
-// the pass over the accumulators.
+// of two: weights then reach 2^8 (binary16, lifted by 2^7: 2^15), which both
+// types hold, and most tiles spare the pass over the accumulators.
 constexpr float MAX_LAG = 8.0f;
 
 // NW wavefronts share tiles of KT keys and values: NW / KG groups of 32
@@ -172,7 +172,8 @@ __global__ __launch_bounds__(64 * D::NW, 2) void k_mla_prefill(MlaPrefillArgs a,
     for (int c = 0; c < CT; ++c)
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[c][r] = 0.0f;
-    float m = NEG, l = 0.0f;
+    constexpr float LIFT = WEIGHT_LIFT<T>, LAG = LIFT + MAX_LAG;
+    float m = NEG, l = 0.0f;   // m: the running maximum less LIFT
     const float scale = a.scale * LOG2E;
     bool odd = false;   // a value that is not finite was set aside
 
@@ -248,8 +249,8 @@ __global__ __launch_bounds__(64 * D::NW, 2) void k_mla_prefill(MlaPrefillArgs a,
 #pragma unroll
             for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
             top = half_max(top) * scale;
-            if (__ballot(top > m + MAX_LAG)) {
-                const float to = top > m + MAX_LAG ? top : m;
+            if (__ballot(top > m + LAG)) {
+                const float to = top > m + LAG ? top - LIFT : m;
                 const float f = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
                 l *= f;
                 m = to;

@@ -644,6 +644,66 @@ def test_prefill_reports_bad_offsets():
         assert status(ws) == m.COLI_EINVAL, (cu_q, cu_k, top)
 
 
+def _lift_tol(tol, keys, v):
+    """Weights of binary16 below its normal numbers are off by half a step, 2^-25, where the row's largest is at least
+    2^5 (2^7, less a scale's fraction and the rounding of the reference): `keys` of them, on values of up to v."""
+    return tol + keys * 2.0 ** -30 * v
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,n_q", [(64, 1), (256, 64)])
+def test_decode_many_small_weights(fp8, heads, n_q):
+    """binary16: one key takes nearly all, 60000 others 2^-25.5 of its weight each, which together are seen: shared out
+    over the GPU, and so many rows that a workgroup goes through all tokens."""
+    say("decode small weights", fp8, heads, n_q)
+    n, page, rank = 60000, 64, 256
+    pages = torch.zeros(n // page + 2, page, rank + 128 if fp8 else rank + 64, dtype=torch.uint8 if fp8 else FP, device="cuda")
+    flat = pages.view(-1, pages.shape[-1])
+    scale = torch.ones(flat.shape[0], device="cuda") if fp8 else None
+    flat[:, 5] = 0x38 if fp8 else 1.0   # one
+    flat[777, 5] = 0
+    flat[777, rank:].view(FP)[:] = 25.5 * math.log(2) / (64 * 192 ** -0.5)
+    table = torch.arange(pages.shape[0], dtype=torch.int32, device="cuda")[None].contiguous()
+    q_lat, q_pe = torch.zeros(n_q, heads, rank, dtype=FP, device="cuda"), torch.ones(n_q, heads, 64, dtype=FP, device="cuda")
+    d = dims(heads, rank, FP, fp8, page, scale=192 ** -0.5)
+    ws = workspace(d, 1, n_q, n)
+    out, lse = torch.full((n_q, heads, rank), NAN, dtype=FP, device="cuda"), torch.full((n_q, heads), NAN, device="cuda")
+    q().coli_mla_decode(d, q_lat, q_pe, pages, scale, table, torch.tensor([n], dtype=torch.int32, device="cuda"), n, out, lse, ws)
+    ok(ws)
+    lat, key = ref.rows_of(pages, scale, rank, FP)
+    want, wl, mag, smag = ref.decode(q_lat, q_pe, lat, key, table, [n], n_q, page, d.softmax_scale)
+    assert 1e-3 < float(want[0, 0, 5]) < 2e-3
+    tol, tl = ref.attend_tol(want, mag, smag, rank + 64, n, FP)
+    ref.close(out, want, _lift_tol(tol, n, 1.0), "out")
+    ref.close(lse, wl, tl, "lse")
+
+
+@pytest.mark.parametrize("nope", [128, 192])
+@pytest.mark.parametrize("heads", [2, 256])
+def test_prefill_many_small_weights(nope, heads):
+    """The same of prefill."""
+    say("prefill small weights", nope, heads)
+    n, v_dim = 60000 if heads == 2 else 20000, 128 if nope == 128 else 256
+    d = dims(heads, 512, FP, nope=nope, v=v_dim)
+    kv = torch.zeros(n, 1, nope + v_dim, dtype=FP, device="cuda")
+    kv[:, :, nope + 5] = 1.0
+    kv[777, :, nope + 5] = 0.0
+    kv = kv.expand(n, heads, nope + v_dim)   # every head reads the same keys and values
+    k_pe = torch.zeros(n, 64, dtype=FP, device="cuda")
+    k_pe[777] = 25.5 * math.log(2) / (64 * d.softmax_scale)
+    qq = torch.ones(1, heads, nope + 64, dtype=FP, device="cuda")
+    cu_q, cu_k = ref.cumulative([1], "cuda"), ref.cumulative([n], "cuda")
+    out, lse = torch.full((1, heads, v_dim), NAN, dtype=FP, device="cuda"), torch.full((1, heads), NAN, device="cuda")
+    ws = workspace(d)
+    q().coli_mla_prefill(d, qq, kv[..., :nope], k_pe, kv[..., nope:], cu_q, cu_k, 1, True, out, lse, ws)
+    ok(ws)
+    want, wl, mag, smag = ref.prefill(qq, kv[..., :nope], k_pe, kv[..., nope:], [1], [n], True, d.softmax_scale)
+    assert 4e-4 < float(want[0, 0, 5]) < 2e-3
+    tol, tl = ref.attend_tol(want, mag, smag, nope + 64, n, FP)
+    ref.close(out, want, _lift_tol(tol, n, 1.0), "out")
+    ref.close(lse, wl, tl, "lse")
+
+
 # ---------------------------------------------------------------- together
 def test_calls_run_on_the_current_stream_or_the_given_one():
     """Inputs that a stream writes late are seen by a call on that stream."""
