@@ -19,9 +19,9 @@
  * Conventions are coli_moe.h's: device pointers, caller's workspace (zero
  * filled once before its first use), calls that enqueue and return, 0 or a
  * negative COLI_E* code with coli_moe_last_error(), and device-side
- * conditions (a slot, page id or length outside the cache, offsets that do
- * not ascend) as sticky bits of the workspace's status word, read and cleared
- * by coli_moe_status().  Outputs after a non-zero status are unspecified;
+ * conditions (a slot, page id or length outside the cache, row offsets that do
+ * not ascend or leave their rows) as sticky bits of the workspace's status
+ * word, read and cleared by coli_moe_status().  Outputs after a non-zero status are unspecified;
  * no access leaves the arrays whose sizes the call was given.  Calls that
  * overlap in time need a workspace each.
  *

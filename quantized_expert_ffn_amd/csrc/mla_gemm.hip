@@ -217,6 +217,11 @@ __global__ __launch_bounds__(64 * D::NW, 2) void k_mla_expand(MlaExpandArgs a, i
     const int id = xcd_item(blockIdx.x, gridDim.x);
     const int across = 4 * parts, run = id / across, wide = min(4, n_tiles - 4 * run);
     const int part = (id - run * across) / wide, t0 = (4 * run + (id - run * across) % wide) * D::TN;
+    if (blockIdx.x == 0 && wave == 0) {   // the offsets, for all: from 0, ascending, inside the rows
+        bool bad = a.cu_k[0] != 0 || a.cu_k[a.batch] > a.rows;
+        for (int b = lane; b < a.batch; b += 64) bad |= a.cu_k[b + 1] < a.cu_k[b];
+        if (__ballot(bad) && lane == 0) raise_status(a.status, ST_BADPAGE);
+    }
     const int rows = min(a.rows, a.cu_k[a.batch]);
     if (t0 >= rows) return;
     const int row_bytes = D::FP8 ? rank + 2 * MLA_ROPE : 2 * (rank + MLA_ROPE);

@@ -553,6 +553,38 @@ def test_expand_reports_bad_pages_and_offsets():
     assert status(ws) == m.COLI_EINVAL
 
 
+@pytest.mark.parametrize("lens,tail", [([30, 20], 0), ([3] * 150, 7)])
+def test_expand_reports_offsets_that_do_not_fit(lens, tail):
+    """Offsets that begin behind or before 0, descend anywhere, or end behind the rows."""
+    say("expand bad offsets", len(lens), tail)
+    g, m, batch = gen(1), q(), len(lens)
+    d = dims(2, 256, BF, False, 16)
+    pages, _, table = cache(g, [64] * batch, 256, BF, False, 16)
+    w = randn(g, 2, 256, 256, dtype=BF)
+    rows = sum(lens) + tail
+    kv, k_pe = torch.zeros(rows, 2, 256, dtype=BF, device="cuda"), torch.zeros(rows, 64, dtype=BF, device="cuda")
+    ws, good = workspace(d), ref.cumulative(lens, "cuda")
+    for what in ("good", "first", "before", "middle", "last descends", "last", "negative", "good"):
+        cu = good.clone()
+        if what == "first":
+            cu[0] = 1
+        elif what == "before":
+            cu[0] = -3
+        elif what == "middle":
+            cu[batch // 2] = cu[batch] + 1
+        elif what == "last descends":
+            cu[batch] = cu[batch - 1] - 1
+        elif what == "last":
+            cu[batch] = rows + 1
+        elif what == "negative":
+            cu[batch] = -1
+        m.coli_mla_expand(d, pages, None, table, cu, w, kv, k_pe, ws)
+        if what == "good":
+            ok(ws)
+        else:
+            assert status(ws) == m.COLI_EINVAL and "offset" in m.coli_moe_last_error(), what
+
+
 # ---------------------------------------------------------------- prefill
 def run_prefill(g, q_lens, k_lens, heads, nope, dtype, causal, spread=1.0, poison=None, packed=True):
     v_dim = 128 if nope == 128 else 256
