@@ -76,6 +76,8 @@ typedef struct coli_mla_dims {
 #define COLI_MLA_MAX_ROWS 16384
 #define COLI_MLA_MAX_BATCH 4096
 #define COLI_MLA_MAX_TOKENS (1ll << 36)
+/* Longest sequence (max_kv), and most rows of queries, keys or expansions. */
+#define COLI_MLA_MAX_LENGTH 0x7fffff00
 /* Largest token stride of prefill's keys and values, in elements. */
 #define COLI_MLA_MAX_STRIDE (1 << 23)
 
@@ -154,7 +156,7 @@ int coli_mla_expand(const coli_mla_dims *dims, int32_t batch, int32_t n_rows, co
  *   q      device [n_q_rows, n_heads, nope + 64] of dtype, rotated part last
  *   k_nope device [n_k_rows, n_heads, nope], k_pe device [n_k_rows, 64] (shared by the heads),
  *   v      device [n_k_rows, n_heads, v_dim]; strides of q, k_nope and v in elements, multiples of 8
- *   max_q  host bound of the sequences' query counts
+ *   max_q  host bound of the sequences' query counts; batch * n_heads * ceil(max_q / 128) < 2^28
  *   out    device [n_q_rows, n_heads, v_dim]; lse device f32 [n_q_rows, n_heads], or NULL
  */
 int coli_mla_prefill(const coli_mla_dims *dims, int32_t batch, int32_t n_q_rows, int32_t n_k_rows, const void *q,

@@ -93,11 +93,11 @@ size_t coli_mla_row_bytes(const coli_mla_dims *d) {
 
 size_t coli_mla_workspace_bytes(const coli_mla_dims *d, int32_t batch, int32_t n_q, int32_t max_kv) {
     if (check_mla_dims(d) != COLI_OK) return 0;
-    if (batch < 0 || batch > COLI_MLA_MAX_BATCH || n_q < 1 || max_kv < 0 ||
+    if (batch < 0 || batch > COLI_MLA_MAX_BATCH || n_q < 1 || max_kv < 0 || max_kv > COLI_MLA_MAX_LENGTH ||
         (int64_t)n_q * d->n_heads > COLI_MLA_MAX_ROWS || (int64_t)batch * max_kv > COLI_MLA_MAX_TOKENS) {
         fail(COLI_EINVAL, "batch=%d, n_q=%d, max_kv=%d: batch in 0..%d, n_q >= 1 with n_q * n_heads <= %d, "
-                          "max_kv >= 0 with batch * max_kv <= %lld", batch, n_q, max_kv, COLI_MLA_MAX_BATCH,
-             COLI_MLA_MAX_ROWS, COLI_MLA_MAX_TOKENS);
+                          "max_kv in 0..%d with batch * max_kv <= %lld", batch, n_q, max_kv, COLI_MLA_MAX_BATCH,
+             COLI_MLA_MAX_ROWS, COLI_MLA_MAX_LENGTH, COLI_MLA_MAX_TOKENS);
         return 0;
     }
     return WS_HEAD + (batch ? mla_decode_part_bytes(*d, batch, n_q, max_kv) : 0);
@@ -179,9 +179,9 @@ int coli_mla_decode(const coli_mla_dims *d, int32_t batch, int32_t n_q, const vo
         return fail(COLI_EINVAL, "batch=%d: must be in 0..%d", batch, COLI_MLA_MAX_BATCH);
     if (n_q < 1 || (int64_t)n_q * d->n_heads > COLI_MLA_MAX_ROWS)
         return fail(COLI_EINVAL, "n_q=%d: must be positive, with n_q * n_heads at most %d", n_q, COLI_MLA_MAX_ROWS);
-    if (max_kv < 0 || (int64_t)batch * max_kv > COLI_MLA_MAX_TOKENS)
-        return fail(COLI_EINVAL, "max_kv=%d: must not be negative, with batch * max_kv at most %lld", max_kv,
-                    COLI_MLA_MAX_TOKENS);
+    if (max_kv < 0 || max_kv > COLI_MLA_MAX_LENGTH || (int64_t)batch * max_kv > COLI_MLA_MAX_TOKENS)
+        return fail(COLI_EINVAL, "max_kv=%d: must be in 0..%d, with batch * max_kv at most %lld", max_kv,
+                    COLI_MLA_MAX_LENGTH, COLI_MLA_MAX_TOKENS);
     if (batch == 0) return COLI_OK;
     if (!q_lat || !q_pe || !table || !kv_lens || !out)
         return fail(COLI_EINVAL, "coli_mla_decode: NULL pointer argument");
@@ -219,7 +219,8 @@ int coli_mla_expand(const coli_mla_dims *d, int32_t batch, int32_t n_rows, const
     if (rc) return rc;
     if (batch < 0 || batch > COLI_MLA_MAX_BATCH)
         return fail(COLI_EINVAL, "batch=%d: must be in 0..%d", batch, COLI_MLA_MAX_BATCH);
-    if (n_rows < 0) return fail(COLI_EINVAL, "n_rows=%d < 0", n_rows);
+    if (n_rows < 0 || n_rows > COLI_MLA_MAX_LENGTH)
+        return fail(COLI_EINVAL, "n_rows=%d: must be in 0..%d", n_rows, COLI_MLA_MAX_LENGTH);
     if (batch == 0 || n_rows == 0) return COLI_OK;
     if (!table || !cu_k || !w || !kv || !k_pe) return fail(COLI_EINVAL, "coli_mla_expand: NULL pointer argument");
     if (!aligned16(w) || !aligned16(kv) || !aligned16(k_pe))
@@ -252,6 +253,8 @@ int coli_mla_prefill(const coli_mla_dims *d, int32_t batch, int32_t n_q_rows, in
         return fail(COLI_EINVAL, "batch=%d: must be in 0..%d", batch, COLI_MLA_MAX_BATCH);
     if (n_q_rows < 0 || n_k_rows < 0 || max_q < 0)
         return fail(COLI_EINVAL, "n_q_rows=%d, n_k_rows=%d, max_q=%d: must not be negative", n_q_rows, n_k_rows, max_q);
+    if (n_q_rows > COLI_MLA_MAX_LENGTH || n_k_rows > COLI_MLA_MAX_LENGTH)
+        return fail(COLI_EINVAL, "n_q_rows=%d, n_k_rows=%d: must be at most %d", n_q_rows, n_k_rows, COLI_MLA_MAX_LENGTH);
     if (causal != 0 && causal != 1) return fail(COLI_EINVAL, "causal=%d: must be 0 or 1", causal);
     if (batch == 0 || n_q_rows == 0 || max_q == 0) return COLI_OK;
     if (!q || !cu_q || !cu_k || !out || (n_k_rows > 0 && (!k_nope || !k_pe || !v)))
@@ -263,7 +266,7 @@ int coli_mla_prefill(const coli_mla_dims *d, int32_t batch, int32_t n_q_rows, in
         return fail(COLI_EINVAL, "coli_mla_prefill: strides must be non-negative multiples of 8");
     if (k_token_stride > COLI_MLA_MAX_STRIDE || v_token_stride > COLI_MLA_MAX_STRIDE)
         return fail(COLI_EINVAL, "coli_mla_prefill: token strides of k_nope and v must be at most %d", COLI_MLA_MAX_STRIDE);
-    if ((int64_t)batch * d->n_heads * ((max_q + 127) / 128) >= (int64_t)1 << 28)
+    if ((int64_t)batch * d->n_heads * (((int64_t)max_q + 127) / 128) >= (int64_t)1 << 28)
         return fail(COLI_EINVAL, "coli_mla_prefill: batch=%d, max_q=%d: too many blocks of queries", batch, max_q);
     if ((rc = check_ws(ws, ws_bytes, WS_HEAD, "coli_mla_prefill"))) return rc;
     if ((rc = api_check_device())) return rc;
@@ -287,7 +290,7 @@ int coli_mla_prefill(const coli_mla_dims *d, int32_t batch, int32_t n_q_rows, in
     a.heads = d->n_heads;
     a.n_q_rows = n_q_rows;
     a.n_k_rows = n_k_rows;
-    a.max_q = max_q;
+    a.max_q = max_q < n_q_rows ? max_q : n_q_rows;   // no sequence has more
     a.causal = causal;
     a.scale = d->softmax_scale;
     return launched(launch_mla_prefill(a, *d, static_cast<hipStream_t>(stream)), "prefill");

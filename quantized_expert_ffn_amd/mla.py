@@ -23,7 +23,7 @@ COLI_BF16, COLI_FP16 = 0, 1
 COLI_KV_PLAIN, COLI_KV_E4M3 = 0, 1
 COLI_ROPE_PAIRS, COLI_ROPE_HALVES = 0, 1
 COLI_MLA_ROPE = 64
-COLI_MLA_MAX_ROWS, COLI_MLA_MAX_BATCH = 16384, 4096
+COLI_MLA_MAX_ROWS, COLI_MLA_MAX_BATCH, COLI_MLA_MAX_LENGTH = 16384, 4096, 2 ** 31 - 256
 
 MLA_EXPORTS = ("coli_mla_row_bytes", "coli_mla_workspace_bytes", "coli_mla_append", "coli_mla_project",
                "coli_mla_decode", "coli_mla_expand", "coli_mla_prefill")

@@ -116,6 +116,23 @@ def test_empty_calls_are_no_ops(name, empty):
     assert CALLS[name][0](_dims(), **empty) == q.COLI_OK
 
 
+def test_lengths_end_before_32_bits_do():
+    """Tiles are counted in 32 bits, from a length rounded up."""
+    top = q.COLI_MLA_MAX_LENGTH
+    assert top == 2 ** 31 - 256
+    d = _dims(page_size=65536)
+    assert q.coli_mla_workspace_bytes(d, 1, 1, top) >= q.coli_mla_workspace_bytes(d, 1, 1, 1 << 20)
+    for n in (top + 1, 2 ** 31 - 1):
+        with pytest.raises(q.ColiError) as e:
+            q.coli_mla_workspace_bytes(d, 1, 1, n)
+        assert e.value.code == q.COLI_EINVAL
+        assert CALLS["decode"][0](d, batch=1, max_kv=n, width=32768) == q.COLI_EINVAL
+        assert CALLS["expand"][0](d, rows=n) == q.COLI_EINVAL
+        assert CALLS["prefill"][0](d, nq=n) == q.COLI_EINVAL
+        assert CALLS["prefill"][0](d, nk=n) == q.COLI_EINVAL
+    assert CALLS["prefill"][0](_dims(n_heads=16), batch=1, max_q=2 ** 31 - 1) == q.COLI_EINVAL   # 2^28 blocks
+
+
 def test_project_arguments():
     def call(dt=0, n=3, h=5, a=128, b=512, x=P, ts=640, hs=128, w=P, out=P):
         return q._lib.coli_mla_project(dt, n, h, a, b, x, ts, hs, w, out, None)
