@@ -371,9 +371,22 @@ hipError_t launch(const MlaPrefillArgs &a, hipStream_t st) {
     const int blocks = (a.max_q + D::ROWS - 1) / D::ROWS;
     const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_mla_prefill<D>), D::LDS);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_mla_prefill<D>, dim3((uint32_t)blocks * 8 * ((a.heads * a.batch + 7) / 8)),
-                       dim3(64 * D::NW), D::LDS, st, a, blocks);
-    return hipGetLastError();
+    // A launch has less than 2^32 threads: as many sequences as that leaves (one whose blocks alone passed it would have
+    // more results than the card has memory).
+    const int64_t groups = ((int64_t)1 << 32) / (64 * D::NW) / ((int64_t)blocks * 8) - 1;   // of eight sequences' heads
+    const int64_t most = groups * 8 / a.heads;
+    const int each = (int)(most < 1 ? 1 : most < a.batch ? most : a.batch);
+    for (int b = 0; b < a.batch; b += each) {
+        MlaPrefillArgs part = a;
+        part.cu_q += b;
+        part.cu_k += b;
+        part.batch = a.batch - b < each ? a.batch - b : each;
+        hipLaunchKernelGGL(k_mla_prefill<D>, dim3((uint32_t)blocks * 8 * ((a.heads * part.batch + 7) / 8)), dim3(64 * D::NW),
+                           D::LDS, st, part, blocks);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 template <class T, int NOPE, int V>

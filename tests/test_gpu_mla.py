@@ -661,6 +661,31 @@ def test_prefill_keeps_a_seen_nan_visible(nope, heads):
     assert out[70:, 0, 5].isnan().all() and out[90:, 1, 7].isinf().all()
 
 
+def test_prefill_of_thousands_of_sequences():
+    """One prompt of 4096 tokens among 4095 of one token each, 128 heads: more blocks by the longest prompt than one launch
+    takes.  A token that sees itself alone gets its value."""
+    say("prefill thousands")
+    g, heads, at, long = gen(40), 128, 2500, 4096
+    lens = [1] * 4096
+    lens[at] = long
+    n = sum(lens)
+    d = dims(heads)
+    qq, kv, k_pe = randn(g, n, heads, 192, dtype=BF), randn(g, n, heads, 256, dtype=BF), randn(g, n, 64, dtype=BF)
+    out, lse = torch.full((n, heads, 128), NAN, dtype=BF, device="cuda"), torch.full((n, heads), NAN, device="cuda")
+    cu, ws = ref.cumulative(lens, "cuda"), workspace(d)
+    q().coli_mla_prefill(d, qq, kv[..., :128], k_pe, kv[..., 128:], cu, cu, long, True, out, lse, ws)
+    ok(ws)
+    one = torch.ones(n, dtype=torch.bool, device="cuda")
+    one[at:at + long] = False
+    assert torch.equal(out[one], kv[one][..., 128:])
+    some, span = [0, 63, 127], slice(at, at + long)
+    args = qq[span][:, some], kv[span][:, some, :128], k_pe[span], kv[span][:, some, 128:]
+    want, wl, mag, smag = ref.prefill(*args, [long], [long], True, d.softmax_scale)
+    tol, tl = ref.attend_tol(want, mag, smag, 192, long, BF)
+    ref.close(out[span][:, some], want, tol, "out")
+    ref.close(lse[span][:, some], wl, tl, "lse")
+
+
 def test_prefill_reports_bad_offsets():
     say("prefill bad offsets")
     m = q()
