@@ -195,9 +195,10 @@ __global__ __launch_bounds__(64 * D::NW, 2) void k_mla_prefill(MlaPrefillArgs a,
                 v_due = false;
             }
         }
-        if (block_seen < nk && t0 + D::KT > block_seen) {
+        if (t0 + D::KT > block_seen) {
             // A tile that some queries see only in part: values that are not finite would reach those that do not see
-            // them as 0 * NaN.  They are set aside, and added at the end where they are seen.
+            // them as 0 * NaN.  They are set aside, and added at the end where they are seen.  Places behind the last
+            // key hold its value again, for nobody.
             const int from = block_seen > t0 ? block_seen - t0 : 0;
             for (int i = tid; i < (D::KT - from) * D::VB * 8; i += THREADS) {
                 const int t = from + i / (D::VB * 8), c = i % (D::VB * 8);
@@ -211,7 +212,7 @@ __global__ __launch_bounds__(64 * D::NW, 2) void k_mla_prefill(MlaPrefillArgs a,
                         bad = true;
                     }
                 if (bad) lds_write(w, v);
-                odd |= bad;
+                odd |= bad && t0 + t < nk;
             }
             barrier_lds();
         }

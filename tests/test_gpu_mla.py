@@ -661,6 +661,21 @@ def test_prefill_keeps_a_seen_nan_visible(nope, heads):
     assert out[70:, 0, 5].isnan().all() and out[90:, 1, 7].isinf().all()
 
 
+@pytest.mark.parametrize("nope,heads", [(128, 2), (192, 2), (128, 256), (192, 256)])
+@pytest.mark.parametrize("q_len,causal", [(1, True), (200, False), (1, False)])
+@pytest.mark.parametrize("k_len", [200, 33])
+def test_prefill_last_value_infinite(nope, heads, q_len, causal, k_len):
+    """The last value of a tile that is not full is infinite, and every query sees it: the places behind it hold nothing."""
+    say("prefill last value", nope, heads, q_len, causal, k_len)
+
+    def poison(k_nope, k_pe, v):
+        v[-1, 0, 5] = float("inf")
+        v[-1, 1, 7] = -float("inf")
+        v[-2, 1, 9] = NAN
+    out, _ = run_prefill(gen(6), [q_len], [k_len], heads, nope, BF, causal, poison=poison)
+    assert (out[:, 0, 5] == math.inf).all() and (out[:, 1, 7] == -math.inf).all()
+
+
 def test_prefill_of_thousands_of_sequences():
     """One prompt of 4096 tokens among 4095 of one token each, 128 heads: more blocks by the longest prompt than one launch
     takes.  A token that sees itself alone gets its value."""
