@@ -5,7 +5,8 @@
 // about 5 us on the same checks in Python and 2 us in ctypes.
 //
 // A function returns the entry point's code, or 1 when anything does not fit,
-// whereupon the Python function finds out what and says so.
+// whereupon the Python function finds out what and says so.  Nothing else
+// launches these kernels for Python: no call goes round these checks.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -90,6 +91,7 @@ struct Cache {
 Cache cache(Args &a, const coli_mla_dims *d, int pages, int scale) {
     const bool codes = d->kv_format == COLI_KV_E4M3;
     const int64_t n = a.size(pages, 0, 3);
+    if (n > INT32_MAX) throw Misfit();
     return {a.dense(pages, codes ? at::kByte : type_of(d), {n, d->page_size, d->rank + (codes ? 2 : 1) * COLI_MLA_ROPE}),
             static_cast<float *>(a.dense_or_none(scale, at::kFloat, {n * d->page_size})), n};
 }
@@ -113,6 +115,13 @@ PyObject *call(PyObject *const *v, Py_ssize_t n, F f) {
     return PyLong_FromLong(rc);
 }
 
+// No two of `outer` x `inner` runs of 64 elements at these strides share an
+// element, the inner ones lying between two outer ones.
+bool apart(int64_t outer, int64_t outer_stride, int64_t inner, int64_t inner_stride) {
+    return (inner == 1 || inner_stride >= COLI_MLA_ROPE) &&
+           (outer == 1 || outer_stride >= (inner - 1) * inner_stride + COLI_MLA_ROPE);
+}
+
 at::Device device_of(const Args &a) { return at::Device(at::kCUDA, (c10::DeviceIndex)a.device); }
 
 // dims, kv_a, norm_w, positions, slots, inv_freq, q_pe, q_pe_out, pages, kv_scale, ws, stream
@@ -128,9 +137,8 @@ PyObject *append(PyObject *, PyObject *const *v, Py_ssize_t n) {
         if (!a.none(6)) q = a.view(6, t, {tokens, d->n_heads, COLI_MLA_ROPE});
         if (!a.none(7)) {
             o = a.view(7, t, {tokens, d->n_heads, COLI_MLA_ROPE});
-            // the common layout, heads of a token apart and tokens behind each other; Python judges others
-            if (d->n_heads > 1 && o.head < COLI_MLA_ROPE) throw Misfit();
-            if (tokens > 1 && o.token < (d->n_heads - 1) * o.head + COLI_MLA_ROPE) throw Misfit();
+            if (tokens > 0 && !apart(tokens, o.token, d->n_heads, o.head) && !apart(d->n_heads, o.head, tokens, o.token))
+                throw Misfit();
         }
         const Cache c = cache(a, d, 8, 9);
         const int64_t ws = a.size(10, 0, 1);
@@ -162,7 +170,7 @@ PyObject *decode(PyObject *, PyObject *const *v, Py_ssize_t n) {
     return call<12>(v, n, [](Args &a, const coli_mla_dims *d) -> long {
         const at::ScalarType t = type_of(d);
         const int64_t rows = a.size(1, 0, 3), batch = a.size(6, 0, 1), width = a.size(5, 1, 2);
-        if (batch < 1 || rows < 1 || rows % batch || rows > INT32_MAX || width > INT32_MAX) throw Misfit();
+        if ((batch > 0 && (rows < 1 || rows % batch)) || rows > INT32_MAX || batch > INT32_MAX || width > INT32_MAX) throw Misfit();
         void *q_lat = a.dense(1, t, {rows, d->n_heads, d->rank}), *q_pe = a.dense(2, t, {rows, d->n_heads, COLI_MLA_ROPE});
         const Cache c = cache(a, d, 3, 4);
         void *table = a.dense(5, at::kInt, {batch, width}), *lens = a.dense(6, at::kInt, {batch});
@@ -171,7 +179,7 @@ PyObject *decode(PyObject *, PyObject *const *v, Py_ssize_t n) {
         const int64_t ws = a.size(10, 0, 1);
         void *w = a.dense(10, at::kByte, {ws});
         const c10::DeviceGuard guard(device_of(a));
-        return coli_mla_decode(d, (int32_t)batch, (int32_t)(rows / batch), q_lat, q_pe, c.pages, c.scale, (int32_t)c.n,
+        return coli_mla_decode(d, (int32_t)batch, batch ? (int32_t)(rows / batch) : 1, q_lat, q_pe, c.pages, c.scale, (int32_t)c.n,
                                static_cast<int32_t *>(table), (int32_t)width, static_cast<int32_t *>(lens), (int32_t)max_kv, out,
                                static_cast<float *>(lse), w, (size_t)ws, a.stream(11));
     });
@@ -182,7 +190,7 @@ PyObject *expand(PyObject *, PyObject *const *v, Py_ssize_t n) {
     return call<10>(v, n, [](Args &a, const coli_mla_dims *d) -> long {
         const at::ScalarType t = type_of(d);
         const int64_t rows = a.size(6, 0, 3), batch = a.size(4, 0, 1) - 1, width = a.size(3, 1, 2), wide = d->nope + d->v_dim;
-        if (batch < 0 || rows > INT32_MAX || width > INT32_MAX) throw Misfit();
+        if (batch < 0 || batch > INT32_MAX || rows > INT32_MAX || width > INT32_MAX) throw Misfit();
         const Cache c = cache(a, d, 1, 2);
         void *table = a.dense(3, at::kInt, {batch, width}), *cu = a.dense(4, at::kInt, {batch + 1});
         void *w = a.dense(5, t, {d->n_heads, d->nope + d->v_dim, d->rank}), *kv = a.dense(6, t, {rows, d->n_heads, wide});
@@ -200,7 +208,7 @@ PyObject *prefill(PyObject *, PyObject *const *v, Py_ssize_t n) {
     return call<13>(v, n, [](Args &a, const coli_mla_dims *d) -> long {
         const at::ScalarType t = type_of(d);
         const int64_t rows = a.size(1, 0, 3), keys = a.size(2, 0, 3), batch = a.size(5, 0, 1) - 1;
-        if (batch < 0 || rows > INT32_MAX || keys > INT32_MAX) throw Misfit();
+        if (batch < 0 || batch > INT32_MAX || rows > INT32_MAX || keys > INT32_MAX) throw Misfit();
         const Args::View q = a.view(1, t, {rows, d->n_heads, d->nope + COLI_MLA_ROPE});
         const Args::View k = a.view(2, t, {keys, d->n_heads, d->nope});
         void *k_pe = a.dense(3, t, {keys, COLI_MLA_ROPE});

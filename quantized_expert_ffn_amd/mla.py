@@ -7,12 +7,14 @@ the workspace's device status.
 
 The checks and the call itself run in a CPython module (csrc/mla_bind.cpp),
 since most of these kernels take less time than the same checks here; what
-does not fit there comes back here, where the checks say what it is.
+does not fit there comes back here, where the checks say what it is.  The
+module makes the tensors' device current for the call.
 """
 from __future__ import annotations
 
 import ctypes
 import importlib.util
+import operator
 import os
 
 import torch
@@ -78,34 +80,66 @@ def _check(rc, where):
         raise ColiError(rc, where)
 
 
-def _arg(t, dtype, shape, what):
-    """Address of a contiguous device tensor of this type and shape."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
-    _refuse(t, dtype, shape, what)
-    raise ValueError(f"{what}: must be contiguous")
+class _Refused:
+    """The arguments of a call that the module below refused, one after the other: raises at the first that does not fit.
+    Nothing is launched from here."""
 
+    def __init__(self, where):
+        self.where, self.device = where, None
 
-def _refuse(t, dtype, shape, what):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what}: expected a torch tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: must be a device tensor")
+    def tensor(self, t, dtype, shape, what):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what}: expected a torch tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_cuda:
+            raise ValueError(f"{what}: must be a device tensor")
+        if self.device is None:
+            self.device = t.device
+        if t.device != self.device:
+            raise ValueError(f"{what}: on device {t.device}, expected device {self.device} as the others")
 
+    def dense(self, t, dtype, shape, what):
+        self.tensor(t, dtype, shape, what)
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: must be contiguous")
 
-def _strided(t, dtype, shape, what):
-    """Address and the first two strides of a device tensor [tokens, heads, width] whose last dimension is dense."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda):
-        _refuse(t, dtype, shape, what)
-    a, b, c = t.stride()
-    if c != 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
-    # the stride of a dimension of one element is never used
-    return t.data_ptr(), a if shape[0] > 1 else 0, b if shape[1] > 1 else 0
+    def view(self, t, dtype, shape, what):
+        """[tokens, heads, width] with strides of its own, the last dimension dense."""
+        self.tensor(t, dtype, shape, what)
+        if t.stride(2) != 1:
+            raise ValueError(f"{what}: the last dimension must be contiguous")
+
+    def pages(self, d, pages, kv_scale):
+        if d.kv_format == COLI_KV_E4M3:
+            dtype, row = torch.uint8, d.rank + 2 * COLI_MLA_ROPE
+        else:
+            dtype, row = _OF[d.dtype], d.rank + COLI_MLA_ROPE
+        n = self.size(pages, 3, 0, "pages")
+        self.dense(pages, dtype, (n, d.page_size, row), "pages")
+        if kv_scale is not None:
+            self.dense(kv_scale, torch.float32, (n * d.page_size,), "kv_scale")
+
+    def workspace(self, ws):
+        self.dense(ws, torch.uint8, (self.size(ws, 1, 0, "ws"),), "ws")
+
+    @staticmethod
+    def size(t, dims, dim, what):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what}: expected a torch tensor")
+        if t.dim() != dims:
+            raise ValueError(f"{what}: {t.dim()} dimensions, expected {dims}")
+        return t.shape[dim]
+
+    @staticmethod
+    def number(n, what):
+        if not -2 ** 31 <= operator.index(n) < 2 ** 31:
+            raise ValueError(f"{what}: {n} does not fit 32 bits")
+
+    def end(self):
+        raise ValueError(f"{self.where}: arguments refused")
 
 
 def _distinct(t, strides, what):
@@ -115,11 +149,6 @@ def _distinct(t, strides, what):
     if n and h and not ((h == 1 or hs >= width) and (n == 1 or ts >= (h - 1) * hs + width)
                         or (n == 1 or ts >= width) and (h == 1 or hs >= (n - 1) * ts + width)):
         raise ValueError(f"{what}: strides overlap")
-
-
-def _ws(ws):
-    n = ws.numel()
-    return _arg(ws, torch.uint8, (n,), "ws"), n
 
 
 def _load_bind():
@@ -136,30 +165,18 @@ _bind = _load_bind()
 _at = ctypes.addressof
 
 
+_MISFIT = 1   # the module's answer to arguments that do not fit
+
+
 def _handle(stream):
     return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
-def _stream(stream, t):
-    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else _handle(stream)
-
-
-def _columns(t, what):
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        raise ValueError(f"{what}: expected a tensor of two dimensions")
-    return t.shape[1]
-
-
-def _pages(d, pages, kv_scale):
-    if d.kv_format == COLI_KV_E4M3:
-        dtype, row = torch.uint8, d.rank + 2 * COLI_MLA_ROPE
-    else:
-        dtype, row = _OF[d.dtype], d.rank + COLI_MLA_ROPE
-    n, page = pages.shape[0], d.page_size
-    at = _arg(pages, dtype, (n, page, row), "pages")
-    if kv_scale is not None:
-        kv_scale = _arg(kv_scale, torch.float32, (n * page,), "kv_scale")
-    return at, kv_scale, n
+def _sequences(no, cu, what):
+    n = no.size(cu, 1, 0, what)
+    if n < 1:
+        raise ValueError(f"{what}: needs an offset more than sequences")
+    return n - 1
 
 
 # ---------------------------------------------------------------- entry points
@@ -179,88 +196,98 @@ def coli_mla_append(dims, kv_a, norm_w, positions, slots, inv_freq, q_pe, q_pe_o
     """norm_w None: the latent is stored as it is.  q_pe and q_pe_out (both may be None): [n, n_heads, 64] views with
     strides of their own; they may be the same tensor."""
     rc = _bind.append(_at(dims), kv_a, norm_w, positions, slots, inv_freq, q_pe, q_pe_out, pages, kv_scale, ws, _handle(stream))
-    if rc != 1:
-        return _check(rc, "coli_mla_append")
-    d, n = dims, kv_a.shape[0]
-    dt = _OF[d.dtype]
-    q = o = (None, 0, 0)
-    if q_pe is not None:
-        q = _strided(q_pe, dt, (n, d.n_heads, COLI_MLA_ROPE), "q_pe")
-    if q_pe_out is not None:
-        o = _strided(q_pe_out, dt, (n, d.n_heads, COLI_MLA_ROPE), "q_pe_out")
-        _distinct(q_pe_out, o[1:], "q_pe_out")
-    at, scale, n_pages = _pages(d, pages, kv_scale)
-    _check(_lib.coli_mla_append(
-        ctypes.byref(d), n, _arg(kv_a, dt, (n, d.rank + COLI_MLA_ROPE), "kv_a"),
-        None if norm_w is None else _arg(norm_w, dt, (d.rank,), "norm_w"),
-        _arg(positions, torch.int32, (n,), "positions"), _arg(slots, torch.int64, (n,), "slots"),
-        _arg(inv_freq, torch.float64, (COLI_MLA_ROPE // 2,), "inv_freq"), *q, *o, at, scale, n_pages, *_ws(ws),
-        _stream(stream, kv_a)), "coli_mla_append")
+    if rc == _MISFIT:
+        no, d, dt = _Refused("coli_mla_append"), dims, _OF[dims.dtype]
+        n = no.size(kv_a, 2, 0, "kv_a")
+        no.pages(d, pages, kv_scale)
+        no.dense(kv_a, dt, (n, d.rank + COLI_MLA_ROPE), "kv_a")
+        if norm_w is not None:
+            no.dense(norm_w, dt, (d.rank,), "norm_w")
+        no.dense(positions, torch.int32, (n,), "positions")
+        no.dense(slots, torch.int64, (n,), "slots")
+        no.dense(inv_freq, torch.float64, (COLI_MLA_ROPE // 2,), "inv_freq")
+        if q_pe is not None:
+            no.view(q_pe, dt, (n, d.n_heads, COLI_MLA_ROPE), "q_pe")
+        if q_pe_out is not None:
+            no.view(q_pe_out, dt, (n, d.n_heads, COLI_MLA_ROPE), "q_pe_out")
+            _distinct(q_pe_out, q_pe_out.stride()[:2], "q_pe_out")
+        no.workspace(ws)
+        no.end()
+    _check(rc, "coli_mla_append")
 
 
 def coli_mla_project(x, w, out, stream=None):
     """out[t, h] = w[h] x[t, h]: x [n, heads, n_in] (a view with strides of its own), w [heads, n_out, n_in], out
     [n, heads, n_out]."""
     rc = _bind.project(x, w, out, _handle(stream))
-    if rc != 1:
-        return _check(rc, "coli_mla_project")
-    if x.dtype not in _TYPES:
-        raise TypeError(f"x: dtype {x.dtype}, expected torch.bfloat16 or torch.float16")
-    n, heads, n_in = x.shape
-    n_out = w.shape[1]
-    _check(_lib.coli_mla_project(
-        _TYPES[x.dtype], n, heads, n_in, n_out, *_strided(x, x.dtype, (n, heads, n_in), "x"),
-        _arg(w, x.dtype, (heads, n_out, n_in), "w"), _arg(out, x.dtype, (n, heads, n_out), "out"),
-        _stream(stream, x)), "coli_mla_project")
+    if rc == _MISFIT:
+        no = _Refused("coli_mla_project")
+        n, heads, n_in, n_out = *(no.size(x, 3, i, "x") for i in range(3)), no.size(w, 3, 1, "w")
+        if x.dtype not in _OF.values():
+            raise TypeError(f"x: dtype {x.dtype}, expected torch.bfloat16 or torch.float16")
+        no.view(x, x.dtype, (n, heads, n_in), "x")
+        no.dense(w, x.dtype, (heads, n_out, n_in), "w")
+        no.dense(out, x.dtype, (n, heads, n_out), "out")
+        no.end()
+    _check(rc, "coli_mla_project")
 
 
 def coli_mla_decode(dims, q_lat, q_pe, pages, kv_scale, table, kv_lens, max_kv, out, lse, ws, stream=None):
     """q_lat [batch * n_q, n_heads, rank]; the batch is kv_lens'.  lse may be None."""
     rc = _bind.decode(_at(dims), q_lat, q_pe, pages, kv_scale, table, kv_lens, max_kv, out, lse, ws, _handle(stream))
-    if rc != 1:
-        return _check(rc, "coli_mla_decode")
-    d, dt, batch, rows = dims, _OF[dims.dtype], kv_lens.shape[0], q_lat.shape[0]
-    if batch and (rows % batch or not rows):
-        raise ValueError(f"q_lat: {rows} rows for {batch} sequences")
-    at, scale, n_pages = _pages(d, pages, kv_scale)
-    width = _columns(table, "table")
-    _check(_lib.coli_mla_decode(
-        ctypes.byref(d), batch, rows // batch if batch else 1, _arg(q_lat, dt, (rows, d.n_heads, d.rank), "q_lat"),
-        _arg(q_pe, dt, (rows, d.n_heads, COLI_MLA_ROPE), "q_pe"), at, scale, n_pages,
-        _arg(table, torch.int32, (batch, width), "table"), width, _arg(kv_lens, torch.int32, (batch,), "kv_lens"),
-        max_kv, _arg(out, dt, (rows, d.n_heads, d.rank), "out"),
-        None if lse is None else _arg(lse, torch.float32, (rows, d.n_heads), "lse"), *_ws(ws),
-        _stream(stream, q_lat)), "coli_mla_decode")
+    if rc == _MISFIT:
+        no, d, dt = _Refused("coli_mla_decode"), dims, _OF[dims.dtype]
+        batch, rows = no.size(kv_lens, 1, 0, "kv_lens"), no.size(q_lat, 3, 0, "q_lat")
+        if batch and (rows % batch or not rows):
+            raise ValueError(f"q_lat: {rows} rows for {batch} sequences")
+        no.pages(d, pages, kv_scale)
+        no.dense(q_lat, dt, (rows, d.n_heads, d.rank), "q_lat")
+        no.dense(q_pe, dt, (rows, d.n_heads, COLI_MLA_ROPE), "q_pe")
+        no.dense(table, torch.int32, (batch, no.size(table, 2, 1, "table")), "table")
+        no.dense(kv_lens, torch.int32, (batch,), "kv_lens")
+        no.number(max_kv, "max_kv")
+        no.dense(out, dt, (rows, d.n_heads, d.rank), "out")
+        if lse is not None:
+            no.dense(lse, torch.float32, (rows, d.n_heads), "lse")
+        no.workspace(ws)
+        no.end()
+    _check(rc, "coli_mla_decode")
 
 
 def coli_mla_expand(dims, pages, kv_scale, table, cu_k, w, kv, k_pe, ws, stream=None):
     rc = _bind.expand(_at(dims), pages, kv_scale, table, cu_k, w, kv, k_pe, ws, _handle(stream))
-    if rc != 1:
-        return _check(rc, "coli_mla_expand")
-    d, dt, n, wide = dims, _OF[dims.dtype], kv.shape[0], dims.nope + dims.v_dim
-    batch = cu_k.shape[0] - 1
-    at, scale, n_pages = _pages(d, pages, kv_scale)
-    width = _columns(table, "table")
-    _check(_lib.coli_mla_expand(
-        ctypes.byref(d), batch, n, at, scale, n_pages, _arg(table, torch.int32, (batch, width), "table"),
-        width, _arg(cu_k, torch.int32, (batch + 1,), "cu_k"), _arg(w, dt, (d.n_heads, wide, d.rank), "w"),
-        _arg(kv, dt, (n, d.n_heads, wide), "kv"), _arg(k_pe, dt, (n, COLI_MLA_ROPE), "k_pe"), *_ws(ws),
-        _stream(stream, kv)), "coli_mla_expand")
+    if rc == _MISFIT:
+        no, d, dt, wide = _Refused("coli_mla_expand"), dims, _OF[dims.dtype], dims.nope + dims.v_dim
+        n, batch = no.size(kv, 3, 0, "kv"), _sequences(no, cu_k, "cu_k")
+        no.pages(d, pages, kv_scale)
+        no.dense(table, torch.int32, (batch, no.size(table, 2, 1, "table")), "table")
+        no.dense(cu_k, torch.int32, (batch + 1,), "cu_k")
+        no.dense(w, dt, (d.n_heads, wide, d.rank), "w")
+        no.dense(kv, dt, (n, d.n_heads, wide), "kv")
+        no.dense(k_pe, dt, (n, COLI_MLA_ROPE), "k_pe")
+        no.workspace(ws)
+        no.end()
+    _check(rc, "coli_mla_expand")
 
 
 def coli_mla_prefill(dims, q, k_nope, k_pe, v, cu_q, cu_k, max_q, causal, out, lse, ws, stream=None):
     """q, k_nope and v are views with strides of their own (k_nope and v as coli_mla_expand leaves them: kv[..., :nope]
     and kv[..., nope:]).  lse may be None."""
     rc = _bind.prefill(_at(dims), q, k_nope, k_pe, v, cu_q, cu_k, max_q, causal, out, lse, ws, _handle(stream))
-    if rc != 1:
-        return _check(rc, "coli_mla_prefill")
-    d, dt, n, m = dims, _OF[dims.dtype], q.shape[0], k_nope.shape[0]
-    batch = cu_q.shape[0] - 1
-    _check(_lib.coli_mla_prefill(
-        ctypes.byref(d), batch, n, m, *_strided(q, dt, (n, d.n_heads, d.nope + COLI_MLA_ROPE), "q"),
-        *_strided(k_nope, dt, (m, d.n_heads, d.nope), "k_nope"), _arg(k_pe, dt, (m, COLI_MLA_ROPE), "k_pe"),
-        *_strided(v, dt, (m, d.n_heads, d.v_dim), "v"), _arg(cu_q, torch.int32, (batch + 1,), "cu_q"),
-        _arg(cu_k, torch.int32, (batch + 1,), "cu_k"), max_q, int(bool(causal)),
-        _arg(out, dt, (n, d.n_heads, d.v_dim), "out"),
-        None if lse is None else _arg(lse, torch.float32, (n, d.n_heads), "lse"), *_ws(ws),
-        _stream(stream, q)), "coli_mla_prefill")
+    if rc == _MISFIT:
+        no, d, dt = _Refused("coli_mla_prefill"), dims, _OF[dims.dtype]
+        n, m, batch = no.size(q, 3, 0, "q"), no.size(k_nope, 3, 0, "k_nope"), _sequences(no, cu_q, "cu_q")
+        no.view(q, dt, (n, d.n_heads, d.nope + COLI_MLA_ROPE), "q")
+        no.view(k_nope, dt, (m, d.n_heads, d.nope), "k_nope")
+        no.dense(k_pe, dt, (m, COLI_MLA_ROPE), "k_pe")
+        no.view(v, dt, (m, d.n_heads, d.v_dim), "v")
+        no.dense(cu_q, torch.int32, (batch + 1,), "cu_q")
+        no.dense(cu_k, torch.int32, (batch + 1,), "cu_k")
+        no.number(max_q, "max_q")
+        bool(causal)
+        no.dense(out, dt, (n, d.n_heads, d.v_dim), "out")
+        if lse is not None:
+            no.dense(lse, torch.float32, (n, d.n_heads), "lse")
+        no.workspace(ws)
+        no.end()
+    _check(rc, "coli_mla_prefill")

@@ -146,6 +146,36 @@ def test_append_in_place_and_without_queries():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("n,heads", [(1, 6), (9, 6), (9, 1)])
+def test_append_query_layouts(n, heads, monkeypatch):
+    """Rotated queries go to any layout whose runs of 64 lie apart, heads outermost too; others are refused."""
+    say("append layouts", n, heads)
+    m, g = q(), gen(5)
+    for entry in m.MLA_EXPORTS[2:]:   # the checks alone launch
+        monkeypatch.setattr(m._lib, entry, None)
+    d = dims(heads, 256, BF, page=16)
+    kv_a, freq, q_pe = randn(g, n, 320, dtype=BF), torch.rand(32, device="cuda", dtype=torch.float64), randn(g, n, heads, 64, dtype=BF)
+    positions, slots = torch.arange(n, device="cuda", dtype=torch.int32), torch.arange(n, device="cuda")
+    pages, ws = torch.zeros(2, 16, 320, dtype=BF, device="cuda"), workspace(d)
+
+    def run(out):
+        m.coli_mla_append(d, kv_a, None, positions, slots, freq, q_pe, out, pages, None, ws)
+        ok(ws)
+        return out
+    want = run(torch.empty(n, heads, 64, dtype=BF, device="cuda"))
+    assert torch.equal(run(torch.empty(heads, n, 64, dtype=BF, device="cuda").transpose(0, 1)), want)
+    assert torch.equal(run(torch.empty(heads, n + 3, 72, dtype=BF, device="cuda")[:, :n, :64].transpose(0, 1)), want)
+    assert torch.equal(run(torch.empty(n, heads, 192, dtype=BF, device="cuda")[..., 128:]), want)
+    if n * heads > 9:
+        for strides in ((0, 64), (64, 0), (64, 64), (8, 64 * 9)):
+            with pytest.raises(ValueError, match="overlap"):
+                run(torch.empty(heads * n * 64, dtype=BF, device="cuda").as_strided((n, heads, 64), (*strides, 1)))
+    empty = torch.empty(0, heads, 256, dtype=BF, device="cuda")
+    lens = torch.empty(0, dtype=torch.int32, device="cuda")
+    m.coli_mla_decode(d, empty, empty[..., :64].contiguous(), pages, None, torch.empty(0, 1, dtype=torch.int32, device="cuda"),
+                      lens, 5, empty, None, ws)
+
+
 def test_append_reports_a_slot_behind_the_cache():
     say("append bad slot")
     d = dims(1, 256, page=4)

@@ -165,3 +165,72 @@ def test_binding_refuses_what_does_not_fit():
     q.mla._distinct(torch.zeros(2, 5, 64), (320, 64), "o")
     q.mla._distinct(torch.zeros(2, 5, 192)[..., 128:], (960, 192), "o")
     q.mla._distinct(torch.zeros(5, 2, 64).transpose(0, 1), (64, 128), "o")
+
+
+class _On(torch.Tensor):
+    """A CPU tensor that says it is on a device."""
+    is_cuda = True
+
+    @property
+    def device(self):
+        return torch.device("cuda", getattr(self, "index", 0))
+
+
+def _on(index, *shape, dtype=torch.bfloat16):
+    t = torch.zeros(shape, dtype=dtype).as_subclass(_On)
+    t.index = index
+    return t
+
+
+def _device_calls(d, index):
+    """Arguments that fit, by entry point; `index` says the device of the tensor of that name, 0 for the others."""
+    i32, f32 = torch.int32, torch.float32
+
+    def t(name, *shape, dtype=torch.bfloat16):
+        return _on(index.get(name, 0), *shape, dtype=dtype)
+    pages, ws = t("pages", 4, 48, 576), t("ws", 1 << 20, dtype=torch.uint8)
+    return {
+        "append": (q.coli_mla_append, dict(
+            dims=d, kv_a=t("kv_a", 3, 576), norm_w=t("norm_w", 512), positions=t("positions", 3, dtype=i32),
+            slots=t("slots", 3, dtype=torch.int64), inv_freq=t("inv_freq", 32, dtype=torch.float64), q_pe=t("q_pe", 3, 5, 64),
+            q_pe_out=t("q_pe_out", 3, 5, 64), pages=pages, kv_scale=None, ws=ws)),
+        "project": (q.coli_mla_project, dict(x=t("x", 3, 5, 128), w=t("w", 5, 512, 128), out=t("out", 3, 5, 512))),
+        "decode": (q.coli_mla_decode, dict(
+            dims=d, q_lat=t("q_lat", 2, 5, 512), q_pe=t("q_pe", 2, 5, 64), pages=pages, kv_scale=None,
+            table=t("table", 2, 2, dtype=i32), kv_lens=t("kv_lens", 2, dtype=i32), max_kv=90, out=t("out", 2, 5, 512),
+            lse=t("lse", 2, 5, dtype=f32), ws=ws)),
+        "expand": (q.coli_mla_expand, dict(
+            dims=d, pages=pages, kv_scale=None, table=t("table", 2, 2, dtype=i32), cu_k=t("cu_k", 3, dtype=i32),
+            w=t("w", 5, 256, 512), kv=t("kv", 7, 5, 256), k_pe=t("k_pe", 7, 64), ws=ws)),
+        "prefill": (q.coli_mla_prefill, dict(
+            dims=d, q=t("q", 7, 5, 192), k_nope=t("k_nope", 9, 5, 128), k_pe=t("k_pe", 9, 64), v=t("v", 9, 5, 128),
+            cu_q=t("cu_q", 3, dtype=i32), cu_k=t("cu_k", 3, dtype=i32), max_q=5, causal=True, out=t("out", 7, 5, 128),
+            lse=t("lse", 7, 5, dtype=f32), ws=ws)),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(CALLS) + ["project"])
+def test_binding_refuses_tensors_of_two_devices(name, monkeypatch):
+    """Whatever the quick way refuses is refused, and never launched from here."""
+    launches = []
+    for entry in q.MLA_EXPORTS:
+        if entry not in ("coli_mla_row_bytes", "coli_mla_workspace_bytes"):
+            monkeypatch.setattr(q._lib, entry, lambda *a, entry=entry: launches.append(entry) or 0)
+    call, args = _device_calls(_dims(), {})[name]
+    tensors = [k for k, v in args.items() if isinstance(v, torch.Tensor)]
+    for odd in tensors:
+        call, args = _device_calls(_dims(), {odd: 1})[name]
+        with pytest.raises(ValueError, match="device cuda"):
+            call(**args, stream=0)
+    call, args = _device_calls(_dims(), {})[name]   # fits by what it says, though not for the quick way
+    with pytest.raises(ValueError, match="refused"):
+        call(**args, stream=0)
+    assert not launches
+
+
+def test_binding_refuses_numbers_past_32_bits():
+    for name, what in (("decode", "max_kv"), ("prefill", "max_q")):
+        call, args = _device_calls(_dims(), {})[name]
+        args[what] = (1 << 32) + 5
+        with pytest.raises(ValueError, match=what):
+            call(**args, stream=0)
