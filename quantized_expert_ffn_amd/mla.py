@@ -162,7 +162,13 @@ def _load_bind():
 
 
 _bind = _load_bind()
-_at = ctypes.addressof
+
+
+def _at(dims):
+    if not isinstance(dims, coli_mla_dims):
+        raise TypeError(f"dims: {type(dims).__name__}, expected coli_mla_dims")
+    return ctypes.addressof(dims)
+
 
 
 _MISFIT = 1   # the module's answer to arguments that do not fit

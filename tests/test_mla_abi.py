@@ -234,3 +234,11 @@ def test_binding_refuses_numbers_past_32_bits():
         args[what] = (1 << 32) + 5
         with pytest.raises(ValueError, match=what):
             call(**args, stream=0)
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_binding_takes_its_own_dims_only(name):
+    call, args = _device_calls(_dims(), {})[name]
+    for other in (ctypes.c_int32(5), q.coli_moe_dims(), None, 7):
+        with pytest.raises(TypeError, match="coli_mla_dims"):
+            call(**{**args, "dims": other}, stream=0)
