@@ -76,7 +76,11 @@ struct Args {
     }
     // a raw stream handle, or None for the device's current stream
     void *stream(int i) {
-        if (!none(i)) return reinterpret_cast<void *>(PyLong_AsSize_t(v[i]));
+        if (!none(i)) {
+            const size_t handle = PyLong_AsSize_t(v[i]);
+            if (handle == (size_t)-1 && PyErr_Occurred()) throw Misfit();
+            return reinterpret_cast<void *>(handle);
+        }
         return c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream();
     }
 };

@@ -174,8 +174,19 @@ def _at(dims):
 _MISFIT = 1   # the module's answer to arguments that do not fit
 
 
-def _handle(stream):
-    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
+def _handle(stream, t):
+    """A stream of t's device, or its raw handle, as a handle; None: the device's current one."""
+    if stream is None:
+        return None
+    if not isinstance(stream, int):
+        if not hasattr(stream, "cuda_stream"):
+            raise TypeError(f"stream: {type(stream).__name__}, expected a torch stream or a handle")
+        if isinstance(t, torch.Tensor) and stream.device != t.device:
+            raise ValueError(f"stream: of device {stream.device}, the tensors' is {t.device}")
+        return stream.cuda_stream
+    if not 0 <= stream < 2 ** 64:
+        raise ValueError(f"stream: {stream} is no handle")
+    return stream
 
 
 def _sequences(no, cu, what):
@@ -201,7 +212,7 @@ def coli_mla_workspace_bytes(dims, batch: int = 0, n_q: int = 1, max_kv: int = 0
 def coli_mla_append(dims, kv_a, norm_w, positions, slots, inv_freq, q_pe, q_pe_out, pages, kv_scale, ws, stream=None):
     """norm_w None: the latent is stored as it is.  q_pe and q_pe_out (both may be None): [n, n_heads, 64] views with
     strides of their own; they may be the same tensor."""
-    rc = _bind.append(_at(dims), kv_a, norm_w, positions, slots, inv_freq, q_pe, q_pe_out, pages, kv_scale, ws, _handle(stream))
+    rc = _bind.append(_at(dims), kv_a, norm_w, positions, slots, inv_freq, q_pe, q_pe_out, pages, kv_scale, ws, _handle(stream, kv_a))
     if rc == _MISFIT:
         no, d, dt = _Refused("coli_mla_append"), dims, _OF[dims.dtype]
         n = no.size(kv_a, 2, 0, "kv_a")
@@ -225,7 +236,7 @@ def coli_mla_append(dims, kv_a, norm_w, positions, slots, inv_freq, q_pe, q_pe_o
 def coli_mla_project(x, w, out, stream=None):
     """out[t, h] = w[h] x[t, h]: x [n, heads, n_in] (a view with strides of its own), w [heads, n_out, n_in], out
     [n, heads, n_out]."""
-    rc = _bind.project(x, w, out, _handle(stream))
+    rc = _bind.project(x, w, out, _handle(stream, x))
     if rc == _MISFIT:
         no = _Refused("coli_mla_project")
         n, heads, n_in, n_out = *(no.size(x, 3, i, "x") for i in range(3)), no.size(w, 3, 1, "w")
@@ -240,7 +251,7 @@ def coli_mla_project(x, w, out, stream=None):
 
 def coli_mla_decode(dims, q_lat, q_pe, pages, kv_scale, table, kv_lens, max_kv, out, lse, ws, stream=None):
     """q_lat [batch * n_q, n_heads, rank]; the batch is kv_lens'.  lse may be None."""
-    rc = _bind.decode(_at(dims), q_lat, q_pe, pages, kv_scale, table, kv_lens, max_kv, out, lse, ws, _handle(stream))
+    rc = _bind.decode(_at(dims), q_lat, q_pe, pages, kv_scale, table, kv_lens, max_kv, out, lse, ws, _handle(stream, q_lat))
     if rc == _MISFIT:
         no, d, dt = _Refused("coli_mla_decode"), dims, _OF[dims.dtype]
         batch, rows = no.size(kv_lens, 1, 0, "kv_lens"), no.size(q_lat, 3, 0, "q_lat")
@@ -261,7 +272,7 @@ def coli_mla_decode(dims, q_lat, q_pe, pages, kv_scale, table, kv_lens, max_kv, 
 
 
 def coli_mla_expand(dims, pages, kv_scale, table, cu_k, w, kv, k_pe, ws, stream=None):
-    rc = _bind.expand(_at(dims), pages, kv_scale, table, cu_k, w, kv, k_pe, ws, _handle(stream))
+    rc = _bind.expand(_at(dims), pages, kv_scale, table, cu_k, w, kv, k_pe, ws, _handle(stream, kv))
     if rc == _MISFIT:
         no, d, dt, wide = _Refused("coli_mla_expand"), dims, _OF[dims.dtype], dims.nope + dims.v_dim
         n, batch = no.size(kv, 3, 0, "kv"), _sequences(no, cu_k, "cu_k")
@@ -279,7 +290,7 @@ def coli_mla_expand(dims, pages, kv_scale, table, cu_k, w, kv, k_pe, ws, stream=
 def coli_mla_prefill(dims, q, k_nope, k_pe, v, cu_q, cu_k, max_q, causal, out, lse, ws, stream=None):
     """q, k_nope and v are views with strides of their own (k_nope and v as coli_mla_expand leaves them: kv[..., :nope]
     and kv[..., nope:]).  lse may be None."""
-    rc = _bind.prefill(_at(dims), q, k_nope, k_pe, v, cu_q, cu_k, max_q, causal, out, lse, ws, _handle(stream))
+    rc = _bind.prefill(_at(dims), q, k_nope, k_pe, v, cu_q, cu_k, max_q, causal, out, lse, ws, _handle(stream, q))
     if rc == _MISFIT:
         no, d, dt = _Refused("coli_mla_prefill"), dims, _OF[dims.dtype]
         n, m, batch = no.size(q, 3, 0, "q"), no.size(k_nope, 3, 0, "k_nope"), _sequences(no, cu_q, "cu_q")

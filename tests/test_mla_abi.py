@@ -242,3 +242,15 @@ def test_binding_takes_its_own_dims_only(name):
     for other in (ctypes.c_int32(5), q.coli_moe_dims(), None, 7):
         with pytest.raises(TypeError, match="coli_mla_dims"):
             call(**{**args, "dims": other}, stream=0)
+
+
+@pytest.mark.parametrize("name", sorted(CALLS) + ["project"])
+def test_binding_refuses_streams_that_do_not_fit(name):
+    """A handle is an address; a stream is the tensors' device's."""
+    call, args = _device_calls(_dims(), {})[name]
+
+    class Other:
+        cuda_stream, device = 7, torch.device("cuda", 1)
+    for bad, error in ((-5, ValueError), (1 << 70, ValueError), (Other(), ValueError), ("7", TypeError), (1.5, TypeError)):
+        with pytest.raises(error, match="stream"):
+            call(**args, stream=bad)
