@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libcolimoe.so")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
-        f"{LIB_PATH} is missing: build it with `python -m quantized_expert_ffn_amd.build` "
+        f"{LIB_PATH} is missing: build it with `python quantized_expert_ffn_amd/build.py` "
         "(or __graft_entry__.build()); the MoE layer has no non-HIP implementation")
 
 # torch's HIP runtime is loaded first, so that the library's libamdhip64.so.7

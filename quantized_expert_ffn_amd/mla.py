@@ -151,17 +151,24 @@ def _distinct(t, strides, what):
         raise ValueError(f"{what}: strides overlap")
 
 
-def _load_bind():
-    path = os.path.join(os.path.dirname(LIB_PATH), "_mla_bind.so")
-    if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: build it with `python -m quantized_expert_ffn_amd.build`")
-    spec = importlib.util.spec_from_file_location("_mla_bind", path)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
-    return mod
+class _Bind:
+    """csrc/mla_bind.cpp's module, loaded by its first call: it is built against torch's headers, and the rest of the
+    package does without it."""
+
+    def __getattr__(self, name):
+        global _bind
+        path = os.path.join(os.path.dirname(LIB_PATH), "_mla_bind.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with `python quantized_expert_ffn_amd/build.py` "
+                              "(or __graft_entry__.build())")
+        spec = importlib.util.spec_from_file_location("_mla_bind", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        _bind = mod
+        return getattr(mod, name)
 
 
-_bind = _load_bind()
+_bind = _Bind()
 
 
 def _at(dims):

@@ -254,3 +254,27 @@ def test_binding_refuses_streams_that_do_not_fit(name):
     for bad, error in ((-5, ValueError), (1 << 70, ValueError), (Other(), ValueError), ("7", TypeError), (1.5, TypeError)):
         with pytest.raises(error, match="stream"):
             call(**args, stream=bad)
+
+
+def test_the_package_stands_without_the_attention_module(tmp_path):
+    """The MoE layer needs the library alone; attention says what is missing and how to build it, by a command that works
+    where the package does not import."""
+    import shutil
+    import subprocess
+    import sys
+    pkg = os.path.join(ROOT, "quantized_expert_ffn_amd")
+    copy = tmp_path / "quantized_expert_ffn_amd"
+    shutil.copytree(pkg, copy, ignore=shutil.ignore_patterns("csrc", "__pycache__", "*.o", "_mla_bind.so"))
+    code = ("import torch, quantized_expert_ffn_amd as q\n"
+            "assert not q.coli_moe_last_error() and q.coli_mla_row_bytes(q.make_mla_dims(1, 512, 128, 128, 16)) == 1152\n"
+            "try:\n    q.coli_mla_project(torch.zeros(1, 1, 64), torch.zeros(1, 64, 64), torch.zeros(1, 1, 64))\n"
+            "except ImportError as e:\n    print(e)\n")
+    run = lambda: subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
+    r = run()
+    assert r.returncode == 0, r.stderr
+    os.remove(copy / "_build" / "libcolimoe.so")
+    gone = run()
+    assert gone.returncode != 0
+    for text in (r.stdout, gone.stderr):
+        named = re.search(r"`python (\S+)`", text)
+        assert named and os.path.samefile(os.path.join(ROOT, named.group(1)), os.path.join(pkg, "build.py")), text
