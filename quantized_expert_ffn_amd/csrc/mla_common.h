@@ -45,8 +45,4 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ float fp8_to_f32(uint32_t code) {
-    return __builtin_amdgcn_cvt_f32_fp8((int)code, 0);
-}
-
 }  // namespace coli

@@ -159,9 +159,6 @@ __device__ __forceinline__ void load_to_lds_from(const void *base, uint32_t at, 
 
 // A value that is the same in every lane, as a scalar.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int64_t uniform64(int64_t v) {
-    return ((int64_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)v);
-}
 
 // Waits until at most N of the wavefront's vector-memory operations are out.
 template <int N>
