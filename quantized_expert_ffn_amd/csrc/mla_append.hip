@@ -97,7 +97,11 @@ __global__ __launch_bounds__(APPEND_THREADS) void k_mla_append(MlaAppendArgs a) 
             for (int i = 0; i < PER; i += 4) {
                 float q[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) q[j] = s > 0.0f ? v[i + j] / s : 0.0f;
+                for (int j = 0; j < 4; ++j) {
+                    q[j] = s > 0.0f ? v[i + j] / s : 0.0f;
+                    // a scale below the normal numbers is so coarse that quotients pass the largest code (NaN stays)
+                    if (fabsf(q[j]) > 448.0f) q[j] = copysignf(448.0f, q[j]);
+                }
                 int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
                 code[i / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
             }

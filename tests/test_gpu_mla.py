@@ -207,6 +207,22 @@ def test_append_keeps_a_nan_visible():
         assert lat[0].isnan().all() and not lat[1].isnan().any()
 
 
+def test_append_scale_below_the_normal_numbers():
+    """E4M3: a scale so small that its own rounding brings codes past 448, the largest (values of 655 steps of binary32's
+    subnormals, a scale of 1.46 of them)."""
+    say("append small scale")
+    d = dims(1, 256, BF, True, page=4, eps=1e4)
+    pages, scale, ws = torch.zeros(2, 4, 384, dtype=torch.uint8, device="cuda"), torch.zeros(8, device="cuda"), workspace(d)
+    kv_a, gain = torch.ones(3, 320, dtype=BF, device="cuda"), torch.full((256,), 2.0 ** -133, dtype=BF, device="cuda")
+    kv_a[1] = -1
+    kv_a[2, 7] = NAN
+    q().coli_mla_append(d, kv_a, gain, torch.zeros(3, device="cuda", dtype=torch.int32), torch.arange(3, device="cuda"),
+                        torch.zeros(32, device="cuda", dtype=torch.float64), None, None, pages, scale, ws)
+    ok(ws)
+    lat, _ = ref.rows_of(pages, scale, 256, BF)
+    assert (lat[0] == 448 * 2.0 ** -149).all() and (lat[1] == -448 * 2.0 ** -149).all() and lat[2].isnan().all()
+
+
 # ---------------------------------------------------------------- project
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("n,heads,n_in,n_out", [
