@@ -27,13 +27,14 @@ constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 // of two: weights then reach 2^8 (binary16, lifted by 2^7: 2^15), which both
 // types hold, and most tiles spare the pass over the accumulators.
 constexpr float MAX_LAG = 8.0f;
-//
+
 // E4M3 tokens have a scale each, f 2^e with 1/2 <= |f| < 1, and what is rounded
 // to 16 bits is weight times scale.  That product has a reference of its own,
 // the row's largest 2^{score + e} so far, lagging alike: a token whose scale is
 // far above the others' takes their bits only as far as its weight lets it
-// count, and one that a row does not see takes none.  f stays outside the
-// exponent and the reference is a whole number, so that e costs no precision.
+// count, and one that a row does not see takes none.  The scale's exponent costs
+// one rounding, of score + e; f stays outside, and the reference is a whole
+// number, so that subtracting it costs none.
 
 // Four wavefronts: RG groups of 32 rows, each of CG = 4 / RG wavefronts that
 // share the output's columns.  Wavefronts 0 and 1 of a group score half of a
@@ -346,24 +347,18 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
             }
             if (tile + 1 == hi && it + 1 < total) touch_q(seq + 1);
             f32x16 s;
-            float sc[16], sum = 0.0f;   // E4M3: scales, from the scores on their fractions
-            auto exponents = [&](int q) { return lds_read<f32x4>(D::L_EXP + 16 * hf + 4 * (buf * DEC_TILE + 32 * th), 32 * q); };
+            float sum = 0.0f;
+            float sc[16], sv[16];   // E4M3: scales, from the scores on their fractions; score + exponent
             auto weigh = [&] {
                 const float ref = m == NEG ? 0.0f : m, refv = mv == NEG ? 0.0f : mv;
                 x8<T> p[2];
                 sum = 0.0f;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    f32x4 e;
-                    if (FP8) e = exponents(q);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 4 * q + i;
-                        float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale, -ref));
-                        sum += w;
-                        if (FP8) w = sc[r] * __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale, e[i] - refv));
-                        p[r >> 3][r & 7] = (T)w;
-                    }
+                for (int r = 0; r < 16; ++r) {
+                    float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale, -ref));
+                    sum += w;
+                    if (FP8) w = sc[r] * __builtin_amdgcn_exp2f(sv[r] - refv);
+                    p[r >> 3][r & 7] = (T)w;
                 }
                 lds_write(p_at, p[0], 0);
                 lds_write(p_at, p[1], 1024);
@@ -436,11 +431,11 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
                     float topv = NEG;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const f32x4 e = exponents(q);
+                        const f32x4 e = lds_read<f32x4>(D::L_EXP + 16 * hf + 4 * (buf * DEC_TILE + 32 * th), 32 * q);
 #pragma unroll
-                        for (int i = 0; i < 4; i += 2)
-                            topv = fmaxf(fmaxf(topv, __builtin_fmaf(s[4 * q + i], scale, e[i])),
-                                         __builtin_fmaf(s[4 * q + i + 1], scale, e[i + 1]));
+                        for (int i = 0; i < 4; ++i) sv[4 * q + i] = __builtin_fmaf(s[4 * q + i], scale, e[i]);
+                        topv = fmaxf(fmaxf(topv, sv[4 * q]), sv[4 * q + 1]);
+                        topv = fmaxf(fmaxf(topv, sv[4 * q + 2]), sv[4 * q + 3]);
                     }
                     topv = half_max(topv);
                     lds_write<float>(top_at + D::TOPS + 128 * th, topv);
