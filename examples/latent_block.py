@@ -60,17 +60,18 @@ class Block:
     def _empty(self, *shape, dtype=None):
         return torch.empty(shape, dtype=dtype or self.dtype, device="cuda")
 
-    def _append(self, x):
-        """Queries of x's tokens, rotated in place; their latents and keys go into the cache."""
+    def _append(self, x, apart: bool):
+        """Queries of x's tokens and their rotated part, in place or apart; their latents and keys go into the cache."""
         n = x.shape[0]
         h = norm(x).to(self.dtype)
         q = (h @ self.w_q.t()).view(n, HEADS, NOPE + ROPE)
         at = torch.arange(self.length, self.length + n, device="cuda")
         slots = self.table[0].long()[at // PAGE] * PAGE + at % PAGE
+        q_pe = self._empty(n, HEADS, ROPE) if apart else q[..., NOPE:]
         moe.coli_mla_append(self.dims, h @ self.w_kv_a.t(), self.gain, at.to(torch.int32), slots, self.inv_freq,
-                            q[..., NOPE:], q[..., NOPE:], self.pages, self.kv_scale, self.ws)
+                            q[..., NOPE:], q_pe, self.pages, self.kv_scale, self.ws)
         self.length += n
-        return q
+        return q, q_pe
 
     def _finish(self, x, attended):
         """Output projection and residual, then the MoE layer and its residual."""
@@ -85,7 +86,7 @@ class Block:
 
     def prompt(self, x):
         n = x.shape[0]
-        q = self._append(x)
+        q, _ = self._append(x, apart=False)   # prefill takes whole queries
         kv, k_pe = self._empty(self.length, HEADS, NOPE + V), self._empty(self.length, ROPE)
         cu_q = torch.tensor([0, n], dtype=torch.int32, device="cuda")
         cu_k = torch.tensor([0, self.length], dtype=torch.int32, device="cuda")
@@ -96,12 +97,12 @@ class Block:
 
     def step(self, x):
         """One token."""
-        q = self._append(x)
+        q, q_pe = self._append(x, apart=True)   # decode takes the parts
         q_lat, o_lat, out = self._empty(1, HEADS, RANK), self._empty(1, HEADS, RANK), self._empty(1, HEADS, V)
         lens = torch.tensor([self.length], dtype=torch.int32, device="cuda")
         moe.coli_mla_project(q[..., :NOPE], self.w_k_t, q_lat)
-        moe.coli_mla_decode(self.dims, q_lat, q[..., NOPE:].contiguous(), self.pages, self.kv_scale, self.table, lens,
-                            self.limit, o_lat, None, self.ws)
+        moe.coli_mla_decode(self.dims, q_lat, q_pe, self.pages, self.kv_scale, self.table, lens, self.limit, o_lat, None,
+                            self.ws)
         moe.coli_mla_project(o_lat, self.w_v, out)
         return self._finish(x, out)
 
