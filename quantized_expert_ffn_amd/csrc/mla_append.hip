@@ -10,8 +10,8 @@
 // sixteen values (eight pairs) a thread.
 //
 // What bounds it: bytes, of which the queries' are the most: 8191 tokens, 64
-// heads, E4M3 latents: 27 us and 149 MB, 5.5 TB/s, from a warm cache, 36 us
-// from a cold one; one token: 2.9 us.
+// heads, E4M3 latents: 26 us and 149 MB, 5.7 TB/s, from a warm cache, 36 us
+// from a cold one; one token: 2.7 us.
 #include "mla_common.h"
 
 namespace coli {

@@ -7,14 +7,16 @@
 // one [tokens] x [rank], of the same cached tile: read from memory once, used
 // twice from LDS.
 //
-// What bounds it: up to 64 rows the cached bytes (131071 tokens, 64 heads,
-// rank 512, bf16: 151 MB; 34.4 us and 9.8 us for the join, 4.4 TB/s in the
-// first); from 128 rows on a tile's own chain of scores, softmax and values,
+// What bounds it: up to 64 rows the cached bytes, and that a CU has no load out
+// from a tile's end, which waits for all, until the next tile's scores (131071
+// tokens, 64 heads, rank 512, bf16: 151 MB; 44 us and 12 us for the join from
+// memory, 3.5 TB/s in the first; 33 and 9.5 where the last-level cache holds
+// them); from 128 rows on a tile's own chain of scores, softmax and values,
 // which one wavefront a SIMD runs through without overlap (registers: 144 of
 // queries and 128 of accumulators): a four-token verify of 64 heads over
-// 115700 E4M3 tokens takes 82 us and 9.4 us, 0.70 PFLOP/s, matrix cores 35%
-// busy; reads from LDS, widening, softmax, loads and page bookkeeping each
-// account for 5 to 7 us of it.
+// 115700 E4M3 tokens takes 84.5 us and 9.6 us, 0.67 PFLOP/s, matrix cores 33%
+// busy; reads from LDS, widening, softmax, loads and page bookkeeping, each
+// taken out alone, saved 5 to 7 us.
 #include "kernels.h"
 #include "mla_mfma.h"
 
@@ -40,8 +42,9 @@ constexpr float MAX_LAG = 8.0f;
 // share the output's columns.  Wavefronts 0 and 1 of a group score half of a
 // tile's tokens each and hand their weights to the others through LDS.  Whole
 // columns for a wavefront would spare that exchange, but 256 registers of
-// accumulators beside 144 of queries spilled 330 and more; one row group of 64
-// columns' quarters would read every tile from LDS four times.
+// accumulators beside 144 of queries spilled 330 and more.  Not built: eight
+// wavefronts, a quarter of the columns and half of each score's sum apiece,
+// which would read LDS as much as this in half the registers.
 template <class T_, int RANK_, bool FP8_, int RG_>
 struct Dec {
     using T = T_;

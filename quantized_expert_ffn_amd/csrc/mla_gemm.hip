@@ -11,12 +11,14 @@
 // was used last, to leave in whole lines.
 //
 // What bounds it: expand of 8192 rows, 64 heads, rank 512, 192 + 256 features,
-// bf16: 239 us, 1.0 PFLOP/s and 470 MB written; without its loads it takes 174
-// us, with one product in eight 167: a step's loads are out for about one
-// step, and LDS serves them beside 0.75 KiB of operands a product (128 x 128 a
-// wavefront would read 0.5, and spills; 128 x 96 takes 300 us).  Stores that
-// pass L2 by took it there from 275 us, 216 of them without any store.  Project is bound by its bytes: 133 tokens, 128 heads, 512 -> 128,
-// fp16: 8.2 us, 4.7 TB/s; one token, 64 heads, 192 -> 512, bf16: 4.0 us.
+// bf16: 236 us, 1.0 PFLOP/s and 470 MB written.  A build of 239 us took 174
+// without its loads and 167 with one product in eight: with two stages a step
+// waits for all of them, and they have been out for one step.  LDS serves them
+// beside 0.75 KiB of operands a product (128 x 128 a wavefront would read 0.5,
+// and spills; 128 x 96 takes 300 us).  Stores that
+// pass L2 by took it there from 275 us, 216 of them without any store.  Project
+// is bound by its bytes: 133 tokens, 128 heads, 512 -> 128, fp16: 8.2 us, 4.7
+// TB/s; one token, 64 heads, 192 -> 512, bf16: 4.1 us.
 #include "kernels.h"
 #include "mla_mfma.h"
 
@@ -327,10 +329,15 @@ hipError_t expand_by_size(const MlaExpandArgs &a, int rank, hipStream_t st) {
 // tokens (160 tiles): 6.7 us against 8.5; 64 heads, 512 -> 256, 100 tokens
 // (512): 8.2 against 8.7, 200 tokens (896): 12.6 against 9.7.  256 x 256 needs
 // long sums and tiles for most CUs: 64 heads, 512 -> 256, 600 tokens (192
-// tiles): 19.8 against 21.8, 4096 tokens: 103 against 131; 16 heads of those,
-// 2048 tokens (128 tiles): 19.1 against 13.9; 64 heads, 192 -> 512, 4096
-// tokens: 130 against 100.  128 heads, 128 -> 512 gain by it at 8000 tokens
-// (395 against 376) and lose at 8192 (353 against 437).
+// tiles): 19.8 against 21.8, 4096 tokens: 133 against 159; 16 heads of those,
+// 2048 tokens (128 tiles): 17.2 against 11.9, 3000 tokens (192): 19.5 against
+// 20.8.  From 192 sums on down it loses more than it gains, at 1024 to 16384
+// tokens: 64 heads, 192 -> 512: 10 to 30% slower at eight of ten lengths, 3%
+// faster at best; 128 heads of those: 9% faster to 10% slower at nine, 21%
+// faster at 8192; 64 heads, 128 -> 512: 5 to 29% slower; 128 heads of those: 1%
+// faster to 11% slower at nine, but 351 against 440 us at 8192, a length at
+// which the smaller tiles are slow for a reason not found (8000 tokens: 369,
+// 12000: 556).
 hipError_t launch_mla_project(const MlaProjectArgs &a, int dtype, hipStream_t st) {
     return mla_with_type(dtype, [&](auto t) {
         using T = decltype(t);

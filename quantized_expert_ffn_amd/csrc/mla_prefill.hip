@@ -5,15 +5,15 @@
 // over the keys j that query i sees, in one pass with the running maximum and
 // sum of the softmax.
 //
-// What bounds it: the matrix cores at the clock they are left with.  8192
-// tokens, 64 heads, widths 192 + 64 and 256, bf16, causal: 1.91 ms, 1.15
-// PFLOP/s, 0.82 of what a large library product of the same type reaches on
-// the card; counters: matrix cores 63% busy at 1.74 GHz, LDS 32%, hardly a
-// bank conflict.  An earlier 1.94 ms became 1.72 without the loads after the
-// first tiles and 1.85 without the exponentials.  Short calls are bound by the
-// chain of a tile: ragged prompts of up to 513 queries over 1500 keys, 32
-// heads, widths 128 + 64 and 128, fp16: 41 us, 24 tiles in a row for the
-// longest.
+// What bounds it: no one part.  8192 tokens, 64 heads, widths 192 + 64 and 256,
+// bf16, causal: 1.94 ms, 1.14 PFLOP/s, 0.81 of what a large library product of
+// the same type reaches on the card (two runs of the same code: 1.94 and 1.97;
+// single kernels under a profiler 2.0 to 2.17); counters: matrix cores 62% busy,
+// LDS 31%, hardly a bank conflict, wavefronts waiting 30% of their time.  A
+// build of 1.94 ms took 1.72 without the loads after the first tiles and 1.85
+// without the exponentials.  Short calls are bound by the chain of a tile:
+// ragged prompts of up to 513 queries over 1500 keys, 32 heads, widths 128 + 64
+// and 128, fp16: 36 us, 24 tiles in a row for the longest.
 #include "kernels.h"
 #include "mla_mfma.h"
 
