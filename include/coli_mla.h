@@ -42,9 +42,6 @@
 extern "C" {
 #endif
 
-#define COLI_BF16 0
-#define COLI_FP16 1
-
 /* coli_mla_dims.kv_format: one cached token is a row of
  *   COLI_KV_PLAIN  rank + 64 values of dtype: latent, rotated key
  *   COLI_KV_E4M3   rank E4M3 codes (OCP, bytes), then 64 values of dtype;
@@ -135,6 +132,34 @@ int coli_mla_decode(const coli_mla_dims *dims, int32_t batch, int32_t n_q, const
                     const void *pages, const float *kv_scale, int32_t n_pages, const int32_t *table,
                     int32_t table_width, const int32_t *kv_lens, int32_t max_kv, void *out, float *lse, void *ws,
                     size_t ws_bytes, void *stream);
+
+/* Most query rows of a coli_mla_decode_shared call (batch * n_q * n_heads). */
+#define COLI_MLA_MAX_SHARED_ROWS (1 << 20)
+
+/* Workspace for coli_mla_decode_shared calls of up to these sizes.  0 when an
+ * argument is invalid. */
+size_t coli_mla_shared_workspace_bytes(const coli_mla_dims *dims, int32_t batch, int32_t n_q, int32_t prefix_len,
+                                       int32_t max_kv);
+
+/*
+ * coli_mla_decode for sequences that begin with the same cached tokens:
+ * sequence b is the prefix_len tokens of prefix_table, then kv_lens[b] tokens
+ * of its own in its pages of table.  The prefix is read once for the rows of
+ * all sequences.  The n_q new tokens are the last of the whole sequence:
+ * query j sees its first prefix_len + kv_lens[b] - n_q + 1 + j tokens (a
+ * sequence of fewer own tokens than n_q has some of them in the prefix), and
+ * one that sees none gets zeros and lse = -inf.
+ *   prefix_table  device int32 [prefix_width]: page ids of the prefix, in order, prefix_width * page_size >=
+ *                 prefix_len; may be NULL with prefix_len = 0
+ *   prefix_len    host; 0 is coli_mla_decode
+ *   max_kv        host bound of kv_lens; 0: no sequence has tokens of its own
+ * Other arguments as for coli_mla_decode; batch * n_q * n_heads at most COLI_MLA_MAX_SHARED_ROWS.
+ */
+int coli_mla_decode_shared(const coli_mla_dims *dims, int32_t batch, int32_t n_q, const void *q_lat, const void *q_pe,
+                           const void *pages, const float *kv_scale, int32_t n_pages, const int32_t *prefix_table,
+                           int32_t prefix_width, int32_t prefix_len, const int32_t *table, int32_t table_width,
+                           const int32_t *kv_lens, int32_t max_kv, void *out, float *lse, void *ws, size_t ws_bytes,
+                           void *stream);
 
 /*
  * Keys and values of every head out of the paged latents, for a ragged

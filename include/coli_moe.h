@@ -61,6 +61,17 @@ extern "C" {
 /* the debug hooks' `bits` value selecting MXFP4 codes */
 #define COLI_MXFP4 (-4)
 
+/* element types of activations, logits and results (where a call takes several) */
+#define COLI_BF16 0
+#define COLI_FP16 1
+#define COLI_F32 2
+
+/* coli_select_dims.scoring and .group_score */
+#define COLI_SCORE_SIGMOID 0
+#define COLI_SCORE_SOFTMAX 1
+#define COLI_GROUP_MAX 0        /* a group's best choice */
+#define COLI_GROUP_TOP2 1       /* the sum of its two best */
+
 /* Most tokens one call takes (n_tokens, max_tokens): the workspace's int32
  * pair and unit counts stay far from overflow below it.  Larger batches are
  * split by the caller; COLI_EINVAL (0 from coli_moe_workspace_bytes)
@@ -143,6 +154,42 @@ size_t coli_moe_workspace_bytes(const coli_moe_dims *dims, int32_t max_tokens);
 int coli_moe_route(const coli_moe_dims *dims, int32_t n_tokens, const float *x,
                    const float *router_w, const float *router_bias, int32_t *topk_idx,
                    float *topk_w, void *ws, size_t ws_bytes, void *stream);
+
+/* Shape of coli_moe_select.  All fields are checked on every call. */
+typedef struct coli_select_dims {
+    int32_t n_experts;            /* E: 1..1024 */
+    int32_t top_k;                /* K: 1..min(32, experts of topk_group groups) */
+    int32_t n_group;              /* groups of E / n_group experts in order: a divisor of E, 1..64 */
+    int32_t topk_group;           /* groups a token may choose from: 1..n_group */
+    int32_t scoring;              /* COLI_SCORE_SIGMOID or COLI_SCORE_SOFTMAX */
+    int32_t group_score;          /* COLI_GROUP_MAX or COLI_GROUP_TOP2 */
+    int32_t norm_topk_prob;       /* 1: weights renormalised over the K selected */
+    float routed_scaling_factor;  /* multiplies the weights; finite */
+} coli_select_dims;
+
+/*
+ * Routing from a gate's logits, in the forms coli_moe_route does not have:
+ *   score  = sigmoid(l), or softmax(l) over the E experts
+ *   choice = score + bias (the bias ranks only)
+ *   a token keeps the topk_group groups of highest group_score over their
+ *   choices, then the K experts of highest choice in them; ties go to the
+ *   lower group and the lower expert
+ *   w_k    = score_k, over the K's sum if norm_topk_prob, times
+ *            routed_scaling_factor; in rank order
+ * Results feed coli_moe_forward.
+ *   logits    device [n_tokens, E] of dtype (COLI_BF16, COLI_FP16, COLI_F32), at token_stride (elements)
+ *   bias      device f32 [E] or NULL (zeros)
+ *   topk_idx  device int32 [n_tokens, K], topk_w device f32 [n_tokens, K]
+ *   ws        at least 256 bytes, zero-filled once: a workspace of this
+ *             library's, of which the call uses the status word
+ * Experts are chosen as in 64 bits: two choices that binary32 cannot tell
+ * apart are ranked by what they are.  Weights are rounded once.  Non-finite
+ * logits, bias or weights set COLI_ENONFINITE in the status word; indices are
+ * distinct and in range all the same.
+ */
+int coli_moe_select(const coli_select_dims *dims, int32_t n_tokens, int32_t dtype, const void *logits,
+                    int64_t token_stride, const float *bias, int32_t *topk_idx, float *topk_w, void *ws,
+                    size_t ws_bytes, void *stream);
 
 /*
  * Expert FFNs and combine for n_tokens tokens with given routing (README

@@ -30,6 +30,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 COLI_OK, COLI_EINVAL, COLI_ENONFINITE, COLI_EHIP, COLI_ENOTRESIDENT, COLI_EWORKSPACE = 0, -1, -2, -3, -4, -5
 COLI_WFMT_INT, COLI_WFMT_MXFP4, COLI_MXFP4 = 0, 1, -4
+COLI_SCORE_SIGMOID, COLI_SCORE_SOFTMAX, COLI_GROUP_MAX, COLI_GROUP_TOP2 = 0, 1, 0, 1
 COLI_MAX_TOKENS = 65536  # most tokens one call takes
 
 EXPORTS = (
@@ -40,7 +41,7 @@ EXPORTS = (
     "coli_moe_debug_force_path", "coli_moe_layer", "coli_moe_debug_mfma_i8",
     "coli_moe_roof_sink_words", "coli_moe_roof_stream_read", "coli_moe_roof_mfma_i8",
     "coli_moe_layer_noalloc", "coli_moe_debug_mfma_f8f6f4", "coli_moe_debug_route_wait",
-    "coli_moe_debug_mfma_i8_16",
+    "coli_moe_debug_mfma_i8_16", "coli_moe_select",
 )
 
 KIND_ROUTER_LOGITS, KIND_ROUTER_SELECT, KIND_GATEUP, KIND_DOWN, KIND_COMBINE = 0, 1, 2, 3, 4
@@ -54,6 +55,14 @@ class coli_moe_dims(ctypes.Structure):
         ("top_k", ctypes.c_int32), ("n_shared", ctypes.c_int32), ("wbits", ctypes.c_int32),
         ("routed_scaling_factor", ctypes.c_float), ("norm_topk_prob", ctypes.c_int32),
         ("group_size", ctypes.c_int32), ("wformat", ctypes.c_int32),
+    ]
+
+
+class coli_select_dims(ctypes.Structure):
+    _fields_ = [
+        ("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+        ("scoring", ctypes.c_int32), ("group_score", ctypes.c_int32), ("norm_topk_prob", ctypes.c_int32),
+        ("routed_scaling_factor", ctypes.c_float),
     ]
 
 
@@ -92,6 +101,8 @@ _sigs = {
     "coli_moe_roof_sink_words": (_SZ, []),
     "coli_moe_roof_stream_read": (ctypes.c_int, [_P, _SZ, _P, _P]),
     "coli_moe_roof_mfma_i8": (ctypes.c_int, [_I32, _P, _P]),
+    "coli_moe_select": (ctypes.c_int, [ctypes.POINTER(coli_select_dims), _I32, _I32, _P, ctypes.c_int64, _P, _P, _P, _P, _SZ,
+                                       _P]),
     "coli_moe_layer_noalloc": (ctypes.c_int, [_D, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
 }
 for _name, (_res, _args) in _sigs.items():
@@ -106,6 +117,13 @@ def make_dims(spec) -> coli_moe_dims:
     return coli_moe_dims(int(spec.hidden), int(spec.inter), int(spec.n_experts), int(spec.top_k),
                          int(spec.n_shared), int(spec.wbits), float(spec.routed_scaling_factor),
                          int(spec.norm_topk_prob), int(getattr(spec, "group", 0)), int(getattr(spec, "fmt", 0)))
+
+
+def make_select_dims(n_experts: int, top_k: int, n_group: int = 1, topk_group: int = 1, scoring: int = COLI_SCORE_SIGMOID,
+                     group_score: int = COLI_GROUP_TOP2, norm_topk_prob: bool = True,
+                     routed_scaling_factor: float = 1.0) -> coli_select_dims:
+    return coli_select_dims(n_experts, top_k, n_group, topk_group, scoring, group_score, int(norm_topk_prob),
+                            routed_scaling_factor)
 
 
 def _dims(d):
@@ -189,6 +207,27 @@ def coli_moe_route(dims, x, router_w, router_bias, topk_idx, topk_w, ws, stream=
         _dev(router_bias, torch.float32, "router_bias"), _dev(topk_idx, torch.int32, "topk_idx"),
         _dev(topk_w, torch.float32, "topk_w"), _dev(ws, torch.uint8, "ws"), _nbytes(ws),
         _stream(stream)), "coli_moe_route")
+
+
+def coli_moe_select(dims, logits, bias, topk_idx, topk_w, ws, stream=None):
+    """Routing from logits [tokens, n_experts] of bfloat16, float16 or float32, rows at a stride of their own; dims from
+    make_select_dims; bias float32 [n_experts] or None; ws any workspace of this package.  The checks run in the CPython
+    module beside the library; what does not fit there is named here."""
+    if not isinstance(dims, coli_select_dims):
+        raise TypeError(f"dims: {type(dims).__name__}, expected coli_select_dims")
+    rc = mla._bind.select(ctypes.addressof(dims), logits, bias, topk_idx, topk_w, ws, mla._handle(stream, logits))
+    if rc == mla._MISFIT:
+        import torch
+        no = mla._Refused("coli_moe_select")
+        n = no.size(logits, 2, 0, "logits")
+        no.rows(logits, (torch.bfloat16, torch.float16, torch.float32), (n, dims.n_experts), "logits")
+        if bias is not None:
+            no.dense(bias, torch.float32, (dims.n_experts,), "bias")
+        no.dense(topk_idx, torch.int32, (n, dims.top_k), "topk_idx")
+        no.dense(topk_w, torch.float32, (n, dims.top_k), "topk_w")
+        no.workspace(ws)
+        no.end()
+    _check(rc, "coli_moe_select")
 
 
 def coli_moe_forward(dims, x, topk_idx, topk_w, expert_blobs, shared_blob, out, ws,
@@ -366,6 +405,12 @@ def coli_moe_roof_mfma_i8(iters: int, sink, stream=None):
 
 # ---------------------------------------------------------------- latent attention
 from .mla import (  # noqa: E402,F401
-    COLI_BF16, COLI_FP16, COLI_KV_E4M3, COLI_KV_PLAIN, COLI_MLA_MAX_BATCH, COLI_MLA_MAX_LENGTH, COLI_MLA_MAX_ROWS,
-    COLI_MLA_ROPE, COLI_ROPE_HALVES, COLI_ROPE_PAIRS, MLA_EXPORTS, coli_mla_append, coli_mla_decode, coli_mla_dims, coli_mla_expand,
-    coli_mla_prefill, coli_mla_project, coli_mla_row_bytes, coli_mla_workspace_bytes, make_mla_dims)
+    COLI_BF16, COLI_F32, COLI_FP16, COLI_KV_E4M3, COLI_KV_PLAIN, COLI_MLA_MAX_BATCH, COLI_MLA_MAX_LENGTH, COLI_MLA_MAX_ROWS,
+    COLI_MLA_MAX_SHARED_ROWS, COLI_MLA_ROPE, COLI_ROPE_HALVES, COLI_ROPE_PAIRS, MLA_EXPORTS, coli_mla_append, coli_mla_decode,
+    coli_mla_decode_shared, coli_mla_dims, coli_mla_expand, coli_mla_prefill, coli_mla_project, coli_mla_row_bytes,
+    coli_mla_shared_workspace_bytes, coli_mla_workspace_bytes, make_mla_dims)
+from . import mla  # noqa: E402
+
+# ---------------------------------------------------------------- 8-bit products
+from .w8 import (  # noqa: E402,F401
+    COLI_W8_MAX_K, COLI_W8_MAX_ROWS, W8_EXPORTS, coli_w8_linear, coli_w8_quantize)

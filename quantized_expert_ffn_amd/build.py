@@ -19,7 +19,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libcolimoe.so")
 BIND = os.path.join(OUT_DIR, "_mla_bind.so")
 SOURCES = ["route.hip", "forward.hip", "down_rows.hip", "prefill.hip", "prefill_mx.hip", "layer.hip", "debug.hip",
-           "api.hip", "mla_append.hip", "mla_gemm.hip", "mla_decode.hip", "mla_prefill.hip", "mla_api.hip"]
+           "api.hip", "mla_append.hip", "mla_gemm.hip", "mla_decode.hip", "mla_prefill.hip", "mla_shared.hip", "mla_api.hip",
+           "select.hip", "w8_quantize.hip", "w8_linear.hip", "w8_api.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -2,6 +2,7 @@
 // carve-up, kernel launches, staging copies, status and timing.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -74,6 +75,31 @@ int check_dims(const coli_moe_dims *d) {
     if (d->wformat == COLI_WFMT_MXFP4 && (d->wbits != 4 || g != 0 || d->inter % 128 != 0))
         return fail(COLI_EINVAL, "MXFP4 experts need wbits=4, group_size=0 and inter a multiple of 128 "
                                  "(wbits=%d, group_size=%d, inter=%d)", d->wbits, g, d->inter);
+    return COLI_OK;
+}
+
+// Bytes of a select call's workspace: the status word's.
+constexpr size_t SELECT_WS = 256;
+
+int check_select_dims(const coli_select_dims *d) {
+    if (!d) return fail(COLI_EINVAL, "dims is NULL");
+    if (d->n_experts < 1 || d->n_experts > 1024)
+        return fail(COLI_EINVAL, "n_experts=%d: must be in 1..1024", d->n_experts);
+    if (d->n_group < 1 || d->n_group > 64 || d->n_experts % d->n_group)
+        return fail(COLI_EINVAL, "n_group=%d: must be in 1..64 and divide n_experts=%d", d->n_group, d->n_experts);
+    if (d->topk_group < 1 || d->topk_group > d->n_group)
+        return fail(COLI_EINVAL, "topk_group=%d: must be in 1..n_group=%d", d->topk_group, d->n_group);
+    const int open = d->n_experts / d->n_group * d->topk_group;
+    if (d->top_k < 1 || d->top_k > 32 || d->top_k > open)
+        return fail(COLI_EINVAL, "top_k=%d: must be in 1..min(32, %d experts of %d groups)", d->top_k, open, d->topk_group);
+    if (d->scoring != COLI_SCORE_SIGMOID && d->scoring != COLI_SCORE_SOFTMAX)
+        return fail(COLI_EINVAL, "scoring=%d: must be COLI_SCORE_SIGMOID (0) or COLI_SCORE_SOFTMAX (1)", d->scoring);
+    if (d->group_score != COLI_GROUP_MAX && d->group_score != COLI_GROUP_TOP2)
+        return fail(COLI_EINVAL, "group_score=%d: must be COLI_GROUP_MAX (0) or COLI_GROUP_TOP2 (1)", d->group_score);
+    if (d->norm_topk_prob != 0 && d->norm_topk_prob != 1)
+        return fail(COLI_EINVAL, "norm_topk_prob=%d: must be 0 or 1", d->norm_topk_prob);
+    if (!std::isfinite(d->routed_scaling_factor))
+        return fail(COLI_EINVAL, "routed_scaling_factor=%g: must be finite", (double)d->routed_scaling_factor);
     return COLI_OK;
 }
 
@@ -382,6 +408,43 @@ int coli_moe_route(const coli_moe_dims *d, int32_t S, const float *x, const floa
     if ((rc = check_device())) return rc;
     return route_launches(d, S, x, router_w, router_bias, topk_idx, topk_w, static_cast<uint8_t *>(ws), L,
                           false, true, static_cast<hipStream_t>(stream));
+}
+
+int coli_moe_select(const coli_select_dims *d, int32_t S, int32_t dtype, const void *logits, int64_t token_stride,
+                    const float *bias, int32_t *topk_idx, float *topk_w, void *ws, size_t ws_bytes, void *stream) {
+    int rc = check_select_dims(d);
+    if (rc) return rc;
+    if (S < 0 || S > COLI_MAX_TOKENS) return fail(COLI_EINVAL, "n_tokens=%d: must be in 0..%d", S, COLI_MAX_TOKENS);
+    if (dtype != COLI_BF16 && dtype != COLI_FP16 && dtype != COLI_F32)
+        return fail(COLI_EINVAL, "dtype=%d: must be COLI_BF16 (0), COLI_FP16 (1) or COLI_F32 (2)", dtype);
+    if (token_stride < 0 || token_stride > (int64_t)1 << 32)
+        return fail(COLI_EINVAL, "token_stride=%lld: must be in 0..2^32", (long long)token_stride);
+    if (S == 0) return COLI_OK;
+    if (!logits || !topk_idx || !topk_w || !ws) return fail(COLI_EINVAL, "coli_moe_select: NULL pointer argument");
+    const uintptr_t size = dtype == COLI_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(logits) % size || reinterpret_cast<uintptr_t>(bias) % 4 ||
+        reinterpret_cast<uintptr_t>(topk_idx) % 4 || reinterpret_cast<uintptr_t>(topk_w) % 4 || !aligned16(ws))
+        return fail(COLI_EINVAL, "coli_moe_select: arrays must be aligned to their elements, the workspace to 16 bytes");
+    if (ws_bytes < SELECT_WS) return fail(COLI_EWORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, SELECT_WS);
+    if ((rc = check_device())) return rc;
+    SelectArgs a{};
+    a.logits = logits;
+    a.bias = bias;
+    a.idx = topk_idx;
+    a.w = topk_w;
+    a.status = static_cast<uint32_t *>(ws);
+    a.stride = token_stride;
+    a.tokens = S;
+    a.experts = d->n_experts;
+    a.top_k = d->top_k;
+    a.groups = d->n_group;
+    a.topk_group = d->topk_group;
+    a.softmax = d->scoring == COLI_SCORE_SOFTMAX;
+    a.top2 = d->group_score == COLI_GROUP_TOP2;
+    a.norm = d->norm_topk_prob;
+    a.rsf = d->routed_scaling_factor;
+    const hipError_t e = launch_select(a, dtype, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? COLI_OK : hip_fail(e, "select launch");
 }
 
 int coli_moe_forward(const coli_moe_dims *d, int32_t S, const float *x, const int32_t *topk_idx,

@@ -231,6 +231,19 @@ size_t down_rows_smem(int S, int I, int E, int K, int n_shared, int group, int b
 hipError_t launch_layer(const FwdArgs &a, const LayerArgs &l, bool route, int bits, hipStream_t st);
 size_t layer_smem(int S, int H, int I, int E, int K, int n_shared);
 
+struct SelectArgs {
+    const void *logits;
+    const float *bias;       // [E] or null
+    int32_t *idx;            // [S, K]
+    float *w;                // [S, K]
+    uint32_t *status;
+    int64_t stride;
+    int tokens, experts, top_k, groups, topk_group;
+    int softmax, top2, norm;
+    float rsf;
+};
+hipError_t launch_select(const SelectArgs &a, int dtype, hipStream_t st);
+
 hipError_t launch_gateup(const FwdArgs &a, int bits, hipStream_t st);
 hipError_t launch_down(const FwdArgs &a, int bits, hipStream_t st);
 hipError_t launch_combine(const FwdArgs &a, hipStream_t st);

@@ -60,12 +60,45 @@ struct MlaDecodeArgs {
     float *lse;
     uint32_t *status;
     float *part;                  // partial results (workspace)
+    float *full;                  // and those of whole sequences, where only partial results are wanted
     int32_t batch, n_q, heads, max_kv;
     float scale;
 };
 hipError_t launch_mla_decode(const MlaDecodeArgs &a, const coli_mla_dims &d, hipStream_t st);
 // Bytes of partial results a decode call needs behind the status page.
 size_t mla_decode_part_bytes(const coli_mla_dims &d, int batch, int n_q, int max_kv);
+
+// Partial results of a decode call, without the join: a sequence whose plan
+// entry (two int32 at part, first and last workgroup) names one workgroup has
+// its result in slot sequence * blocks + block of `full`; others in slots
+// 2 (block * groups + g) + (g == first) of part + first floats.  A slot holds
+// `rows` rows, [32 rows][column tile][4][64 lanes] of four floats, then their
+// (maximum, sum) pairs.
+struct MlaParts {
+    int rows, blocks, groups, slot, first;
+};
+MlaParts mla_decode_parts(const coli_mla_dims &d, int batch, int n_q, int max_kv);
+hipError_t launch_mla_decode_parts(const MlaDecodeArgs &a, const coli_mla_dims &d, hipStream_t st);
+
+// Attention behind a prefix that all sequences share: its partial results, and
+// the join with those of the sequences' own tokens.
+struct MlaSharedArgs {
+    MlaCache c;                   // the prefix's pages
+    const void *q_lat, *q_pe;
+    const int32_t *kv_lens;       // the sequences' own tokens
+    void *out;
+    float *lse;
+    uint32_t *status;
+    float *part;                  // partial results over the prefix
+    const float *own, *full;      // of the sequences' own tokens (MlaParts), or null
+    int32_t batch, n_q, heads, prefix, max_kv;
+    MlaParts p;
+    float scale;
+};
+hipError_t launch_mla_shared(const MlaSharedArgs &a, const coli_mla_dims &d, hipStream_t st);
+hipError_t launch_mla_shared_join(const MlaSharedArgs &a, const coli_mla_dims &d, hipStream_t st);
+// Bytes of the prefix's partial results.
+size_t mla_shared_part_bytes(const coli_mla_dims &d, int64_t rows, int prefix);
 
 struct MlaPrefillArgs {
     const void *q, *k_nope, *k_pe, *v;

@@ -68,6 +68,40 @@ int check_cache(const coli_mla_dims *d, const void *pages, const float *kv_scale
     return COLI_OK;
 }
 
+int check_shared(const coli_mla_dims *d, int32_t batch, int32_t n_q, int32_t prefix_len, int32_t max_kv) {
+    if (batch < 0 || batch > COLI_MLA_MAX_BATCH)
+        return fail(COLI_EINVAL, "batch=%d: must be in 0..%d", batch, COLI_MLA_MAX_BATCH);
+    if (n_q < 1 || (int64_t)n_q * d->n_heads > COLI_MLA_MAX_ROWS)
+        return fail(COLI_EINVAL, "n_q=%d: must be positive, with n_q * n_heads at most %d", n_q, COLI_MLA_MAX_ROWS);
+    if ((int64_t)batch * n_q * d->n_heads > COLI_MLA_MAX_SHARED_ROWS)
+        return fail(COLI_EINVAL, "batch=%d, n_q=%d: batch * n_q * n_heads must be at most %d", batch, n_q,
+                    COLI_MLA_MAX_SHARED_ROWS);
+    if (prefix_len < 0 || prefix_len > COLI_MLA_MAX_LENGTH)
+        return fail(COLI_EINVAL, "prefix_len=%d: must be in 0..%d", prefix_len, COLI_MLA_MAX_LENGTH);
+    if (max_kv < 0 || max_kv > COLI_MLA_MAX_LENGTH || (int64_t)batch * max_kv > COLI_MLA_MAX_TOKENS)
+        return fail(COLI_EINVAL, "max_kv=%d: must be in 0..%d, with batch * max_kv at most %lld", max_kv,
+                    COLI_MLA_MAX_LENGTH, COLI_MLA_MAX_TOKENS);
+    return COLI_OK;
+}
+
+// Where a shared decode's workspace holds what: the status page, the own
+// tokens' partial results, those of whole sequences, the prefix's.
+struct SharedLayout {
+    size_t full, prefix, total;
+};
+SharedLayout shared_layout(const coli_mla_dims *d, int batch, int n_q, int prefix_len, int max_kv) {
+    SharedLayout l{};
+    if (batch == 0) {
+        l.total = WS_HEAD;
+        return l;
+    }
+    const MlaParts p = mla_decode_parts(*d, batch, n_q, max_kv);
+    l.full = WS_HEAD + mla_decode_part_bytes(*d, batch, n_q, max_kv);
+    l.prefix = l.full + 4 * (size_t)p.slot * p.blocks * batch;
+    l.total = l.prefix + mla_shared_part_bytes(*d, (int64_t)batch * n_q * d->n_heads, prefix_len);
+    return l;
+}
+
 bool bad_stride(int64_t s) { return s < 0 || s % 8 != 0; }
 
 MlaCache cache(const coli_mla_dims *d, const void *pages, const float *kv_scale, int32_t n_pages,
@@ -209,6 +243,78 @@ int coli_mla_decode(const coli_mla_dims *d, int32_t batch, int32_t n_q, const vo
     a.max_kv = max_kv;
     a.scale = d->softmax_scale;
     return launched(launch_mla_decode(a, *d, static_cast<hipStream_t>(stream)), "decode");
+}
+
+size_t coli_mla_shared_workspace_bytes(const coli_mla_dims *d, int32_t batch, int32_t n_q, int32_t prefix_len,
+                                       int32_t max_kv) {
+    if (check_mla_dims(d) != COLI_OK || check_shared(d, batch, n_q, prefix_len, max_kv) != COLI_OK) return 0;
+    return shared_layout(d, batch, n_q, prefix_len, max_kv).total;
+}
+
+int coli_mla_decode_shared(const coli_mla_dims *d, int32_t batch, int32_t n_q, const void *q_lat, const void *q_pe,
+                           const void *pages, const float *kv_scale, int32_t n_pages, const int32_t *prefix_table,
+                           int32_t prefix_width, int32_t prefix_len, const int32_t *table, int32_t table_width,
+                           const int32_t *kv_lens, int32_t max_kv, void *out, float *lse, void *ws, size_t ws_bytes,
+                           void *stream) {
+    int rc = check_mla_dims(d);
+    if (rc) return rc;
+    if ((rc = check_shared(d, batch, n_q, prefix_len, max_kv))) return rc;
+    if (batch == 0) return COLI_OK;
+    if (!q_lat || !q_pe || !table || !kv_lens || !out || (prefix_len > 0 && !prefix_table))
+        return fail(COLI_EINVAL, "coli_mla_decode_shared: NULL pointer argument");
+    if (!aligned16(q_lat) || !aligned16(q_pe) || !aligned16(out))
+        return fail(COLI_EINVAL, "coli_mla_decode_shared: q_lat, q_pe and out must be 16-byte aligned");
+    if (prefix_len > 0 && (prefix_width < 1 || (int64_t)prefix_width * d->page_size < prefix_len))
+        return fail(COLI_EINVAL, "coli_mla_decode_shared: prefix_width=%d pages do not hold prefix_len=%d tokens",
+                    prefix_width, prefix_len);
+    if (table_width < 1 || (int64_t)table_width * d->page_size < max_kv)
+        return fail(COLI_EINVAL, "coli_mla_decode_shared: table_width=%d pages do not hold max_kv=%d tokens", table_width,
+                    max_kv);
+    if ((rc = check_cache(d, pages, kv_scale, n_pages, "coli_mla_decode_shared"))) return rc;
+    const SharedLayout at = shared_layout(d, batch, n_q, prefix_len, max_kv);
+    if ((rc = check_ws(ws, ws_bytes, at.total, "coli_mla_decode_shared"))) return rc;
+    if ((rc = api_check_device())) return rc;
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    MlaDecodeArgs a{};
+    a.c = cache(d, pages, kv_scale, n_pages, table, table_width);
+    a.q_lat = q_lat;
+    a.q_pe = q_pe;
+    a.kv_lens = kv_lens;
+    a.out = out;
+    a.lse = lse;
+    a.status = static_cast<uint32_t *>(ws);
+    a.part = reinterpret_cast<float *>(base + WS_HEAD);
+    a.full = reinterpret_cast<float *>(base + at.full);
+    a.batch = batch;
+    a.n_q = n_q;
+    a.heads = d->n_heads;
+    a.max_kv = max_kv;
+    a.scale = d->softmax_scale;
+    if (prefix_len == 0) return launched(launch_mla_decode(a, *d, st), "decode");
+    MlaSharedArgs s{};
+    s.c = cache(d, pages, kv_scale, n_pages, prefix_table, prefix_width);
+    s.q_lat = q_lat;
+    s.q_pe = q_pe;
+    s.kv_lens = kv_lens;
+    s.out = out;
+    s.lse = lse;
+    s.status = a.status;
+    s.part = reinterpret_cast<float *>(base + at.prefix);
+    s.batch = batch;
+    s.n_q = n_q;
+    s.heads = d->n_heads;
+    s.prefix = prefix_len;
+    s.max_kv = max_kv;
+    s.scale = d->softmax_scale;
+    if (max_kv > 0) {
+        s.own = a.part;
+        s.full = a.full;
+        s.p = mla_decode_parts(*d, batch, n_q, max_kv);
+        if ((rc = launched(launch_mla_decode_parts(a, *d, st), "decode"))) return rc;
+    }
+    if ((rc = launched(launch_mla_shared(s, *d, st), "shared decode"))) return rc;
+    return launched(launch_mla_shared_join(s, *d, st), "join");
 }
 
 int coli_mla_expand(const coli_mla_dims *d, int32_t batch, int32_t n_rows, const void *pages,

@@ -1,5 +1,5 @@
-// The quick way from torch tensors to the latent-attention entry points: a
-// CPython module whose functions take the arguments of the Python ones, check
+// The quick way from torch tensors to the entry points of latent attention,
+// 8-bit products and expert selection: a CPython module whose functions take the arguments of the Python ones, check
 // types, shapes, layouts and devices, and call the library.  A kernel of a few
 // microseconds waits on its caller otherwise: a call of nine tensors spends
 // about 5 us on the same checks in Python and 2 us in ctypes.
@@ -15,8 +15,10 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <initializer_list>
+#include <type_traits>
 
 #include "coli_mla.h"
+#include "coli_w8.h"
 
 namespace {
 
@@ -100,9 +102,11 @@ Cache cache(Args &a, const coli_mla_dims *d, int pages, int scale) {
             static_cast<float *>(a.dense_or_none(scale, at::kFloat, {n * d->page_size})), n};
 }
 
-// Runs f on the arguments (the first of them the address of the dims, except
-// for project) with the tensors' device current.
-template <int N, class F>
+struct None;   // a call without dims
+
+// Runs f on the arguments (the first of them the address of the dims, where
+// there are any) with the tensors' device current.
+template <int N, class Dims = coli_mla_dims, class F>
 PyObject *call(PyObject *const *v, Py_ssize_t n, F f) {
     if (n != N) {
         PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
@@ -111,7 +115,7 @@ PyObject *call(PyObject *const *v, Py_ssize_t n, F f) {
     long rc = 1;
     try {
         Args a{v};
-        rc = f(a, reinterpret_cast<const coli_mla_dims *>(N == 4 ? 0 : PyLong_AsSize_t(v[0])));
+        rc = f(a, reinterpret_cast<const Dims *>(std::is_same<Dims, None>::value ? 0 : PyLong_AsSize_t(v[0])));
     } catch (const Misfit &) {
     } catch (const std::exception &) {
     }
@@ -156,7 +160,7 @@ PyObject *append(PyObject *, PyObject *const *v, Py_ssize_t n) {
 
 // x, w, out, stream
 PyObject *project(PyObject *, PyObject *const *v, Py_ssize_t n) {
-    return call<4>(v, n, [](Args &a, const coli_mla_dims *) -> long {
+    return call<4, None>(v, n, [](Args &a, const None *) -> long {
         const at::ScalarType t = a.tensor(0).scalar_type();
         if (t != at::kBFloat16 && t != at::kHalf) throw Misfit();
         const int64_t tokens = a.size(0, 0, 3), heads = a.size(0, 1, 3), n_in = a.size(0, 2, 3), n_out = a.size(1, 1, 3);
@@ -186,6 +190,93 @@ PyObject *decode(PyObject *, PyObject *const *v, Py_ssize_t n) {
         return coli_mla_decode(d, (int32_t)batch, batch ? (int32_t)(rows / batch) : 1, q_lat, q_pe, c.pages, c.scale, (int32_t)c.n,
                                static_cast<int32_t *>(table), (int32_t)width, static_cast<int32_t *>(lens), (int32_t)max_kv, out,
                                static_cast<float *>(lse), w, (size_t)ws, a.stream(11));
+    });
+}
+
+// dims, q_lat, q_pe, pages, kv_scale, prefix_table, prefix_len, table, kv_lens, max_kv, out, lse, ws, stream
+PyObject *decode_shared(PyObject *, PyObject *const *v, Py_ssize_t n) {
+    return call<14>(v, n, [](Args &a, const coli_mla_dims *d) -> long {
+        const at::ScalarType t = type_of(d);
+        const int64_t rows = a.size(1, 0, 3), batch = a.size(8, 0, 1), width = a.size(7, 1, 2), prefix_width = a.size(5, 0, 1);
+        if ((batch > 0 && (rows < 1 || rows % batch)) || rows > INT32_MAX || batch > INT32_MAX || width > INT32_MAX ||
+            prefix_width > INT32_MAX)
+            throw Misfit();
+        void *q_lat = a.dense(1, t, {rows, d->n_heads, d->rank}), *q_pe = a.dense(2, t, {rows, d->n_heads, COLI_MLA_ROPE});
+        const Cache c = cache(a, d, 3, 4);
+        void *prefix = a.dense(5, at::kInt, {prefix_width});
+        const int64_t prefix_len = a.number(6);
+        void *table = a.dense(7, at::kInt, {batch, width}), *lens = a.dense(8, at::kInt, {batch});
+        const int64_t max_kv = a.number(9);
+        void *out = a.dense(10, t, {rows, d->n_heads, d->rank}), *lse = a.dense_or_none(11, at::kFloat, {rows, d->n_heads});
+        const int64_t ws = a.size(12, 0, 1);
+        void *w = a.dense(12, at::kByte, {ws});
+        const c10::DeviceGuard guard(device_of(a));
+        return coli_mla_decode_shared(d, (int32_t)batch, batch ? (int32_t)(rows / batch) : 1, q_lat, q_pe, c.pages, c.scale,
+                                      (int32_t)c.n, static_cast<int32_t *>(prefix), (int32_t)prefix_width, (int32_t)prefix_len,
+                                      static_cast<int32_t *>(table), (int32_t)width, static_cast<int32_t *>(lens), (int32_t)max_kv,
+                                      out, static_cast<float *>(lse), w, (size_t)ws, a.stream(13));
+    });
+}
+
+// The library's number of an element type.
+int32_t number_of(const at::Tensor &t) {
+    switch (t.scalar_type()) {
+    case at::kBFloat16: return COLI_BF16;
+    case at::kHalf: return COLI_FP16;
+    case at::kFloat: return COLI_F32;
+    default: throw Misfit();
+    }
+}
+
+// [rows, width] with a row stride of its own, the last dimension dense.
+struct Rows {
+    void *at;
+    int64_t n, width, stride;
+};
+Rows rows_of(Args &a, int i) {
+    const at::Tensor &t = a.tensor(i);
+    if (t.dim() != 2 || t.size(0) > INT32_MAX || t.size(1) > INT32_MAX || (t.size(1) > 1 && t.stride(1) != 1)) throw Misfit();
+    // the stride of one row is never used
+    return {t.data_ptr(), t.size(0), t.size(1), t.size(0) > 1 ? t.stride(0) : t.size(1)};
+}
+
+// x, codes, scale, stream
+PyObject *quantize(PyObject *, PyObject *const *v, Py_ssize_t n) {
+    return call<4, None>(v, n, [](Args &a, const None *) -> long {
+        const Rows x = rows_of(a, 0);
+        void *codes = a.dense(1, at::kChar, {x.n, x.width}), *scale = a.dense(2, at::kFloat, {x.n});
+        const c10::DeviceGuard guard(device_of(a));
+        return coli_w8_quantize(number_of(a.tensor(0)), (int32_t)x.n, (int32_t)x.width, x.at, x.stride, static_cast<int8_t *>(codes),
+                                static_cast<float *>(scale), a.stream(3));
+    });
+}
+
+// codes, scale, w, w_scale, bias, out, stream
+PyObject *linear(PyObject *, PyObject *const *v, Py_ssize_t n) {
+    return call<7, None>(v, n, [](Args &a, const None *) -> long {
+        const Rows x = rows_of(a, 0), o = rows_of(a, 5);
+        if (a.tensor(0).scalar_type() != at::kChar || o.n != x.n || (o.n > 1 && o.stride < o.width)) throw Misfit();
+        void *scale = a.dense(1, at::kFloat, {x.n}), *w = a.dense(2, at::kChar, {o.width, x.width});
+        void *w_scale = a.dense(3, at::kFloat, {o.width}), *bias = a.dense_or_none(4, at::kFloat, {o.width});
+        const c10::DeviceGuard guard(device_of(a));
+        return coli_w8_linear(number_of(a.tensor(5)), (int32_t)x.n, (int32_t)x.width, (int32_t)o.width, static_cast<int8_t *>(x.at),
+                              x.stride, static_cast<float *>(scale), static_cast<int8_t *>(w), static_cast<float *>(w_scale),
+                              static_cast<float *>(bias), o.at, o.stride, a.stream(6));
+    });
+}
+
+// dims, logits, bias, topk_idx, topk_w, ws, stream
+PyObject *select(PyObject *, PyObject *const *v, Py_ssize_t n) {
+    return call<7, coli_select_dims>(v, n, [](Args &a, const coli_select_dims *d) -> long {
+        const Rows x = rows_of(a, 1);
+        if (x.width != d->n_experts) throw Misfit();
+        void *bias = a.dense_or_none(2, at::kFloat, {x.width});
+        void *idx = a.dense(3, at::kInt, {x.n, d->top_k}), *w = a.dense(4, at::kFloat, {x.n, d->top_k});
+        const int64_t ws = a.size(5, 0, 1);
+        void *space = a.dense(5, at::kByte, {ws});
+        const c10::DeviceGuard guard(device_of(a));
+        return coli_moe_select(d, (int32_t)x.n, number_of(a.tensor(1)), x.at, x.stride, static_cast<float *>(bias),
+                               static_cast<int32_t *>(idx), static_cast<float *>(w), space, (size_t)ws, a.stream(6));
     });
 }
 
@@ -234,6 +325,10 @@ PyObject *prefill(PyObject *, PyObject *const *v, Py_ssize_t n) {
 PyMethodDef methods[] = {{"append", (PyCFunction)(void (*)())append, METH_FASTCALL, nullptr},
                          {"project", (PyCFunction)(void (*)())project, METH_FASTCALL, nullptr},
                          {"decode", (PyCFunction)(void (*)())decode, METH_FASTCALL, nullptr},
+                         {"decode_shared", (PyCFunction)(void (*)())decode_shared, METH_FASTCALL, nullptr},
+                         {"quantize", (PyCFunction)(void (*)())quantize, METH_FASTCALL, nullptr},
+                         {"linear", (PyCFunction)(void (*)())linear, METH_FASTCALL, nullptr},
+                         {"select", (PyCFunction)(void (*)())select, METH_FASTCALL, nullptr},
                          {"expand", (PyCFunction)(void (*)())expand, METH_FASTCALL, nullptr},
                          {"prefill", (PyCFunction)(void (*)())prefill, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

@@ -20,6 +20,8 @@
 #include "kernels.h"
 #include "mla_mfma.h"
 
+#include <type_traits>
+
 namespace coli {
 namespace {
 
@@ -111,7 +113,10 @@ __device__ __forceinline__ int dec_swz(int t) {
 // A tile takes two barriers: one when it has arrived, one when its weights
 // have.  The weights are formed with the maximum of the tiles before, and
 // formed again (a third barrier) only where a score exceeds that by MAX_LAG.
-template <class D>
+//
+// PARTS: whole sequences too leave a partial result, in a slot of their own at
+// a.full, for a join with what else their queries see.
+template <class D, bool PARTS = false>
 __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int groups) {
     using T = typename D::T;
     constexpr int RANK = D::RANK, CT = D::CT, KS = D::KS;
@@ -573,7 +578,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
         const float half_off = FP8 && l != 0.0f ? __builtin_amdgcn_exp2f(0.5f * (mv - m)) : 1.0f;
         const float f = l == 0.0f ? 0.0f : half_off / l;
         auto result = [&](int c, int r) { return FP8 ? o[c][r] * f * half_off : o[c][r] * f; };
-        if (lo == 0 && hi == n_tiles) {
+        if (!PARTS && lo == 0 && hi == n_tiles) {
             // through the buffer of the last tile, 64 columns at a time, so that rows leave in whole lines
             const uint32_t at = spent + wave * 32 * 144;
 #pragma unroll
@@ -600,6 +605,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
             // slot 0: the segment begins inside its sequence, slot 1: with it
             const int64_t slot = ((int64_t)blockIdx.y * groups + g) * 2 + (lo == 0 ? 1 : 0);
             float *dst = a.part + 2 * ((a.batch + 7) & ~7) + slot * D::SLOT;
+            if (PARTS && lo == 0 && hi == n_tiles) dst = a.full + ((int64_t)seq * gridDim.y + blockIdx.y) * D::SLOT;
             float *at = dst + (rg * (RANK / 32) + cg * CT) * 1024 + 4 * lane;
 #pragma unroll
             for (int c = 0; c < CT; ++c)
@@ -738,6 +744,15 @@ hipError_t launch(const MlaDecodeArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <class D>
+hipError_t launch_parts(const MlaDecodeArgs &a, hipStream_t st) {
+    const int rows = a.n_q * a.heads, groups = dec_groups(a.batch, rows, a.max_kv);
+    const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_mla_decode<D, true>), D::LDS);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_mla_decode<D, true>), dim3(groups, (rows + D::ROWS - 1) / D::ROWS), dim3(256), D::LDS, st, a, groups);
+    return hipGetLastError();
+}
+
 template <class T, int RANK, bool FP8>
 hipError_t by_rows(const MlaDecodeArgs &a, hipStream_t st) {
     return dec_rows(a.n_q * a.heads) == 32 ? launch<Dec<T, RANK, FP8, 1>>(a, st)
@@ -754,6 +769,34 @@ size_t mla_decode_part_bytes(const coli_mla_dims &d, int batch, int n_q, int max
     int64_t slots = blocks > 256 ? blocks : 256;
     if (slots > blocks * tiles) slots = blocks * tiles;
     return 8 * (((size_t)batch + 7) & ~(size_t)7) + 4 * 2 * ((size_t)per * d.rank + 2 * per) * (size_t)slots;
+}
+
+MlaParts mla_decode_parts(const coli_mla_dims &d, int batch, int n_q, int max_kv) {
+    MlaParts p;
+    const int rows = n_q * d.n_heads;
+    p.rows = dec_rows(rows);
+    p.blocks = (rows + p.rows - 1) / p.rows;
+    p.groups = dec_groups(batch, rows, max_kv);
+    p.slot = p.rows * d.rank + 2 * p.rows;
+    p.first = 2 * ((batch + 7) & ~7);
+    return p;
+}
+
+hipError_t launch_mla_decode_parts(const MlaDecodeArgs &a, const coli_mla_dims &d, hipStream_t st) {
+    return mla_with_type(d.dtype, [&](auto t) {
+        using T = decltype(t);
+        const bool few = dec_rows(a.n_q * a.heads) == 32;
+        auto go = [&](auto rank, auto fp8) {
+            constexpr int R = decltype(rank)::value;
+            constexpr bool F = decltype(fp8)::value;
+            return few ? launch_parts<Dec<T, R, F, 1>>(a, st) : launch_parts<Dec<T, R, F, 2>>(a, st);
+        };
+        using std::integral_constant;
+        integral_constant<int, 512> wide;
+        integral_constant<int, 256> narrow;
+        if (d.kv_format == COLI_KV_E4M3) return d.rank == 512 ? go(wide, std::true_type()) : go(narrow, std::true_type());
+        return d.rank == 512 ? go(wide, std::false_type()) : go(narrow, std::false_type());
+    });
 }
 
 hipError_t launch_mla_decode(const MlaDecodeArgs &a, const coli_mla_dims &d, hipStream_t st) {

@@ -21,14 +21,16 @@ import torch
 
 from . import _lib, LIB_PATH, ColiError
 
-COLI_BF16, COLI_FP16 = 0, 1
+COLI_BF16, COLI_FP16, COLI_F32 = 0, 1, 2
 COLI_KV_PLAIN, COLI_KV_E4M3 = 0, 1
 COLI_ROPE_PAIRS, COLI_ROPE_HALVES = 0, 1
 COLI_MLA_ROPE = 64
 COLI_MLA_MAX_ROWS, COLI_MLA_MAX_BATCH, COLI_MLA_MAX_LENGTH = 16384, 4096, 2 ** 31 - 256
+COLI_MLA_MAX_SHARED_ROWS = 1 << 20
 
 MLA_EXPORTS = ("coli_mla_row_bytes", "coli_mla_workspace_bytes", "coli_mla_append", "coli_mla_project",
-               "coli_mla_decode", "coli_mla_expand", "coli_mla_prefill")
+               "coli_mla_decode", "coli_mla_expand", "coli_mla_prefill", "coli_mla_shared_workspace_bytes",
+               "coli_mla_decode_shared")
 
 _TYPES = {torch.bfloat16: COLI_BF16, torch.float16: COLI_FP16, COLI_BF16: COLI_BF16, COLI_FP16: COLI_FP16}
 _OF = {COLI_BF16: torch.bfloat16, COLI_FP16: torch.float16}
@@ -52,6 +54,9 @@ _sigs = {
     "coli_mla_project": (ctypes.c_int, [_I32, _I32, _I32, _I32, _I32, _P, _I64, _I64, _P, _P, _P]),
     "coli_mla_decode": (ctypes.c_int, [_D, _I32, _I32, _P, _P, _P, _P, _I32, _P, _I32, _P, _I32, _P, _P, _P, _SZ,
                                        _P]),
+    "coli_mla_shared_workspace_bytes": (_SZ, [_D, _I32, _I32, _I32, _I32]),
+    "coli_mla_decode_shared": (ctypes.c_int, [_D, _I32, _I32, _P, _P, _P, _P, _I32, _P, _I32, _I32, _P, _I32, _P, _I32, _P,
+                                              _P, _P, _SZ, _P]),
     "coli_mla_expand": (ctypes.c_int, [_D, _I32, _I32, _P, _P, _I32, _P, _I32, _P, _P, _P, _P, _P, _SZ, _P]),
     "coli_mla_prefill": (ctypes.c_int, [_D, _I32, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _P,
                                         _P, _I32, _I32, _P, _P, _P, _SZ, _P]),
@@ -121,6 +126,15 @@ class _Refused:
         self.dense(pages, dtype, (n, d.page_size, row), "pages")
         if kv_scale is not None:
             self.dense(kv_scale, torch.float32, (n * d.page_size,), "kv_scale")
+
+    def rows(self, t, dtypes, shape, what):
+        """[rows, width] with a stride of its own, the last dimension dense, of one of some types."""
+        self.size(t, 2, 0, what)
+        if t.dtype not in dtypes:
+            raise TypeError(f"{what}: dtype {t.dtype}, expected one of {', '.join(str(d) for d in dtypes)}")
+        self.tensor(t, t.dtype, shape, what)
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{what}: the last dimension must be contiguous")
 
     def workspace(self, ws):
         self.dense(ws, torch.uint8, (self.size(ws, 1, 0, "ws"),), "ws")
@@ -276,6 +290,41 @@ def coli_mla_decode(dims, q_lat, q_pe, pages, kv_scale, table, kv_lens, max_kv, 
         no.workspace(ws)
         no.end()
     _check(rc, "coli_mla_decode")
+
+
+def coli_mla_shared_workspace_bytes(dims, batch: int, n_q: int, prefix_len: int, max_kv: int) -> int:
+    """Raises ColiError(COLI_EINVAL) for sizes that no call takes."""
+    n = int(_lib.coli_mla_shared_workspace_bytes(ctypes.byref(dims), batch, n_q, prefix_len, max_kv))
+    if n == 0:
+        raise ColiError(-1, "coli_mla_shared_workspace_bytes")
+    return n
+
+
+def coli_mla_decode_shared(dims, q_lat, q_pe, pages, kv_scale, prefix_table, prefix_len, table, kv_lens, max_kv, out, lse,
+                           ws, stream=None):
+    """coli_mla_decode for sequences that begin with the prefix_len tokens of prefix_table [pages]; table and kv_lens are of
+    their own tokens.  lse may be None."""
+    rc = _bind.decode_shared(_at(dims), q_lat, q_pe, pages, kv_scale, prefix_table, prefix_len, table, kv_lens, max_kv, out,
+                             lse, ws, _handle(stream, q_lat))
+    if rc == _MISFIT:
+        no, d, dt = _Refused("coli_mla_decode_shared"), dims, _OF[dims.dtype]
+        batch, rows = no.size(kv_lens, 1, 0, "kv_lens"), no.size(q_lat, 3, 0, "q_lat")
+        if batch and (rows % batch or not rows):
+            raise ValueError(f"q_lat: {rows} rows for {batch} sequences")
+        no.pages(d, pages, kv_scale)
+        no.dense(q_lat, dt, (rows, d.n_heads, d.rank), "q_lat")
+        no.dense(q_pe, dt, (rows, d.n_heads, COLI_MLA_ROPE), "q_pe")
+        no.dense(prefix_table, torch.int32, (no.size(prefix_table, 1, 0, "prefix_table"),), "prefix_table")
+        no.number(prefix_len, "prefix_len")
+        no.dense(table, torch.int32, (batch, no.size(table, 2, 1, "table")), "table")
+        no.dense(kv_lens, torch.int32, (batch,), "kv_lens")
+        no.number(max_kv, "max_kv")
+        no.dense(out, dt, (rows, d.n_heads, d.rank), "out")
+        if lse is not None:
+            no.dense(lse, torch.float32, (rows, d.n_heads), "lse")
+        no.workspace(ws)
+        no.end()
+    _check(rc, "coli_mla_decode_shared")
 
 
 def coli_mla_expand(dims, pages, kv_scale, table, cu_k, w, kv, k_pe, ws, stream=None):
