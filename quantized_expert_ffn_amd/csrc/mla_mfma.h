@@ -157,6 +157,13 @@ __device__ __forceinline__ void load_to_lds_from(const void *base, uint32_t at, 
                  : "memory", "scc", "m0");
 }
 
+// A 32-bit word of each lane straight into LDS, lane l's to lds + 4 l.
+__device__ __forceinline__ void load_word_to_lds(const void *src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src),
+                 "s"(__builtin_amdgcn_readfirstlane((int)lds))
+                 : "memory", "m0");
+}
+
 // A value that is the same in every lane, as a scalar.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 

@@ -9,6 +9,8 @@
 #include "kernels.h"
 #include "mla_mfma.h"
 
+#include <type_traits>
+
 namespace coli {
 namespace {
 
@@ -31,7 +33,8 @@ struct Shd {
     static constexpr int L_ID = RING * TILE;                    // int32 [RING][4 wavefronts][64]: page ids of tiles to come
     static constexpr int L_SCALE = L_ID + RING * 1024;          // float [RING][32]: E4M3 scales
     static constexpr int L_EXP = L_SCALE + RING * 4 * SHD_TILE; // float [RING][32]: their exponents
-    static constexpr int LDS = L_EXP + RING * 4 * SHD_TILE;
+    static constexpr int L_FRAC = L_EXP + RING * 4 * SHD_TILE;  // float [RING][32]: and fractions
+    static constexpr int LDS = L_FRAC + RING * 4 * SHD_TILE;
     static constexpr int SLOT = SHD_ROWS * RANK + 2 * SHD_ROWS;
     static_assert(LDS <= 160 * 1024, "the LDS of a CU");
 };
@@ -51,6 +54,45 @@ Units shd_units(int64_t rows, int prefix) {
     u.shares = (int)(u.units < 256 ? u.units : 256);
     return u;
 }
+
+// A product whose sum stays in ordinary registers, beside accumulators that
+// fill the others.  The first wait covers operands just written by vector
+// instructions; whoever reads the sum waits for it (settled).
+template <class T>
+__device__ __forceinline__ void mfma_v(f32x16 &c, x8<T> a, x8<T> b) {
+    if constexpr (std::is_same<T, __bf16>::value)
+        asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+    else
+        asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+}
+// Waits out a matrix instruction of up to sixteen passes.
+__device__ __forceinline__ void settled(f32x16 &c) { asm volatile("s_nop 15\n\ts_nop 7" : "+v"(c)); }
+
+// Accumulators by a factor, and out of their registers: eight at a time
+// through one ordinary register each, since the compiler would bring them all
+// over at once, for which there is no room.
+template <int I>
+__device__ __forceinline__ void acc_scale(f32x16 &c, float f) {
+    float t, v0 = c[I], v1 = c[I + 1], v2 = c[I + 2], v3 = c[I + 3], v4 = c[I + 4], v5 = c[I + 5], v6 = c[I + 6], v7 = c[I + 7];
+#define COLI_SCALE(r) "v_accvgpr_read_b32 %8, " r "\n\ts_nop 1\n\tv_mul_f32 %8, %8, %9\n\ts_nop 1\n\tv_accvgpr_write_b32 " r ", %8\n\t"
+    asm volatile(COLI_SCALE("%0") COLI_SCALE("%1") COLI_SCALE("%2") COLI_SCALE("%3") COLI_SCALE("%4") COLI_SCALE("%5")
+                     COLI_SCALE("%6") COLI_SCALE("%7") "s_nop 3"
+                 : "+a"(v0), "+a"(v1), "+a"(v2), "+a"(v3), "+a"(v4), "+a"(v5), "+a"(v6), "+a"(v7), "=&v"(t)
+                 : "v"(f));
+#undef COLI_SCALE
+    c[I] = v0, c[I + 1] = v1, c[I + 2] = v2, c[I + 3] = v3, c[I + 4] = v4, c[I + 5] = v5, c[I + 6] = v6, c[I + 7] = v7;
+}
+__device__ __forceinline__ f32x4 acc_read(float a, float b, float c, float d) {
+    f32x4 v;
+    float x, y, z, w;
+    asm volatile("v_accvgpr_read_b32 %0, %4\n\tv_accvgpr_read_b32 %1, %5\n\tv_accvgpr_read_b32 %2, %6\n\tv_accvgpr_read_b32 %3, %7\n\ts_nop 1"
+                 : "=&v"(x), "=&v"(y), "=&v"(z), "=&v"(w)
+                 : "a"(a), "a"(b), "a"(c), "a"(d));
+    v[0] = x, v[1] = y, v[2] = z, v[3] = w;
+    return v;
+}
+// Waits out the matrix instructions before.
+__device__ __forceinline__ void acc_settled() { asm volatile("s_nop 15\n\ts_nop 7" ::: "memory"); }
 
 __device__ __forceinline__ int shd_swz(int t) { return 4 * ((t >> 1) & 1) + 2 * ((t >> 2) & 1) + ((t >> 3) & 1); }
 
@@ -79,17 +121,88 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
     bool bad_page = false;
 
     // ---- lane addresses inside a tile
-    uint32_t ka[4], va[4];
+    uint32_t ka, va;
     {
-        const int f = shd_swz(n), x = lane & 15, cb = (lane >> 4) & 1;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            ka[v] = (n >> 3) * D::CB * 1024 + (n & 7) * 128 + (((2 * v + hf) ^ f) << 4);
-            const int e = v >> 1, t8 = 4 * hf + (x >> 2), fv = shd_swz(8 * e + t8);
-            va[v] = e * D::CB * 1024 + t8 * 128 + (((4 * (v & 1) + 2 * cb + ((x & 3) >> 1)) ^ fv) << 4) + 8 * (x & 1);
+        const int x = lane & 15, cb = (lane >> 4) & 1, t8 = 4 * hf + (x >> 2);
+        ka = (n >> 3) * D::CB * 1024 + (n & 7) * 128 + ((hf ^ shd_swz(n)) << 4);          // chunk 2 v + hf at ka ^ 32 v
+        va = t8 * 128 + (((2 * cb + ((x & 3) >> 1)) ^ shd_swz(t8)) << 4) + 8 * (x & 1);   // odd column tiles at va ^ 64,
+    }                                                                                     // tokens 8 .. 15 at va ^ 16 + 1 KiB lines
+    // ---- the tiles on their way: a thread loads chunk lane % 8 of every line of token lt
+    const int lt = 8 * wave + (lane >> 3), lf = shd_swz(lt), chunk = (lane & 7) ^ lf;
+    auto base_of = [](int tile) { return (uint32_t)(tile & (D::RING - 1)) * D::TILE; };
+    struct Place {
+        int page, in;
+    };
+    auto place = [&](int tile) {
+        const int t = min(tile * SHD_TILE + lt, a.prefix - 1), pi = div_by(t, a.c.page, page_inv);
+        return Place{pi, t - pi * a.c.page};
+    };
+    auto slot_of = [&](int id, const Place &p) {
+        const bool bad = (uint32_t)id >= (uint32_t)a.c.n_pages;
+        bad_page |= bad;
+        return (int64_t)(bad ? 0 : id) * a.c.page + p.in;
+    };
+    // plain rows: page ids go to LDS two tiles before the rows do
+    const uint32_t id_at = D::L_ID + wave * 256;
+    auto issue_id = [&](int tile) { load_word_to_lds(a.c.table + place(tile).page, id_at + (tile & (D::RING - 1)) * 1024); };
+    auto issue = [&](int tile) {
+        const int id = lds_read<int>(id_at + (tile & (D::RING - 1)) * 1024 + 4 * lane);
+        const uint8_t *src = a.c.pages + slot_of(id, place(tile)) * D::ROW + 16 * chunk;
+        const uint32_t dst = base_of(tile) + wave * D::CB * 1024;
+        load_to_lds<0>(src, dst);
+        load_to_lds<128>(src, dst, 1024);
+        load_to_lds<256>(src, dst, 2048);
+        load_to_lds<384>(src, dst, 3 * 1024);
+        load_to_lds<512>(src, dst, 4 * 1024);
+        if constexpr (D::CB > 5) {
+            load_to_lds<640>(src, dst, 5 * 1024);
+            load_to_lds<768>(src, dst, 6 * 1024);
+            load_to_lds<896>(src, dst, 7 * 1024);
+            load_to_lds<1024>(src, dst, 8 * 1024);
         }
-    }
-    const int lt = 8 * wave + (lane >> 3), lf = shd_swz(lt);   // the token whose chunks this thread loads
+    };
+    // codes: through registers, widened on the way
+    constexpr int CODES = FP8 ? RANK / 128 : 1;
+    u32x4 codes[CODES];
+    x8<T> key;
+    float token_scale = 0.0f;
+    int id_next = 0;
+    auto fetch_id = [&](int tile) { id_next = a.c.table[place(tile).page]; };
+    auto fetch = [&](int tile) {   // with the id that fetch_id has fetched
+        const int64_t slot = slot_of(id_next, place(tile));
+        const uint8_t *src = a.c.pages + slot * D::ROW;
+#pragma unroll
+        for (int i = 0; i < CODES; ++i) codes[i] = *reinterpret_cast<const u32x4 *>(src + 16 * (lane & 7) + 128 * i);
+        key = *reinterpret_cast<const x8<T> *>(src + RANK + 16 * (lane & 7));
+        token_scale = a.c.scale[slot];
+    };
+    auto put = [&](int tile) {
+        const uint32_t dst = base_of(tile) + wave * D::CB * 1024 + (lane >> 3) * 128, at = 4 * ((tile & (D::RING - 1)) * SHD_TILE + lt);
+        const uint32_t line = dst + ((lane & 7) >> 2) * 1024;
+#pragma unroll
+        for (int i = 0; i < CODES; ++i) {   // sixteen codes are chunks 2 c and 2 c + 1 of the widened row, c = lane % 8 + 8 i
+            lds_write(line + (((2 * lane & 7) ^ lf) << 4), widen8<T>(u32x2{codes[i][0], codes[i][1]}), 2048 * i);
+            lds_write(line + (((2 * lane + 1 & 7) ^ lf) << 4), widen8<T>(u32x2{codes[i][2], codes[i][3]}), 2048 * i);
+        }
+        lds_write(dst + (chunk << 4), key, (D::CB - 1) * 1024);
+        lds_write<float>(D::L_SCALE + at, token_scale);
+        lds_write<float>(D::L_FRAC + at, __builtin_amdgcn_frexp_mantf(token_scale));
+        lds_write<float>(D::L_EXP + at, token_scale == 0.0f ? NEG : (float)__builtin_amdgcn_frexp_expf(token_scale));
+    };
+    // A tile that some rows see only in part: values that are not finite would reach rows that do not see them.
+    auto clear = [&](int tile, int from) {
+        constexpr int CH = (D::CB - 1) * 8;
+        for (int i = tid; i < (SHD_TILE - from) * CH; i += 256) {
+            const int t = from + i / CH, c = i % CH;
+            const uint32_t w = base_of(tile) + ((t >> 3) * D::CB + (c >> 3)) * 1024 + (t & 7) * 128 + ((c & 7) << 4);
+            x8<T> v = lds_read<x8<T>>(w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (!finite_f32((float)v[k])) v[k] = (T)0.0f;
+            lds_write(w, v);
+        }
+        barrier_lds();
+    };
 
     while (unit < end) {
         const int blk = (int)(unit / u.tiles), lo = (int)(unit - (int64_t)blk * u.tiles);
@@ -98,6 +211,14 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
         const int64_t row = (int64_t)blk * SHD_ROWS + 32 * wave + n, wave_row = (int64_t)blk * SHD_ROWS + 32 * wave;
         const bool works = wave_row < rows;
         const int64_t at_row = row < rows ? row : rows - 1;
+        if constexpr (!FP8) {
+            issue_id(lo);
+            issue_id(lo + 1);
+            issue_id(lo + 2);
+            issue_id(lo + 3);
+        } else {
+            fetch_id(lo);
+        }
         x8<T> qf[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s)
@@ -113,6 +234,25 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
             block_seen = min(block_seen, shd_seen(a, r));
         for (int o = 32; o; o >>= 1) block_seen = min(block_seen, __shfl_xor(block_seen, o));
         block_seen = uniform(block_seen);
+        const int partly = block_seen < a.prefix ? block_seen : INT32_MAX;   // tiles that end behind it
+#pragma unroll
+        for (int s = 0; s < KS; ++s) arrived(qf[s]);
+        wait_vm<0>();
+        if constexpr (!FP8) {
+            issue(lo);
+            issue(lo + 1);
+            issue(lo + 2);
+            issue_id(lo + 4);
+        } else {
+            fetch(lo);
+            fetch_id(lo + 1);
+            put(lo);
+            fetch(lo + 1);
+            fetch_id(lo + 2);
+            put(lo + 1);
+            fetch(lo + 2);
+            fetch_id(lo + 3);
+        }
 
         f32x16 o[CT];
 #pragma unroll
@@ -120,156 +260,200 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[c][r] = 0.0f;
         float m = NEG, l = 0.0f, mv = NEG;
+        f32x16 s;
+        f32x4 frac, expo;   // E4M3: four tokens' scales
+        float f = 1.0f, ref = 0.0f, refv = 0.0f;
+        bool moved = false;
+        x8<T> p[2], pn[2];
 
-        for (int tile = lo; tile < hi; ++tile) {
-            const int t0 = tile * SHD_TILE;
-            __syncthreads();   // the tile before is done with
-            {
-                const int t = min(t0 + lt, a.prefix - 1), pi = div_by(t, a.c.page, page_inv);
-                int id = a.c.table[pi];
-                if ((uint32_t)id >= (uint32_t)a.c.n_pages) {
-                    bad_page = true;
-                    id = 0;
-                }
-                const int64_t slot = (int64_t)id * a.c.page + (t - pi * a.c.page);
-                const uint8_t *src = a.c.pages + slot * D::ROW;
-                const uint32_t dst = wave * D::CB * 1024 + (lane >> 3) * 128;
-                if (FP8) {
+        // ---- scores of a tile
+        auto score = [&](int tile) {
+            const uint32_t base = base_of(tile);
+            uint32_t kb[4];
 #pragma unroll
-                    for (int i = 0; i < RANK / 128; ++i) {
-                        const int c = (lane & 7) + 8 * i;   // of sixteen codes: chunks 2 c and 2 c + 1
-                        const u32x4 w = *reinterpret_cast<const u32x4 *>(src + 16 * c);
-                        const uint32_t line = dst + (c >> 2) * 1024;
-                        lds_write(line + (((2 * c & 7) ^ lf) << 4), widen8<T>(u32x2{w[0], w[1]}));
-                        lds_write(line + (((2 * c + 1 & 7) ^ lf) << 4), widen8<T>(u32x2{w[2], w[3]}));
-                    }
-                    const x8<T> v = *reinterpret_cast<const x8<T> *>(src + RANK + 16 * (lane & 7));
-                    lds_write(dst + (D::CB - 1) * 1024 + (((lane & 7) ^ lf) << 4), v);
-                    if ((lane & 7) == 0) {
-                        const float sc = a.c.scale[slot];
-                        lds_write<float>(D::L_SCALE + 4 * lt, sc);
-                        lds_write<float>(D::L_EXP + 4 * lt, sc == 0.0f ? NEG : (float)__builtin_amdgcn_frexp_expf(sc));
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < D::CB; ++c) {
-                        const x8<T> v = *reinterpret_cast<const x8<T> *>(src + 128 * c + 16 * (lane & 7));
-                        lds_write(dst + c * 1024 + (((lane & 7) ^ lf) << 4), v);
-                    }
-                }
-            }
-            __syncthreads();
-            f32x16 s;
-            float sc[16];
+            for (int v = 0; v < 4; ++v) kb[v] = base + (ka ^ 32 * v);
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = 0.0f;
+            // operands AHEAD reads before their products
+            constexpr int AHEAD = FP8 && RANK == 512 ? 2 : 4;
+            u32x4 ahead[2][AHEAD];
 #pragma unroll
-            for (int k = 0; k < RANK / 16; ++k) s = mfma32<T>(lds_read<x8<T>>(ka[k & 3], (k >> 2) * 1024), qf[k], s);
-            if (FP8) {
+            for (int i = 0; i < AHEAD; ++i) ahead[0][i] = lds_read<u32x4>(kb[i]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f32x4 v = lds_read<f32x4>(D::L_SCALE + 16 * hf, 32 * q);
+            for (int c = 0; c < KS; c += AHEAD) {
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        s[4 * q + i] *= v[i];
-                        sc[4 * q + i] = __builtin_amdgcn_frexp_mantf(v[i]);
+                for (int i = c + AHEAD; i < KS && i < c + 2 * AHEAD; ++i)
+                    ahead[(c / AHEAD + 1) & 1][i % AHEAD] = lds_read<u32x4>(kb[i & 3], (i >> 2) * 1024);
+                if (FP8 && c == RANK / 16) {
+                    settled(s);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4 v = lds_read<f32x4>(D::L_SCALE + 16 * hf + 4 * (tile & (D::RING - 1)) * SHD_TILE, 32 * q);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[4 * q + i] *= v[i];
                     }
                 }
-            }
 #pragma unroll
-            for (int k = RANK / 16; k < KS; ++k) s = mfma32<T>(lds_read<x8<T>>(ka[k & 3], (k >> 2) * 1024), qf[k], s);
+                for (int i = 0; i < AHEAD; ++i) mfma_v<T>(s, __builtin_bit_cast(x8<T>, ahead[(c / AHEAD) & 1][i]), qf[c + i]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            const int t0 = tile * SHD_TILE;
             if (t0 + SHD_TILE > wave_seen) {
-                const int rem = seen - t0 - 4 * hf;
+                settled(s);
+                int rem = seen - t0 - 4 * hf;
+                arrived(rem);   // a branch, not selects that every tile would pay for
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (8 * (r >> 2) + (r & 3) >= rem) {
-                        s[r] = NEG;
-                        sc[r] = 0.0f;
-                    }
+                    if (8 * (r >> 2) + (r & 3) >= rem) s[r] = NEG;
             }
-            // ---- softmax
-            float top = s[0], sv[16];
+        };
+        // ---- its softmax in CT steps, for the shadows of matrix instructions
+        auto soften = [&](int tile, int step) {
+            // The products of steps 0 and 1 stand between the scores' last one and this wait, which covers the end of it.
+            if (step == 1) {
+                settled(s);
+                float top = fmaxf(fmaxf(s[0], s[1]), s[2]);
 #pragma unroll
-            for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
-            top = half_max(top) * scale;
-            float topv = NEG;
-            if (FP8) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f32x4 e = lds_read<f32x4>(D::L_EXP + 16 * hf, 32 * q);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        sv[4 * q + i] = __builtin_fmaf(s[4 * q + i], scale, e[i]);
-                        topv = fmaxf(topv, sv[4 * q + i]);
-                    }
-                }
-                topv = half_max(topv);
-            }
-            if (__ballot(top > m + LAG || (FP8 && topv > mv + LAG))) {
-                const float to = top > m + LAG ? top - LIFT : m;
-                float f = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+                for (int r = 3; r < 15; r += 2) top = fmaxf(fmaxf(top, s[r]), s[r + 1]);
+                top = half_max(fmaxf(top, s[15])) * scale;
+                bool grows = top > m + LAG;
+                const float to = grows ? top - LIFT : m;
+                f = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
                 l *= f;
                 m = to;
+                ref = m == NEG ? 0.0f : m;
                 if (FP8) {
-                    const float tov = topv > mv + LAG ? rintf(topv) - LIFT : mv;
+                    float topv = NEG;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4 e = lds_read<f32x4>(D::L_EXP + 16 * hf + 4 * (tile & (D::RING - 1)) * SHD_TILE, 32 * q);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) topv = fmaxf(topv, __builtin_fmaf(s[4 * q + i], scale, e[i]));
+                    }
+                    topv = half_max(topv);
+                    const bool growsv = topv > mv + LAG;
+                    const float tov = growsv ? rintf(topv) - LIFT : mv;
                     f = mv == tov ? 1.0f : __builtin_amdgcn_exp2f(mv - tov);
                     mv = tov;
+                    refv = mv == NEG ? 0.0f : mv;
+                    grows |= growsv;
+                }
+                moved = __ballot(grows) != 0;
+            } else if (step > 1) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (r >= (step - 2) * 16 / (CT - 2) && r < (step - 1) * 16 / (CT - 2)) {
+                        float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale, -ref));
+                        l += w;
+                        if (FP8) {
+                            if (r % 4 == 0) {
+                                const int at = 16 * hf + 4 * (tile & (D::RING - 1)) * SHD_TILE;
+                                frac = lds_read<f32x4>(D::L_FRAC + at, 8 * r);
+                                expo = lds_read<f32x4>(D::L_EXP + at, 8 * r);
+                            }
+                            w = frac[r % 4] * __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale, expo[r % 4]) - refv);
+                            if (s[r] == NEG) w = 0.0f;   // not seen, whatever its scale
+                        }
+                        pn[r >> 3][r & 7] = (T)w;
+                    }
+            }
+        };
+        auto take = [&] {   // the weights formed are the ones to use
+            p[0] = pn[0];
+            p[1] = pn[1];
+            if (moved) {
+                acc_settled();
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    acc_scale<0>(o[c], f);
+                    acc_scale<8>(o[c], f);
+                }
+            }
+        };
+        // ---- a tile's values by its weights; the next tile's softmax between the products
+        auto values = [&](int tile, auto next) {
+            const uint32_t base = base_of(tile);
+            uint32_t vb[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) vb[v] = base + (va ^ (64 * (v & 1) + 16 * (v >> 1))) + (v >> 1) * D::CB * 1024;
+            auto read = [&](int c, int k) {
+                const int imm = 2 * k * D::CB * 1024 + (c >> 1) * 1024;
+                const u32x2 v0 = lds_read_tr16(vb[c & 1], imm), v1 = lds_read_tr16(vb[2 + (c & 1)], imm);
+                return u32x4{v0[0], v0[1], v1[0], v1[1]};
+            };
+            u32x4 ahead[2][2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) ahead[0][k] = read(0, k);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (c + 1 < CT) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) ahead[(c + 1) & 1][k] = read(c + 1, k);
                 }
 #pragma unroll
-                for (int c = 0; c < CT; ++c)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) o[c][r] *= f;
+                for (int k = 0; k < 2; ++k) o[c] = mfma32<T>(__builtin_bit_cast(x8<T>, ahead[c & 1][k]), p[k], o[c]);
+                if constexpr (decltype(next)::value) soften(tile + 1, c);
             }
-            const float ref = m == NEG ? 0.0f : m, refv = mv == NEG ? 0.0f : mv;
-            x8<T> p[2];
+            __builtin_amdgcn_sched_barrier(0);
+        };
+
+        if constexpr (!FP8) wait_vm<2 * D::CB + 1>();
+        barrier_lds();
+        score(lo);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], scale, -ref));
-                l += w;
-                if (FP8) w = sc[r] * __builtin_amdgcn_exp2f(sv[r] - refv);
-                p[r >> 3][r & 7] = (T)w;
+        for (int c = 0; c < CT; ++c) soften(lo, c);
+        take();
+        int i = lo;
+        for (; i + 1 < hi; ++i) {
+            if constexpr (!FP8) {
+                if (i + 2 < hi)
+                    wait_vm<D::CB + 1>();
+                else
+                    wait_vm<0>();
             }
-            // A tile that some rows see only in part: values that are not finite would reach rows that do not see them.
-            if (block_seen < a.prefix && t0 + SHD_TILE > block_seen) {
-                __syncthreads();
-                const int from = block_seen > t0 ? block_seen - t0 : 0;
-                constexpr int CH = (D::CB - 1) * 8;
-                for (int i = tid; i < (SHD_TILE - from) * CH; i += 256) {
-                    const int t = from + i / CH, c = i % CH;
-                    const uint32_t w = ((t >> 3) * D::CB + (c >> 3)) * 1024 + (t & 7) * 128 + ((c & 7) << 4);
-                    x8<T> v = lds_read<x8<T>>(w);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (!finite_f32((float)v[k])) v[k] = (T)0.0f;
-                    lds_write(w, v);
-                }
-                __syncthreads();
+            barrier_lds();   // tile i + 1 is there, and every wavefront is done with tile i - 1
+            if constexpr (!FP8) {
+                if (i + 3 < hi) issue(i + 3);
+                issue_id(i + 5);
             }
-#pragma unroll
-            for (int c = 0; c < CT; ++c)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int imm = 2 * k * D::CB * 1024 + (c >> 1) * 1024;
-                    const u32x2 v0 = lds_read_tr16(va[c & 1], imm), v1 = lds_read_tr16(va[2 + (c & 1)], imm);
-                    o[c] = mfma32<T>(__builtin_bit_cast(x8<T>, u32x4{v0[0], v0[1], v1[0], v1[1]}), p[k], o[c]);
-                }
+            if ((i + 1) * SHD_TILE > partly) clear(i, max(0, block_seen - i * SHD_TILE));
+            score(i + 1);
+            if constexpr (FP8) {
+                put(i + 2);
+                fetch(i + 3);
+                fetch_id(i + 4);
+            }
+            values(i, std::true_type());
+            take();
         }
+        if ((i + 1) * SHD_TILE > partly) {
+            barrier_lds();
+            clear(i, max(0, block_seen - i * SHD_TILE));
+        }
+        values(i, std::false_type());
+        wait_vm<0>();
+        barrier_lds();   // the ring is free
+        acc_settled();
 
         // ---- the segment's result, divided by its sum
         l = half_sum(l);
         if (works) {
             const float half_off = FP8 && l != 0.0f ? __builtin_amdgcn_exp2f(0.5f * (mv - m)) : 1.0f;
-            const float f = l == 0.0f ? 0.0f : half_off / l;
+            const float by = l == 0.0f ? 0.0f : half_off / l;
             float *dst = a.part + (int64_t)(g + blk) * D::SLOT, *at = dst + wave * CT * 1024 + 4 * lane;
 #pragma unroll
-            for (int c = 0; c < CT; ++c)
+            for (int c = 0; c < CT; ++c) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    f32x4 v;
+                    __builtin_amdgcn_sched_barrier(0);
+                    f32x4 v = acc_read(o[c][4 * q], o[c][4 * q + 1], o[c][4 * q + 2], o[c][4 * q + 3]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = FP8 ? o[c][4 * q + i] * f * half_off : o[c][4 * q + i] * f;
+                    for (int k = 0; k < 4; ++k) v[k] = FP8 ? v[k] * by * half_off : v[k] * by;
                     *reinterpret_cast<f32x4 *>(at + (c * 4 + q) * 256) = v;
                 }
+            }
             if (hf == 0) *reinterpret_cast<float2 *>(dst + SHD_ROWS * RANK + 2 * (32 * wave + n)) = make_float2(m, l);
         }
     }
