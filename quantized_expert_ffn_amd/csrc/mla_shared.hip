@@ -28,10 +28,12 @@ struct Shd {
     static constexpr int CB = (RANK + MLA_ROPE) / 64;   // 128-byte lines of a token in LDS, where codes are widened
     static constexpr int KS = (RANK + MLA_ROPE) / 16;   // matrix steps of a score
     static constexpr int CT = RANK / 32;                // 32-column tiles of the output
-    static constexpr int RING = 4;
+    static constexpr int RING = FP8 ? 3 : 4;
     static constexpr int TILE = SHD_TILE * CB * 128;
-    static constexpr int L_ID = RING * TILE;                    // int32 [RING][4 wavefronts][64]: page ids of tiles to come
-    static constexpr int L_SCALE = L_ID + RING * 1024;          // float [RING][32]: E4M3 scales
+    static constexpr int L_ID = RING * TILE;                    // int32 [4][4 wavefronts][64]: page ids of tiles to come
+    // codes as they come, [2][4 wavefronts]: lines of 1 KiB, then 256 bytes of scales
+    static constexpr int LINES = ROW / 128, RAW = LINES * 1024 + 256, L_RAW = L_ID + 4 * 1024;
+    static constexpr int L_SCALE = L_RAW + (FP8 ? 8 * RAW : 0); // float [RING][32]: E4M3 scales
     static constexpr int L_EXP = L_SCALE + RING * 4 * SHD_TILE; // float [RING][32]: their exponents
     static constexpr int L_FRAC = L_EXP + RING * 4 * SHD_TILE;  // float [RING][32]: and fractions
     static constexpr int LDS = L_FRAC + RING * 4 * SHD_TILE;
@@ -129,7 +131,9 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
     }                                                                                     // tokens 8 .. 15 at va ^ 16 + 1 KiB lines
     // ---- the tiles on their way: a thread loads chunk lane % 8 of every line of token lt
     const int lt = 8 * wave + (lane >> 3), lf = shd_swz(lt), chunk = (lane & 7) ^ lf;
-    auto base_of = [](int tile) { return (uint32_t)(tile & (D::RING - 1)) * D::TILE; };
+    auto slot_in_ring = [](int tile) { return (uint32_t)tile % (uint32_t)D::RING; };
+    auto base_of = [&](int tile) { return slot_in_ring(tile) * D::TILE; };
+    auto scale_of = [&](int tile) { return 4 * slot_in_ring(tile) * SHD_TILE; };
     struct Place {
         int page, in;
     };
@@ -142,52 +146,49 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
         bad_page |= bad;
         return (int64_t)(bad ? 0 : id) * a.c.page + p.in;
     };
-    // plain rows: page ids go to LDS two tiles before the rows do
+    // page ids go to LDS two tiles before the rows do
     const uint32_t id_at = D::L_ID + wave * 256;
-    auto issue_id = [&](int tile) { load_word_to_lds(a.c.table + place(tile).page, id_at + (tile & (D::RING - 1)) * 1024); };
+    auto issue_id = [&](int tile) { load_word_to_lds(a.c.table + place(tile).page, id_at + (tile & 3) * 1024); };
+    // plain rows go to their place in the ring, codes to one of two buffers
+    constexpr int OPS = FP8 ? D::LINES + 1 : D::LINES;   // loads of a tile
+    auto raw_of = [&](int tile) { return (uint32_t)(D::L_RAW + ((tile & 1) * 4 + wave) * D::RAW); };
     auto issue = [&](int tile) {
-        const int id = lds_read<int>(id_at + (tile & (D::RING - 1)) * 1024 + 4 * lane);
-        const uint8_t *src = a.c.pages + slot_of(id, place(tile)) * D::ROW + 16 * chunk;
-        const uint32_t dst = base_of(tile) + wave * D::CB * 1024;
+        const int id = lds_read<int>(id_at + (tile & 3) * 1024 + 4 * lane);
+        const int64_t slot = slot_of(id, place(tile));
+        const uint8_t *src = a.c.pages + slot * D::ROW + 16 * (FP8 ? lane & 7 : chunk);
+        const uint32_t dst = FP8 ? raw_of(tile) : base_of(tile) + wave * D::CB * 1024;
         load_to_lds<0>(src, dst);
         load_to_lds<128>(src, dst, 1024);
         load_to_lds<256>(src, dst, 2048);
-        load_to_lds<384>(src, dst, 3 * 1024);
-        load_to_lds<512>(src, dst, 4 * 1024);
-        if constexpr (D::CB > 5) {
+        if constexpr (D::LINES > 3) {
+            load_to_lds<384>(src, dst, 3 * 1024);
+            load_to_lds<512>(src, dst, 4 * 1024);
+        }
+        if constexpr (D::LINES > 5) {
             load_to_lds<640>(src, dst, 5 * 1024);
             load_to_lds<768>(src, dst, 6 * 1024);
             load_to_lds<896>(src, dst, 7 * 1024);
             load_to_lds<1024>(src, dst, 8 * 1024);
         }
+        if constexpr (FP8) load_word_to_lds(a.c.scale + slot, dst + D::LINES * 1024);
     };
-    // codes: through registers, widened on the way
-    constexpr int CODES = FP8 ? RANK / 128 : 1;
-    u32x4 codes[CODES];
-    x8<T> key;
-    float token_scale = 0.0f;
-    int id_next = 0;
-    auto fetch_id = [&](int tile) { id_next = a.c.table[place(tile).page]; };
-    auto fetch = [&](int tile) {   // with the id that fetch_id has fetched
-        const int64_t slot = slot_of(id_next, place(tile));
-        const uint8_t *src = a.c.pages + slot * D::ROW;
-#pragma unroll
-        for (int i = 0; i < CODES; ++i) codes[i] = *reinterpret_cast<const u32x4 *>(src + 16 * (lane & 7) + 128 * i);
-        key = *reinterpret_cast<const x8<T> *>(src + RANK + 16 * (lane & 7));
-        token_scale = a.c.scale[slot];
-    };
-    auto put = [&](int tile) {
-        const uint32_t dst = base_of(tile) + wave * D::CB * 1024 + (lane >> 3) * 128, at = 4 * ((tile & (D::RING - 1)) * SHD_TILE + lt);
-        const uint32_t line = dst + ((lane & 7) >> 2) * 1024;
-#pragma unroll
-        for (int i = 0; i < CODES; ++i) {   // sixteen codes are chunks 2 c and 2 c + 1 of the widened row, c = lane % 8 + 8 i
-            lds_write(line + (((2 * lane & 7) ^ lf) << 4), widen8<T>(u32x2{codes[i][0], codes[i][1]}), 2048 * i);
-            lds_write(line + (((2 * lane + 1 & 7) ^ lf) << 4), widen8<T>(u32x2{codes[i][2], codes[i][3]}), 2048 * i);
+    // A line of a thread's codes, its own of the loads above, widened into the ring: sixteen codes are chunks 2 c and 2 c + 1
+    // of a row, c = lane % 8 + 8 line.  The last line is the key, then the scale follows.
+    auto widen = [&](int tile, int line) {
+        const uint32_t raw = raw_of(tile) + 16 * lane, dst = base_of(tile) + wave * D::CB * 1024 + (lane >> 3) * 128;
+        const u32x4 v = lds_read<u32x4>(raw, 1024 * line);
+        if (line < D::LINES - 1) {
+            const uint32_t at = dst + ((lane & 7) >> 2) * 1024;
+            lds_write(at + ((((2 * lane) & 7) ^ lf) << 4), widen8<T>(u32x2{v[0], v[1]}), 2048 * line);
+            lds_write(at + ((((2 * lane + 1) & 7) ^ lf) << 4), widen8<T>(u32x2{v[2], v[3]}), 2048 * line);
+        } else {
+            lds_write(dst + (chunk << 4), v, (D::CB - 1) * 1024);
+            const float sc = lds_read<float>(raw_of(tile) + D::LINES * 1024 + 4 * lane);
+            const uint32_t at = scale_of(tile) + 4 * lt;
+            lds_write<float>(D::L_SCALE + at, sc);
+            lds_write<float>(D::L_FRAC + at, __builtin_amdgcn_frexp_mantf(sc));
+            lds_write<float>(D::L_EXP + at, sc == 0.0f ? NEG : (float)__builtin_amdgcn_frexp_expf(sc));
         }
-        lds_write(dst + (chunk << 4), key, (D::CB - 1) * 1024);
-        lds_write<float>(D::L_SCALE + at, token_scale);
-        lds_write<float>(D::L_FRAC + at, __builtin_amdgcn_frexp_mantf(token_scale));
-        lds_write<float>(D::L_EXP + at, token_scale == 0.0f ? NEG : (float)__builtin_amdgcn_frexp_expf(token_scale));
     };
     // A tile that some rows see only in part: values that are not finite would reach rows that do not see them.
     auto clear = [&](int tile, int from) {
@@ -211,14 +212,10 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
         const int64_t row = (int64_t)blk * SHD_ROWS + 32 * wave + n, wave_row = (int64_t)blk * SHD_ROWS + 32 * wave;
         const bool works = wave_row < rows;
         const int64_t at_row = row < rows ? row : rows - 1;
-        if constexpr (!FP8) {
-            issue_id(lo);
-            issue_id(lo + 1);
-            issue_id(lo + 2);
-            issue_id(lo + 3);
-        } else {
-            fetch_id(lo);
-        }
+        issue_id(lo);
+        issue_id(lo + 1);
+        issue_id(lo + 2);
+        issue_id(lo + 3);
         x8<T> qf[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s)
@@ -238,21 +235,18 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
 #pragma unroll
         for (int s = 0; s < KS; ++s) arrived(qf[s]);
         wait_vm<0>();
-        if constexpr (!FP8) {
-            issue(lo);
-            issue(lo + 1);
-            issue(lo + 2);
-            issue_id(lo + 4);
-        } else {
-            fetch(lo);
-            fetch_id(lo + 1);
-            put(lo);
-            fetch(lo + 1);
-            fetch_id(lo + 2);
-            put(lo + 1);
-            fetch(lo + 2);
-            fetch_id(lo + 3);
+        issue(lo);
+        issue(lo + 1);
+        if constexpr (FP8) {
+            wait_vm<0>();
+#pragma unroll
+            for (int line = 0; line < D::LINES; ++line) {
+                widen(lo, line);
+                widen(lo + 1, line);
+            }
         }
+        issue(lo + 2);
+        issue_id(lo + 4);
 
         f32x16 o[CT];
 #pragma unroll
@@ -266,8 +260,8 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
         bool moved = false;
         x8<T> p[2], pn[2];
 
-        // ---- scores of a tile
-        auto score = [&](int tile) {
+        // ---- scores of a tile; between the products, the codes of the one after it are widened
+        auto score = [&](int tile, bool widens) {
             const uint32_t base = base_of(tile);
             uint32_t kb[4];
 #pragma unroll
@@ -275,7 +269,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = 0.0f;
             // operands AHEAD reads before their products
-            constexpr int AHEAD = FP8 && RANK == 512 ? 2 : 4;
+            constexpr int AHEAD = 4;
             u32x4 ahead[2][AHEAD];
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) ahead[0][i] = lds_read<u32x4>(kb[i]);
@@ -289,13 +283,14 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
                     settled(s);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const f32x4 v = lds_read<f32x4>(D::L_SCALE + 16 * hf + 4 * (tile & (D::RING - 1)) * SHD_TILE, 32 * q);
+                        const f32x4 v = lds_read<f32x4>(D::L_SCALE + 16 * hf + scale_of(tile), 32 * q);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) s[4 * q + i] *= v[i];
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) mfma_v<T>(s, __builtin_bit_cast(x8<T>, ahead[(c / AHEAD) & 1][i]), qf[c + i]);
+                if (FP8 && widens && c / AHEAD < D::LINES) widen(tile + 1, c / AHEAD);
             }
             __builtin_amdgcn_sched_barrier(0);
             const int t0 = tile * SHD_TILE;
@@ -327,7 +322,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
                     float topv = NEG;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const f32x4 e = lds_read<f32x4>(D::L_EXP + 16 * hf + 4 * (tile & (D::RING - 1)) * SHD_TILE, 32 * q);
+                        const f32x4 e = lds_read<f32x4>(D::L_EXP + 16 * hf + scale_of(tile), 32 * q);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) topv = fmaxf(topv, __builtin_fmaf(s[4 * q + i], scale, e[i]));
                     }
@@ -348,7 +343,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
                         l += w;
                         if (FP8) {
                             if (r % 4 == 0) {
-                                const int at = 16 * hf + 4 * (tile & (D::RING - 1)) * SHD_TILE;
+                                const uint32_t at = 16 * hf + scale_of(tile);
                                 frac = lds_read<f32x4>(D::L_FRAC + at, 8 * r);
                                 expo = lds_read<f32x4>(D::L_EXP + at, 8 * r);
                             }
@@ -399,32 +394,32 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
             __builtin_amdgcn_sched_barrier(0);
         };
 
-        if constexpr (!FP8) wait_vm<2 * D::CB + 1>();
+        if constexpr (!FP8) wait_vm<2 * OPS + 1>();
         barrier_lds();
-        score(lo);
+        score(lo, false);
 #pragma unroll
         for (int c = 0; c < CT; ++c) soften(lo, c);
         take();
         int i = lo;
         for (; i + 1 < hi; ++i) {
+            // plain rows: tile i + 1 has come, i + 2 is out
             if constexpr (!FP8) {
                 if (i + 2 < hi)
-                    wait_vm<D::CB + 1>();
+                    wait_vm<OPS + 1>();
                 else
                     wait_vm<0>();
             }
             barrier_lds();   // tile i + 1 is there, and every wavefront is done with tile i - 1
-            if constexpr (!FP8) {
-                if (i + 3 < hi) issue(i + 3);
-                issue_id(i + 5);
-            }
+            if (i + 3 < hi) issue(i + 3);
+            issue_id(i + 5);
             if ((i + 1) * SHD_TILE > partly) clear(i, max(0, block_seen - i * SHD_TILE));
-            score(i + 1);
-            if constexpr (FP8) {
-                put(i + 2);
-                fetch(i + 3);
-                fetch_id(i + 4);
+            if constexpr (FP8) {   // the codes of tile i + 2 have come
+                if (i + 3 < hi)
+                    wait_vm<OPS + 1>();
+                else
+                    wait_vm<1>();
             }
+            score(i + 1, true);
             values(i, std::true_type());
             take();
         }
