@@ -152,31 +152,55 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
     // plain rows go to their place in the ring, codes to one of two buffers
     constexpr int OPS = FP8 ? D::LINES + 1 : D::LINES;   // loads of a tile
     auto raw_of = [&](int tile) { return (uint32_t)(D::L_RAW + ((tile & 1) * 4 + wave) * D::RAW); };
-    auto issue = [&](int tile) {
+    struct Aim {
+        const uint8_t *src;
+        const float *scale;
+        uint32_t dst;
+    };
+    auto aim = [&](int tile) {
         const int id = lds_read<int>(id_at + (tile & 3) * 1024 + 4 * lane);
         const int64_t slot = slot_of(id, place(tile));
-        const uint8_t *src = a.c.pages + slot * D::ROW + 16 * (FP8 ? lane & 7 : chunk);
-        const uint32_t dst = FP8 ? raw_of(tile) : base_of(tile) + wave * D::CB * 1024;
-        load_to_lds<0>(src, dst);
-        load_to_lds<128>(src, dst, 1024);
-        load_to_lds<256>(src, dst, 2048);
-        if constexpr (D::LINES > 3) {
-            load_to_lds<384>(src, dst, 3 * 1024);
-            load_to_lds<512>(src, dst, 4 * 1024);
+        return Aim{a.c.pages + slot * D::ROW + 16 * (FP8 ? lane & 7 : chunk), FP8 ? a.c.scale + slot : nullptr,
+                   FP8 ? raw_of(tile) : base_of(tile) + wave * D::CB * 1024};
+    };
+    auto issue_op = [](const Aim &x, int op) {   // one of OPS
+        switch (op) {
+        case 0: load_to_lds<0>(x.src, x.dst); break;
+        case 1: load_to_lds<128>(x.src, x.dst, 1024); break;
+        case 2: load_to_lds<256>(x.src, x.dst, 2048); break;
+        case 3:
+            if constexpr (D::LINES > 3) load_to_lds<384>(x.src, x.dst, 3 * 1024);
+            break;
+        case 4:
+            if constexpr (D::LINES > 3) load_to_lds<512>(x.src, x.dst, 4 * 1024);
+            break;
+        case 5:
+            if constexpr (D::LINES > 5) load_to_lds<640>(x.src, x.dst, 5 * 1024);
+            break;
+        case 6:
+            if constexpr (D::LINES > 5) load_to_lds<768>(x.src, x.dst, 6 * 1024);
+            break;
+        case 7:
+            if constexpr (D::LINES > 5) load_to_lds<896>(x.src, x.dst, 7 * 1024);
+            break;
+        default:
+            if constexpr (D::LINES > 5) load_to_lds<1024>(x.src, x.dst, 8 * 1024);
         }
-        if constexpr (D::LINES > 5) {
-            load_to_lds<640>(src, dst, 5 * 1024);
-            load_to_lds<768>(src, dst, 6 * 1024);
-            load_to_lds<896>(src, dst, 7 * 1024);
-            load_to_lds<1024>(src, dst, 8 * 1024);
-        }
-        if constexpr (FP8) load_word_to_lds(a.c.scale + slot, dst + D::LINES * 1024);
+    };
+    auto issue_scale = [&](const Aim &x) {
+        if constexpr (FP8) load_word_to_lds(x.scale, x.dst + D::LINES * 1024);
+    };
+    auto issue = [&](int tile) {
+        const Aim x = aim(tile);
+#pragma unroll
+        for (int op = 0; op < D::LINES; ++op) issue_op(x, op);
+        issue_scale(x);
     };
     // A line of a thread's codes, its own of the loads above, widened into the ring: sixteen codes are chunks 2 c and 2 c + 1
     // of a row, c = lane % 8 + 8 line.  The last line is the key, then the scale follows.
-    auto widen = [&](int tile, int line) {
-        const uint32_t raw = raw_of(tile) + 16 * lane, dst = base_of(tile) + wave * D::CB * 1024 + (lane >> 3) * 128;
-        const u32x4 v = lds_read<u32x4>(raw, 1024 * line);
+    auto raw_line = [&](int tile, int line) { return lds_read<u32x4>(raw_of(tile) + 16 * lane, 1024 * line); };
+    auto widen = [&](int tile, int line, u32x4 v) {
+        const uint32_t dst = base_of(tile) + wave * D::CB * 1024 + (lane >> 3) * 128;
         if (line < D::LINES - 1) {
             const uint32_t at = dst + ((lane & 7) >> 2) * 1024;
             lds_write(at + ((((2 * lane) & 7) ^ lf) << 4), widen8<T>(u32x2{v[0], v[1]}), 2048 * line);
@@ -241,12 +265,11 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
             wait_vm<0>();
 #pragma unroll
             for (int line = 0; line < D::LINES; ++line) {
-                widen(lo, line);
-                widen(lo + 1, line);
+                widen(lo, line, raw_line(lo, line));
+                widen(lo + 1, line, raw_line(lo + 1, line));
             }
         }
         issue(lo + 2);
-        issue_id(lo + 4);
 
         f32x16 o[CT];
 #pragma unroll
@@ -260,26 +283,29 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
         bool moved = false;
         x8<T> p[2], pn[2];
 
-        // ---- scores of a tile; between the products, the codes of the one after it are widened
-        auto score = [&](int tile, bool widens) {
+        // ---- scores of a tile.  Between the products the loads of the tile after the next go out (all of them at once would
+        // hold the wavefront up; behind the last tile: rows that are not used), and the codes of the next are widened.
+        auto score = [&](int tile, auto steady) {
+            constexpr bool STEADY = decltype(steady)::value;
+            Aim x{};
+            if constexpr (STEADY) x = aim(tile + 2);
             const uint32_t base = base_of(tile);
             uint32_t kb[4];
 #pragma unroll
             for (int v = 0; v < 4; ++v) kb[v] = base + (ka ^ 32 * v);
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = 0.0f;
-            // operands AHEAD reads before their products
-            constexpr int AHEAD = 4;
-            u32x4 ahead[2][AHEAD];
+            // operands four reads before their products
+            u32x4 w[6], raw{};
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) ahead[0][i] = lds_read<u32x4>(kb[i]);
+            for (int i = 0; i < 4; ++i) w[i] = lds_read<u32x4>(kb[i]);
+            if (STEADY && FP8) raw = raw_line(tile + 1, 0);
 #pragma unroll
-            for (int c = 0; c < KS; c += AHEAD) {
+            for (int k = 0; k < KS; k += 2) {
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = c + AHEAD; i < KS && i < c + 2 * AHEAD; ++i)
-                    ahead[(c / AHEAD + 1) & 1][i % AHEAD] = lds_read<u32x4>(kb[i & 3], (i >> 2) * 1024);
-                if (FP8 && c == RANK / 16) {
+                for (int i = k + 4; i < k + 6 && i < KS; ++i) w[i % 6] = lds_read<u32x4>(kb[i & 3], (i >> 2) * 1024);
+                if (FP8 && k == RANK / 16) {
                     settled(s);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -289,9 +315,18 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < AHEAD; ++i) mfma_v<T>(s, __builtin_bit_cast(x8<T>, ahead[(c / AHEAD) & 1][i]), qf[c + i]);
-                if (FP8 && widens && c / AHEAD < D::LINES) widen(tile + 1, c / AHEAD);
+                for (int i = k; i < k + 2; ++i) mfma_v<T>(s, __builtin_bit_cast(x8<T>, w[i % 6]), qf[i]);
+                if (STEADY && k % 4 == 0 && k / 4 < D::LINES) {
+                    issue_op(x, k / 4);
+                    if (FP8) {
+                        widen(tile + 1, k / 4, raw);
+                        if (k / 4 + 1 < D::LINES) raw = raw_line(tile + 1, k / 4 + 1);
+                    }
+                }
             }
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (STEADY) issue_scale(x);
+            issue_id(tile + 4);
             __builtin_amdgcn_sched_barrier(0);
             const int t0 = tile * SHD_TILE;
             if (t0 + SHD_TILE > wave_seen) {
@@ -377,49 +412,35 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
                 const u32x2 v0 = lds_read_tr16(vb[c & 1], imm), v1 = lds_read_tr16(vb[2 + (c & 1)], imm);
                 return u32x4{v0[0], v0[1], v1[0], v1[1]};
             };
-            u32x4 ahead[2][2];
+            // all columns by the first sixteen tokens, then by the others, so that no product waits for the one before it;
+            // operands three reads ahead
+            u32x4 w[4];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) ahead[0][k] = read(0, k);
+            for (int i = 0; i < 3; ++i) w[i] = read(i % CT, i / CT);
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                __builtin_amdgcn_sched_barrier(0);
-                if (c + 1 < CT) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) ahead[(c + 1) & 1][k] = read(c + 1, k);
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) o[c] = mfma32<T>(__builtin_bit_cast(x8<T>, ahead[c & 1][k]), p[k], o[c]);
-                if constexpr (decltype(next)::value) soften(tile + 1, c);
+            for (int i = 0; i < 2 * CT; ++i) {
+                if (i % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+                if (i + 3 < 2 * CT) w[(i + 3) & 3] = read((i + 3) % CT, (i + 3) / CT);
+                o[i % CT] = mfma32<T>(__builtin_bit_cast(x8<T>, w[i & 3]), p[i / CT], o[i % CT]);
+                if constexpr (decltype(next)::value)
+                    if (i % 2) soften(tile + 1, i / 2);
             }
             __builtin_amdgcn_sched_barrier(0);
         };
 
-        if constexpr (!FP8) wait_vm<2 * OPS + 1>();
+        if constexpr (!FP8) wait_vm<2 * OPS>();
         barrier_lds();
-        score(lo, false);
+        score(lo, std::false_type());
 #pragma unroll
         for (int c = 0; c < CT; ++c) soften(lo, c);
         take();
         int i = lo;
         for (; i + 1 < hi; ++i) {
-            // plain rows: tile i + 1 has come, i + 2 is out
-            if constexpr (!FP8) {
-                if (i + 2 < hi)
-                    wait_vm<OPS + 1>();
-                else
-                    wait_vm<0>();
-            }
+            // plain rows: tile i + 1 has come, i + 2 is out; codes: those of tile i + 2 have come
+            wait_vm<FP8 ? 1 : OPS + 1>();
             barrier_lds();   // tile i + 1 is there, and every wavefront is done with tile i - 1
-            if (i + 3 < hi) issue(i + 3);
-            issue_id(i + 5);
             if ((i + 1) * SHD_TILE > partly) clear(i, max(0, block_seen - i * SHD_TILE));
-            if constexpr (FP8) {   // the codes of tile i + 2 have come
-                if (i + 3 < hi)
-                    wait_vm<OPS + 1>();
-                else
-                    wait_vm<1>();
-            }
-            score(i + 1, true);
+            score(i + 1, std::true_type());
             values(i, std::true_type());
             take();
         }
@@ -455,59 +476,95 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
     if (bad_page) raise_status(a.status, ST_BADPAGE);
 }
 
-// Joins the partial results of 32 rows by 8 columns: out = sum 2^{m_i - M} l_i
-// o_i / sum 2^{m_i - M} l_i, those over the prefix in order, then those of the
-// rows' sequences.  A workgroup's W wavefronts take every W-th each.
-template <class T, int RANK, int W>
-__global__ __launch_bounds__(64 * W) void k_mla_shared_join(MlaSharedArgs a, Units u) {
-    constexpr int SLOT = SHD_ROWS * RANK + 2 * SHD_ROWS;
+// Joins partial results: out = sum 2^{m_i - M} l_i o_i / sum 2^{m_i - M} l_i,
+// those over the prefix in order, then those of the rows' sequences.  A
+// wavefront has 32 rows by 8 COLS columns.  W > 1: a workgroup's wavefronts take every
+// W-th partial each of one such piece, for few rows in many parts.
+template <class T, int RANK, int W, int COLS>
+__global__ __launch_bounds__(W > 1 ? 64 * W : 256) void k_mla_shared_join(MlaSharedArgs a, Units u) {
+    constexpr int SLOT = SHD_ROWS * RANK + 2 * SHD_ROWS, PIECES = RANK / 8 / COLS;
     constexpr float NEG = -__builtin_inff();
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 31, cq = blockIdx.x % (RANK / 8);
-    const int64_t rows = (int64_t)a.batch * a.n_q * a.heads, row = (int64_t)(blockIdx.x / (RANK / 8)) * 32 + n;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 31;
+    const int64_t id = W > 1 ? blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
+    const int piece = (int)(id % PIECES), part = W > 1 ? wave : 0;
+    const int64_t rows = (int64_t)a.batch * a.n_q * a.heads, row = id / PIECES * 32 + n;
+    if (W == 1 && id / PIECES * 32 >= rows) return;
     const int64_t at_row = row < rows ? row : rows - 1;
-    __shared__ f32x4 so[W][64];
-    __shared__ float sm[W][64], sl[W][64];
+    __shared__ f32x4 so[W > 1 ? W : 1][64];
+    __shared__ float sm[W > 1 ? W : 1][64], sl[W > 1 ? W : 1][64];
     float m = NEG, l = 0.0f;
-    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto add = [&](const float *at, const float *ml) {
-        const float2 x = *reinterpret_cast<const float2 *>(ml);
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(at);
-        const float to = fmaxf(m, x.x), old = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-        const float f = x.y * (x.x == to ? 1.0f : __builtin_amdgcn_exp2f(x.x - to));
-        m = to;
-        l = __builtin_fmaf(l, old, f);
+    f32x4 o[COLS];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(v[i], f, o[i] * old);
+    for (int c = 0; c < COLS; ++c) o[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // AHEAD partials at a time; those past the last one again, with no weight
+    constexpr int AHEAD = W > 1 ? 4 : 2;
+    auto add = [&](int first, int count, auto at) {
+        for (int i = first; i < count; i += AHEAD * W) {
+            float2 ml[AHEAD];
+            f32x4 v[AHEAD][COLS];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const float *base, *stats;
+                at(min(i + k * W, count - 1), base, stats);
+                ml[k] = *reinterpret_cast<const float2 *>(stats);
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) v[k][c] = *reinterpret_cast<const f32x4 *>(base + 256 * c);
+            }
+            float to = m;
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) to = fmaxf(to, ml[k].x);
+            const float old = m == to ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+            m = to;
+            l *= old;
+#pragma unroll
+            for (int c = 0; c < COLS; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[c][j] *= old;
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (i + k * W < count) {
+                    const float f = ml[k].y * (ml[k].x == to ? 1.0f : __builtin_amdgcn_exp2f(ml[k].x - to));
+                    l += f;
+#pragma unroll
+                    for (int c = 0; c < COLS; ++c)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[c][j] = __builtin_fmaf(v[k][c][j], f, o[c][j]);
+                }
+        }
     };
     {
         const int64_t blk = row / SHD_ROWS, unit = blk * u.tiles;
         const int r = (int)(row - blk * SHD_ROWS), g0 = u.owner(unit), g1 = u.owner(unit + u.tiles - 1);
-        for (int g = g0 + wave; g <= g1; g += W) {
-            const float *slot = a.part + (g + blk) * SLOT;
-            add(slot + (r / 32 * (RANK / 8) + cq) * 256 + 4 * lane, slot + SHD_ROWS * RANK + 2 * r);
-        }
+        const int col = (r / 32 * (RANK / 8) + piece * COLS) * 256 + 4 * lane, stat = SHD_ROWS * RANK + 2 * r;
+        add(part, g1 - g0 + 1, [&](int i, const float *&base, const float *&stats) {
+            const float *slot = a.part + (g0 + i + blk) * SLOT;
+            base = slot + col;
+            stats = slot + stat;
+        });
     }
     if (a.own) {
         const int per = a.n_q * a.heads, b = (int)(at_row / per), w = (int)(at_row - (int64_t)b * per);
         const int block = w / a.p.rows, r = w - block * a.p.rows;
         const int32_t *plan = reinterpret_cast<const int32_t *>(a.own) + 2 * b;
         const int g0 = plan[0], g1 = plan[1];
-        const int at = (r / 32 * (RANK / 8) + cq) * 256 + 4 * (r % 32 + 32 * (lane >> 5)), ml = a.p.rows * RANK + 2 * r;
-        for (int g = g0 + wave; g <= g1; g += W) {
+        const int col = (r / 32 * (RANK / 8) + piece * COLS) * 256 + 4 * (r % 32 + 32 * (lane >> 5)), stat = a.p.rows * RANK + 2 * r;
+        add(part, g1 - g0 + 1, [&](int i, const float *&base, const float *&stats) {
             const float *slot = g0 == g1 ? a.full + ((int64_t)b * a.p.blocks + block) * a.p.slot
-                                         : a.own + a.p.first + (2 * ((int64_t)block * a.p.groups + g) + (g == g0 ? 1 : 0)) * a.p.slot;
-            add(slot + at, slot + ml);
-        }
+                                         : a.own + a.p.first + (2 * ((int64_t)block * a.p.groups + g0 + i) + (i == 0 ? 1 : 0)) * a.p.slot;
+            base = slot + col;
+            stats = slot + stat;
+        });
     }
-    if (W > 1) {
-        so[wave][lane] = o;
+    if constexpr (W > 1) {
+        static_assert(COLS == 1, "one piece a workgroup");
+        so[wave][lane] = o[0];
         sm[wave][lane] = m;
         sl[wave][lane] = l;
         __syncthreads();
         if (wave) return;
 #pragma unroll
         for (int w = 1; w < W; ++w) m = fmaxf(m, sm[w][lane]);
-        o = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        o[0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         l = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
@@ -515,16 +572,19 @@ __global__ __launch_bounds__(64 * W) void k_mla_shared_join(MlaSharedArgs a, Uni
             const f32x4 v = so[w][lane];
             l = __builtin_fmaf(sl[w][lane], f, l);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(v[i], f, o[i]);
+            for (int i = 0; i < 4; ++i) o[0][i] = __builtin_fmaf(v[i], f, o[0][i]);
         }
     }
     if (row >= rows) return;
     const float f = l == 0.0f ? 0.0f : 1.0f / l;
-    x4<T> v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (T)(o[i] * f);
-    *reinterpret_cast<x4<T> *>(static_cast<T *>(a.out) + row * RANK + 8 * cq + 4 * (lane >> 5)) = v;
-    if (a.lse && cq == 0 && lane < 32) a.lse[row] = l == 0.0f ? NEG : (m + __builtin_amdgcn_logf(l)) * LN2;
+    for (int c = 0; c < COLS; ++c) {
+        x4<T> v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = (T)(o[c][i] * f);
+        *reinterpret_cast<x4<T> *>(static_cast<T *>(a.out) + row * RANK + 8 * (piece * COLS + c) + 4 * (lane >> 5)) = v;
+    }
+    if (a.lse && piece == 0 && lane < 32) a.lse[row] = l == 0.0f ? NEG : (m + __builtin_amdgcn_logf(l)) * LN2;
 }
 
 // Calls f with the type, rank and format of the dims as types.
@@ -538,6 +598,8 @@ hipError_t with_shape(const coli_mla_dims &d, F f) {
 }
 
 }  // namespace
+
+constexpr int JOIN_DEEP = 32, JOIN_COLS = 4;
 
 size_t mla_shared_part_bytes(const coli_mla_dims &d, int64_t rows, int prefix) {
     // slots are counted by workgroup + block of rows: a bound that grows with each argument
@@ -561,8 +623,14 @@ hipError_t launch_mla_shared_join(const MlaSharedArgs &a, const coli_mla_dims &d
     const Units u = shd_units(rows, a.prefix);
     return with_shape(d, [&](auto shape) {
         using D = decltype(shape);
-        const dim3 grid((uint32_t)((rows + 31) / 32 * (D::RANK / 8)));
-        hipLaunchKernelGGL((k_mla_shared_join<typename D::T, D::RANK, 4>), grid, dim3(256), 0, st, a, u);
+        const int64_t groups = (rows + 31) / 32, pieces = D::RANK / 8;
+        // parts of a row: those of the prefix, and of its own tokens
+        if (groups <= JOIN_DEEP)
+            hipLaunchKernelGGL((k_mla_shared_join<typename D::T, D::RANK, 16, 1>), dim3((uint32_t)(groups * pieces)), dim3(1024), 0, st,
+                               a, u);
+        else
+            hipLaunchKernelGGL((k_mla_shared_join<typename D::T, D::RANK, 1, JOIN_COLS>),
+                               dim3((uint32_t)((groups * (pieces / JOIN_COLS) + 3) / 4)), dim3(256), 0, st, a, u);
         return hipGetLastError();
     });
 }
