@@ -1,55 +1,310 @@
 // Products of 8-bit codes with scales for each token and output channel
-// (coli_w8_linear): out[t, o] = s_t s_o sum_k q_tk w_ok + bias_o.
-//
-// v_mfma_i32_32x32x32_i8 with the channels as its rows and the tokens as its
-// columns: a wavefront takes 32 of each, its operands straight from memory.
+// (coli_w8_linear): out[t, o] = s_t s_o sum_k q_tk w_ok + bias_o, on the int8
+// matrix cores, with the channels as rows and the tokens as columns, so that a
+// lane's results are consecutive channels of one token.  Sums are exact, so
+// how they are split changes nothing.
 #include "kernels.h"
 #include "mfma.h"
+#include "mla_mfma.h"
 #include "w8.h"
 
 namespace coli {
 namespace {
 
-template <class T>
-__global__ __launch_bounds__(256) void k_w8_linear(W8LinearArgs a) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 31, hf = lane >> 5;
-    const int across = (a.n_out + 127) / 128;
-    const int o0 = (blockIdx.x % across * 4 + wave) * 32, t0 = blockIdx.x / across * 32;
-    if (o0 >= a.n_out) return;
-    const int8_t *w = a.w + (int64_t)min(o0 + n, a.n_out - 1) * a.k;
-    const int8_t *x = a.x + (int64_t)min(t0 + n, a.tokens - 1) * a.x_stride;
-    i32x16 acc = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-    for (int k = 0; k < a.k; k += 32) {
-        i32x4 av = {0, 0, 0, 0}, bv = {0, 0, 0, 0};
-        if (k + 16 * hf < a.k) {
-            av = *reinterpret_cast<const i32x4 *>(w + k + 16 * hf);
-            bv = *reinterpret_cast<const i32x4 *>(x + k + 16 * hf);
-        }
-        acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(av, bv, acc, 0, 0, 0);
-    }
-    const int t = t0 + n;
-    if (t >= a.tokens) return;
-    const float s = a.x_scale[t];
-    T *out = static_cast<T *>(a.out) + (int64_t)t * a.o_stride;
+typedef int32_t i32x4v __attribute__((ext_vector_type(4)));
+
+// Where chunks behind the end of a row read.
+__device__ const uint4 w8_zeros[8] = {};
+
+// A result: three roundings to binary32 of the product, one with a bias.
+__device__ __forceinline__ float finish(int32_t sum, float st, float so, float bias, bool has_bias) {
+    const float v = (float)sum * st * so;
+    return has_bias ? v + bias : v;
+}
+
+// ---------------------------------------------------------------- few tokens
+// The weights pass once from memory to registers: a wavefront takes 16 MT
+// channels and every W-th run of four steps of 64 along k, and a workgroup's W
+// wavefronts add their sums in LDS.  Tokens (16 NT) come from the L2.
+template <class T, int MT, int NT, int W>
+__global__ __launch_bounds__(64 * W) void k_w8_few(W8LinearArgs a) {
+    constexpr int U = 4;
+    __shared__ i32x4v part[W][MT * NT][64];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, kc = 16 * (lane >> 4);
+    const int o0 = blockIdx.x * 16 * MT;
+    const int8_t *wp[MT], *xp[NT];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int o = o0 + 8 * (r / 4) + 4 * hf + r % 4;
-        if (o < a.n_out) {
-            float v = (float)acc[r] * s * a.w_scale[o];
-            if (a.bias) v += a.bias[o];
-            out[o] = (T)v;
+    for (int i = 0; i < MT; ++i) wp[i] = a.w + (int64_t)min(o0 + 16 * i + n, a.n_out - 1) * a.k + kc;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) xp[j] = a.x + (int64_t)min(16 * j + n, a.tokens - 1) * a.x_stride + kc;
+    i32x4v acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = i32x4v{0, 0, 0, 0};
+    for (int k = wave * 64 * U; k < a.k; k += W * 64 * U) {
+        i32x4v av[U][MT], bv[U][NT];
+        if (k + 64 * U <= a.k) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    av[u][i] = __builtin_nontemporal_load(reinterpret_cast<const i32x4v *>(wp[i] + k + 64 * u));
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) bv[u][j] = *reinterpret_cast<const i32x4v *>(xp[j] + k + 64 * u);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool in = k + 64 * u + kc < a.k;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) av[u][i] = in ? *reinterpret_cast<const i32x4v *>(wp[i] + k + 64 * u) : i32x4v{0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) bv[u][j] = in ? *reinterpret_cast<const i32x4v *>(xp[j] + k + 64 * u) : i32x4v{0, 0, 0, 0};
+            }
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[u][i], bv[u][j], acc[i][j], 0, 0, 0);
     }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
+    __syncthreads();
+    for (int p = wave; p < MT * NT; p += W) {
+        i32x4v sum = part[0][p][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) sum += part[w][p][lane];
+        const int t = 16 * (p % NT) + n, o = o0 + 16 * (p / NT) + 4 * (lane >> 4);
+        if (t >= a.tokens) continue;
+        const float st = a.x_scale[t];
+        T *out = static_cast<T *>(a.out) + (int64_t)t * a.o_stride;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (o + r < a.n_out) out[o + r] = (T)finish(sum[r], st, a.w_scale[o + r], a.bias ? a.bias[o + r] : 0.0f, a.bias != nullptr);
+    }
+}
+
+// ---------------------------------------------------------------- tiles
+// NW wavefronts in WM x NW / WM pieces of a tile of TM channels by TN tokens;
+// WGS workgroups fit a CU.  Steps of 128 along k, a line of every row, form one
+// stream over a workgroup's tiles, through a ring of LDS stages loaded straight
+// from memory; results pass through the stage used last, to leave in whole lines.
+template <class T_, int TM_, int TN_, int NW_, int WM_, int STAGES_, int WGS_>
+struct Tile {
+    using T = T_;
+    static constexpr int TM = TM_, TN = TN_, NW = NW_, WM = WM_, WN = NW_ / WM_, STAGES = STAGES_, WGS = WGS_;
+    static constexpr int FM = TM / WM / 32, FN = TN / WN / 32;       // 32 x 32 tiles of a wavefront
+    static constexpr int ASTAGE = TM * 128, STAGE = ASTAGE + TN * 128;
+    static constexpr int LA = TM / 8 / NW, LB = TN / 8 / NW;         // 1 KiB loads a wavefront and step
+    static constexpr int OF = sizeof(T) == 4 || FM < 2 ? 1 : 2;      // 32-channel tiles that leave together
+    static constexpr int OROW = 32 * OF * sizeof(T) + 16, OUT = NW * 32 * OROW;
+    static constexpr int L_SCALE = STAGES * STAGE;                   // float [TM]: channels' scales, then their biases
+    static constexpr int LDS = L_SCALE + 8 * TM;
+    static_assert(LA >= 1 && LB >= 1 && OUT <= STAGE && LDS * WGS <= 160 * 1024, "LDS");
+};
+
+// Lane's place in a 1 KiB load: eight rows of eight chunks, swizzled so that
+// sixteen rows' same chunk lies in sixteen groups of banks.
+__device__ __forceinline__ int swz(int r) { return 4 * ((r >> 1) & 1) + 2 * ((r >> 2) & 1) + ((r >> 3) & 1); }
+
+// Work items to XCDs: workgroups go to the eight XCDs in turn; each XCD takes
+// a contiguous run of items.
+__device__ __forceinline__ int xcd_item(int block, int total) {
+    const int share = (total + 7) / 8, rest = total - (share - 1) * 8, xcd = block & 7, nth = block >> 3;
+    return xcd < rest ? xcd * share + nth : rest * share + (xcd - rest) * (share - 1) + nth;
+}
+
+template <class D>
+__global__ __launch_bounds__(64 * D::NW, D::NW * D::WGS / 4) void k_w8_tiles(W8LinearArgs a, int m_tiles, int parts, int n_tiles, int wide_out) {
+    using T = typename D::T;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), n = lane & 31, hf = lane >> 5;
+    const int wm = wave % D::WM, wn = wave / D::WM;
+    // An XCD has all parts of few token tiles: its L2 keeps those while the weights pass through it.
+    const int id = xcd_item(blockIdx.x, gridDim.x);
+    const int across = 4 * parts, run = id / across, wide = min(4, n_tiles - 4 * run);
+    const int part = (id - run * across) / wide, t0 = (4 * run + (id - run * across) % wide) * D::TN;
+    int mt = (int)((int64_t)part * m_tiles / parts);
+    const int mt_end = (int)((int64_t)(part + 1) * m_tiles / parts), steps = (a.k + 127) / 128;
+    // ---- the stream of loads
+    const int8_t *wp[D::LA], *xp[D::LB];
+    int load_mt = mt, load_k = 0, load_slot = 0;
+    auto chunk = [&](int r) { return ((lane & 7) ^ swz(r)) << 4; };
+#pragma unroll
+    for (int i = 0; i < D::LB; ++i) {
+        const int r = (wave * D::LB + i) * 8 + (lane >> 3);
+        xp[i] = a.x + (int64_t)min(t0 + r, a.tokens - 1) * a.x_stride + chunk(r);
+    }
+    auto aim = [&] {
+#pragma unroll
+        for (int i = 0; i < D::LA; ++i) {
+            const int r = (wave * D::LA + i) * 8 + (lane >> 3);
+            wp[i] = a.w + (int64_t)min(load_mt * D::TM + r, a.n_out - 1) * a.k + chunk(r);
+        }
+    };
+    auto issue = [&] {
+        if (load_mt >= mt_end) return;
+        const uint32_t base = load_slot * D::STAGE;
+        const int k = load_k * 128;
+        if (k + 128 <= a.k) {
+#pragma unroll
+            for (int i = 0; i < D::LA; ++i) load_to_lds(wp[i] + k, base + (wave * D::LA + i) * 1024);
+#pragma unroll
+            for (int i = 0; i < D::LB; ++i) load_to_lds(xp[i] + k, base + D::ASTAGE + (wave * D::LB + i) * 1024);
+        } else {   // the last step of a row that ends inside a line: zeros behind it
+            const int8_t *zero = reinterpret_cast<const int8_t *>(w8_zeros);
+#pragma unroll
+            for (int i = 0; i < D::LA; ++i)
+                load_to_lds(k + chunk((wave * D::LA + i) * 8 + (lane >> 3)) < a.k ? wp[i] + k : zero, base + (wave * D::LA + i) * 1024);
+#pragma unroll
+            for (int i = 0; i < D::LB; ++i)
+                load_to_lds(k + chunk((wave * D::LB + i) * 8 + (lane >> 3)) < a.k ? xp[i] + k : zero,
+                            base + D::ASTAGE + (wave * D::LB + i) * 1024);
+        }
+        load_slot = load_slot == D::STAGES - 1 ? 0 : load_slot + 1;
+        if (++load_k == steps) {
+            load_k = 0;
+            ++load_mt;
+            aim();
+        }
+    };
+    aim();
+#pragma unroll
+    for (int i = 0; i < D::STAGES - 1; ++i) issue();
+    // Matrix step e of a stage takes k = 32 e + 16 hf + 0..15 of both sides.
+    uint32_t aa[4], ba[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t at = (n >> 3) * 1024 + (n & 7) * 128 + (((2 * e + hf) ^ swz(n)) << 4);
+        aa[e] = wm * D::FM * 4096 + at;
+        ba[e] = D::ASTAGE + wn * D::FN * 4096 + at;
+    }
+    float st[D::FN];
+#pragma unroll
+    for (int j = 0; j < D::FN; ++j) st[j] = a.x_scale[min(t0 + (wn * D::FN + j) * 32 + n, a.tokens - 1)];
+#pragma unroll
+    for (int j = 0; j < D::FN; ++j) arrived(st[j]);
+    int slot = 0, ready = 0;   // steps whose loads are known to have arrived
+    wait_vm<0>();
+    ready = D::STAGES - 1;
+    for (; mt < mt_end; ++mt) {
+        i32x16 acc[D::FM][D::FN];
+#pragma unroll
+        for (int i = 0; i < D::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < D::FN; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+        uint32_t base = 0;
+        for (int k = 0; k < steps; ++k) {
+            if (ready > 0)
+                --ready;
+            else if (D::STAGES > 2 && (mt + 1 < mt_end || k + 1 < steps))
+                wait_vm<(D::STAGES - 2) * (D::LA + D::LB)>();
+            else
+                wait_vm<0>();
+            barrier_lds();
+            issue();
+            base = slot * D::STAGE;
+            slot = slot == D::STAGES - 1 ? 0 : slot + 1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                i32x4 av[D::FM], bv[D::FN];
+#pragma unroll
+                for (int j = 0; j < D::FN; ++j) bv[j] = lds_read<i32x4>(base + ba[e], j * 4096);
+#pragma unroll
+                for (int i = 0; i < D::FM; ++i) av[i] = lds_read<i32x4>(base + aa[e], i * 4096);
+#pragma unroll
+                for (int i = 0; i < D::FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < D::FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(av[i], bv[j], acc[i][j], 0, 0, 0);
+            }
+        }
+        // The loads that are out, before the stores: a later count of loads must not wait for those.
+        wait_vm<0>();
+        ready = D::STAGES - 1;
+        for (int i = tid; i < D::TM; i += 64 * D::NW) {
+            const int o = min(mt * D::TM + i, a.n_out - 1);
+            lds_write<float>(D::L_SCALE + 4 * i, a.w_scale[o]);
+            lds_write<float>(D::L_SCALE + 4 * D::TM + 4 * i, a.bias ? a.bias[o] : 0.0f);
+        }
+        barrier_lds();
+        const uint32_t at = base + wave * 32 * D::OROW;
+        constexpr int VEC = 16 / sizeof(T), PER = 32 * D::OF / VEC;   // channels of 16 bytes, lanes a token's run of them
+        typedef T vec __attribute__((ext_vector_type(VEC)));
+        typedef T four __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int j = 0; j < D::FN; ++j)
+#pragma unroll
+            for (int i = 0; i < D::FM; i += D::OF) {
+#pragma unroll
+                for (int q = 0; q < 4 * D::OF; ++q) {
+                    const uint32_t ch = D::L_SCALE + 4 * ((wm * D::FM + i) * 32 + 4 * hf);
+                    const f32x4 so = lds_read<f32x4>(ch, 32 * q), b = lds_read<f32x4>(ch, 4 * D::TM + 32 * q);
+                    four v;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = (T)finish(acc[i + q / 4][j][4 * (q % 4) + k], st[j], so[k], b[k], a.bias != nullptr);
+                    lds_write(at + n * D::OROW + 4 * sizeof(T) * hf, v, 8 * sizeof(T) * q);
+                }
+                const int o = mt * D::TM + (wm * D::FM + i) * 32 + VEC * (lane % PER);
+#pragma unroll
+                for (int p = 0; p < PER / 2; ++p) {
+                    const int r = p * (64 / PER) + lane / PER, t = t0 + (wn * D::FN + j) * 32 + r;
+                    const vec v = lds_read<vec>(at + r * D::OROW + 16 * (lane % PER));
+                    if (t < a.tokens) {
+                        T *dst = static_cast<T *>(a.out) + (int64_t)t * a.o_stride + o;
+                        if (wide_out && o + VEC <= a.n_out) {
+                            *reinterpret_cast<vec *>(dst) = v;
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < VEC; ++k)
+                                if (o + k < a.n_out) dst[k] = v[k];
+                        }
+                    }
+                }
+            }
+        barrier_lds();   // the scales are read
+    }
+}
+
+template <class D>
+hipError_t tiles(const W8LinearArgs &a, hipStream_t st) {
+    const int mt = (a.n_out + D::TM - 1) / D::TM, nt = (a.tokens + D::TN - 1) / D::TN;
+    int64_t parts = 256 * D::WGS / nt;
+    parts = parts < 1 ? 1 : parts < mt ? parts : mt;
+    const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_w8_tiles<D>), D::LDS);
+    if (e != hipSuccess) return e;
+    const int wide_out = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.o_stride * (int64_t)sizeof(typename D::T) % 16 == 0;
+    hipLaunchKernelGGL(k_w8_tiles<D>, dim3((uint32_t)(parts * nt)), dim3(64 * D::NW), D::LDS, st, a, mt, (int)parts, nt, wide_out);
+    return hipGetLastError();
+}
+
+template <class T, int MT, int NT, int W>
+hipError_t few(const W8LinearArgs &a, hipStream_t st) {
+    hipLaunchKernelGGL((k_w8_few<T, MT, NT, W>), dim3((a.n_out + 16 * MT - 1) / (16 * MT)), dim3(64 * W), 0, st, a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_w8_linear(const W8LinearArgs &a, int dtype, hipStream_t st) {
     return w8_with_type(dtype, [&](auto t) {
-        const int64_t grid = (int64_t)((a.n_out + 127) / 128) * ((a.tokens + 31) / 32);
-        if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
-        hipLaunchKernelGGL(k_w8_linear<decltype(t)>, dim3((uint32_t)grid), dim3(256), 0, st, a);
-        return hipGetLastError();
+        using T = decltype(t);
+#ifdef FORCE
+        return FORCE(a, st);
+#else
+        if (a.tokens <= 16) return few<T, 1, 1, 8>(a, st);
+        if (a.tokens <= 32) return few<T, 1, 2, 8>(a, st);
+        if (a.tokens <= 64) return few<T, 2, 4, 8>(a, st);
+        if (a.tokens <= 256) return tiles<Tile<T, 128, 64, 4, 4, 3, 2>>(a, st);
+        if (a.tokens <= 1024) return tiles<Tile<T, 128, 128, 4, 2, 2, 2>>(a, st);
+        return tiles<Tile<T, 256, 256, 8, 2, 2, 1>>(a, st);
+#endif
     });
 }
 
