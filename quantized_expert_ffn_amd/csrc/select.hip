@@ -33,6 +33,25 @@ __device__ __forceinline__ double ror(double v) {
     const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(b >> 32), 0x120 + N, 0xf, 0xf, true);
     return __longlong_as_double((uint64_t)hi << 32 | lo);
 }
+// This lane's value and that of the lane 16, or 32, away, in some order.
+__device__ __forceinline__ void swap16(float v, float &a, float &b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    a = __uint_as_float(r[0]), b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void swap32(float v, float &a, float &b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    a = __uint_as_float(r[0]), b = __uint_as_float(r[1]);
+}
+template <bool FAR>
+__device__ __forceinline__ void swap64(double v, double &a, double &b) {
+    const uint64_t u = __double_as_longlong(v);
+    const uint32_t l = (uint32_t)u, h = (uint32_t)(u >> 32);
+    const auto lo = FAR ? __builtin_amdgcn_permlane32_swap(l, l, false, false) : __builtin_amdgcn_permlane16_swap(l, l, false, false);
+    const auto hi = FAR ? __builtin_amdgcn_permlane32_swap(h, h, false, false) : __builtin_amdgcn_permlane16_swap(h, h, false, false);
+    a = __longlong_as_double((uint64_t)hi[0] << 32 | lo[0]), b = __longlong_as_double((uint64_t)hi[1] << 32 | lo[1]);
+}
+__device__ __forceinline__ void swap16(double v, double &a, double &b) { swap64<false>(v, a, b); }
+__device__ __forceinline__ void swap32(double v, double &a, double &b) { swap64<true>(v, a, b); }
 // Reductions over a token's lanes, for all of them.
 template <int LANES, class V, class F>
 __device__ __forceinline__ V all_lanes(V v, F f) {
@@ -41,8 +60,11 @@ __device__ __forceinline__ V all_lanes(V v, F f) {
     v = f(v, ror<2>(v));
     v = f(v, ror<1>(v));
     if constexpr (LANES == 64) {
-        v = f(v, __shfl_xor(v, 16));
-        v = f(v, __shfl_xor(v, 32));
+        V x, y;
+        swap16(v, x, y);
+        v = f(x, y);
+        swap32(v, x, y);
+        v = f(x, y);
     }
     return v;
 }
@@ -71,12 +93,17 @@ constexpr float LOG2E = 1.44269504088896340736f;
 // The place of an expert's value in LDS, in words: runs of sixteen, four apart.
 __device__ __forceinline__ int place(int e) { return e + (e >> 4) * 4; }
 __host__ __device__ constexpr int row_words(int experts) { return (experts + 15) / 16 * 20; }
-// Bytes of a wavefront's room in LDS: two rows of values a token, the second
-// of which also holds one token's choices in binary64 and 64 groups' scores;
-// then a candidate a lane, in 8 + 4 bytes.
-__host__ __device__ constexpr size_t select_room(int lanes, int experts) {
+// Bytes of a wavefront's room in LDS: its tokens' logits; their approximate
+// choices, where groups are read from there, and in the same place one token's
+// choices in binary64 and 64 groups' scores; a candidate a lane, in 8 + 4 bytes.
+__host__ __device__ constexpr size_t select_room(int lanes, int experts, bool near) {
     const size_t rows = (size_t)(64 / lanes) * row_words(experts) * 4, slow = 8 * ((size_t)experts + 64);
-    return (rows + (rows > slow ? rows : slow) + 15) / 16 * 16 + 64 * 12;
+    return (rows + (near && rows > slow ? rows : slow) + 15) / 16 * 16 + 64 * 12;
+}
+// Lanes of a group, if it is whole ones and a power of two of them; else 0.
+__host__ __device__ constexpr int group_span(int size, int per) {
+    const int span = size % per ? 0 : size / per;
+    return span & (span - 1) ? 0 : span;
 }
 
 // An expert's score in binary64.
@@ -149,7 +176,9 @@ __global__ __launch_bounds__(256) void k_select(SelectArgs a, int vector) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tok = lane / LANES, sub = lane % LANES;
     const int words = row_words(a.experts), size = a.experts / a.groups;
     // a wavefront's room: logits [TOK], approximate choices [TOK] (or one token's in binary64 and its groups'), candidates
-    const size_t room = select_room(LANES, a.experts);
+    const bool groups = a.topk_group < a.groups;
+    const int span = group_span(size, PER);
+    const size_t room = select_room(LANES, a.experts, groups && !span);
     char *mem = reinterpret_cast<char *>(lds) + wave * room;
     float *logit = reinterpret_cast<float *>(mem) + tok * words;
     char *second_row = mem + (size_t)TOK * words * 4;
@@ -165,29 +194,70 @@ __global__ __launch_bounds__(256) void k_select(SelectArgs a, int vector) {
     constexpr float NEG = -__builtin_inff();
     float key[PER];
     bool bad = false;
+    // No load of these waits for another: places behind the last expert read the last, or the first again.
     if (vector) {   // whole runs, 16-byte aligned
         constexpr int N = sizeof(T) == 4 ? 4 : PER < 8 ? 4 : 8;
         typedef T vec __attribute__((ext_vector_type(N)));
+        vec v[PER / N];
 #pragma unroll
-        for (int i = 0; i < PER; i += N) {
-            vec v;
-            if (e0 + i < a.experts) v = *reinterpret_cast<const vec *>(row + e0 + i);
+        for (int i = 0; i < PER / N; ++i) v[i] = *reinterpret_cast<const vec *>(row + (e0 + N * i < a.experts ? e0 + N * i : 0));
 #pragma unroll
-            for (int j = 0; j < N; ++j) key[i + j] = e0 + i < a.experts ? (float)v[j] : NEG;
-        }
+        for (int i = 0; i < PER; ++i) key[i] = (float)v[i / N][i % N];
     } else {
+        T v[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) key[i] = e0 + i < a.experts ? (float)row[e0 + i] : NEG;
+        for (int i = 0; i < PER; ++i) v[i] = row[min(e0 + i, a.experts - 1)];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = (float)v[i];
     }
-    float top = NEG;
+    float b[PER];
+    float most_bias = 0.0f;
+    if (a.bias) {
+        if (vector) {
+            f32x4 v[PER / 4];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        if (e0 + i < a.experts && !finite_f32(key[i])) {
-            bad = true;
-            key[i] = 0.0f;
+            for (int i = 0; i < PER / 4; ++i) v[i] = *reinterpret_cast<const f32x4 *>(a.bias + (e0 + 4 * i < a.experts ? e0 + 4 * i : 0));
+#pragma unroll
+            for (int i = 0; i < PER; ++i) b[i] = v[i / 4][i % 4];
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) b[i] = a.bias[min(e0 + i, a.experts - 1)];
         }
-        top = fmaxf(top, key[i]);
+        float odd = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            odd = __builtin_fmaf(b[i], 0.0f, odd);   // NaN from what is not finite
+            most_bias = fmaxf(most_bias, fabsf(b[i]));
+        }
+        if (odd != 0.0f) {
+            bad = true;
+            most_bias = 0.0f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                b[i] = finite_f32(b[i]) ? b[i] : 0.0f;
+                most_bias = fmaxf(most_bias, fabsf(b[i]));
+            }
+        }
     }
+    float top = NEG, odd = 0.0f;
+    const int left = a.experts - e0;   // where not all are there, those of a lane are or are not, or some are
+    const bool some = left > 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) odd = __builtin_fmaf(key[i], 0.0f, odd);
+    if (odd != 0.0f) {
+        bad = true;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = finite_f32(key[i]) ? key[i] : 0.0f;
+    }
+    if (a.experts % PER) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = i < left ? key[i] : NEG;
+    } else if (a.experts < LANES * PER) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = some ? key[i] : NEG;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) top = fmaxf(top, key[i]);
     if (e0 < a.experts) {
 #pragma unroll
         for (int i = 0; i < PER; i += 4) *reinterpret_cast<f32x4 *>(logit + place(e0 + i)) = f32x4{key[i], key[i + 1], key[i + 2], key[i + 3]};
@@ -198,40 +268,41 @@ __global__ __launch_bounds__(256) void k_select(SelectArgs a, int vector) {
     if (a.softmax && (a.bias || !a.norm || (a.top2 && a.topk_group < a.groups))) {
         double sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (e0 + i < a.experts) sum += exp((double)key[i] - top);
+        for (int i = 0; i < PER; ++i) sum += exp((double)key[i] - top);   // none behind the last expert: exp(-inf)
         inv_sum = 1.0 / all_lanes<LANES>(sum, Add());
     }
     // ---- approximate choices, off by at most eps: a sigmoid by 2^-21 (0.2 of the exponential's relative error, sum and
     // quotient by a step each, the sum with the bias by half of one), a softmax by 2^-20 of the largest (the exponent by two
     // steps and a half of itself, d 2^-d < 1, the exponential and its product by a step each), and half a step of the bias
-    const bool groups = a.topk_group < a.groups, approximate = a.bias || (groups && a.top2);
-    float eps = 0.0f;
+    const bool approximate = a.bias || (groups && a.top2);
+    float eps = 0.0f, seen[PER];   // seen: what groups go by
+#pragma unroll
+    for (int i = 0; i < PER; ++i) seen[i] = key[i];
     if (approximate) {
         const float inv = (float)inv_sum;
-        float most = 0.0f;
         float c[PER];
+        if (a.softmax) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = e0 + i;
-            float b = 0.0f;
-            if (a.bias && e < a.experts) {
-                b = a.bias[e];
-                if (!finite_f32(b)) {
-                    bad = true;
-                    b = 0.0f;
-                }
-            }
-            most = fmaxf(most, fabsf(b));
-            const float x = a.softmax ? __builtin_amdgcn_exp2f((key[i] - top) * LOG2E) * inv
-                                      : __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-LOG2E * key[i]));
-            c[i] = e < a.experts ? x + b : NEG;
+            for (int i = 0; i < PER; ++i) c[i] = __builtin_amdgcn_exp2f((key[i] - top) * LOG2E) * inv;
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-LOG2E * key[i]));
         }
-        eps = 0x1p-20f * (a.softmax ? inv : 0.5f) + 0x1p-22f * all_lanes<LANES>(most, Max());
-        if (groups && e0 < a.experts) {
+        if (a.bias) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) c[i] += b[i];
+        }
+        if (a.experts < LANES * PER) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) c[i] = key[i] == NEG ? NEG : c[i];
+        }
+        eps = 0x1p-20f * (a.softmax ? inv : 0.5f) + 0x1p-22f * all_lanes<LANES>(most_bias, Max());
+        if (groups && !span && e0 < a.experts) {
 #pragma unroll
             for (int i = 0; i < PER; i += 4) *reinterpret_cast<f32x4 *>(near + place(e0 + i)) = f32x4{c[i], c[i + 1], c[i + 2], c[i + 3]};
         }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) seen[i] = c[i];
         if (a.bias) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) key[i] = c[i];
@@ -241,34 +312,60 @@ __global__ __launch_bounds__(256) void k_select(SelectArgs a, int vector) {
     // ---- groups: a lane each (there are at most LANES)
     bool slow = false;
     if (groups) {
-        const float *from = approximate ? near : logit;
         float first = NEG, second = NEG;
-        if (sub < a.groups)
-            for (int e = sub * size; e < (sub + 1) * size; ++e) {
-                const float v = from[place(e)];
-                second = fmaxf(second, fminf(first, v));
-                first = fmaxf(first, v);
+        if (span) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                second = fmaxf(second, fminf(first, seen[i]));
+                first = fmaxf(first, seen[i]);
             }
+            for (int o = 1; o < span; o += o) {
+                const float f = __shfl_xor(first, o), t = __shfl_xor(second, o);
+                second = fmaxf(fmaxf(second, t), fminf(first, f));
+                first = fmaxf(first, f);
+            }
+        } else {
+            const float *from = approximate ? near : logit;
+            if (sub < a.groups)
+                for (int e = sub * size, end = e + size; e < end; e += 8) {   // the last of them again, if eight do not divide
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = from[place(min(e + i, end - 1))];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float w = e + i < end ? v[i] : NEG;
+                        second = fmaxf(second, fminf(first, w));
+                        first = fmaxf(first, w);
+                    }
+                }
+        }
+        // its number, and the lane that has another's
+        const int self = span ? sub / span : sub, apart = span ? span : 1;
         const float mine = a.top2 && size > 1 ? first + second : first;
         int before = 0;
         for (int g = 0; g < a.groups; ++g) {
-            const float other = __shfl(mine, lane - sub + g);
-            before += other > mine || (other == mine && g < sub);
+            const float other = __shfl(mine, lane - sub + g * apart);
+            before += other > mine || (other == mine && g < self);
         }
-        const bool in = sub < a.groups && before < a.topk_group;
-        const uint64_t open = __ballot(in) >> (lane - sub);
+        const bool there = self < a.groups, in = there && before < a.topk_group;
         if (approximate) {
-            const float least = all_lanes<LANES>(in ? mine : -NEG, Min()), next = all_lanes<LANES>(sub < a.groups && !in ? mine : NEG, Max());
+            const float least = all_lanes<LANES>(in ? mine : -NEG, Min()), next = all_lanes<LANES>(there && !in ? mine : NEG, Max());
             // sums of two are off by 2 eps and their own rounding
             slow = !(least - next > 4.0f * eps + 0x1p-22f * (fabsf(least) + fabsf(next)));
         }
-        int g = e0 / size, rest = e0 - g * size;
+        if (span) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            if (!(open >> g & 1)) key[i] = NEG;
-            if (++rest == size) {
-                rest = 0;
-                ++g;
+            for (int i = 0; i < PER; ++i) key[i] = in ? key[i] : NEG;
+        } else {
+            const uint64_t open = __ballot(in) >> (lane - sub);
+            int g = e0 / size, rest = e0 - g * size;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (!(open >> g & 1)) key[i] = NEG;
+                if (++rest == size) {
+                    rest = 0;
+                    ++g;
+                }
             }
         }
     }
@@ -280,28 +377,23 @@ __global__ __launch_bounds__(256) void k_select(SelectArgs a, int vector) {
 #pragma unroll
         for (int i = 1; i < SUB; ++i) most[q] = fmaxf(most[q], key[SUB * q + i]);
     }
+    const uint64_t lower = ((1ull << sub) - 1) << (lane - sub);   // the token's lanes before this one
     float bound = NEG;
     for (int k = 0; k < a.top_k; ++k) {
         const float mine = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
         bound = all_lanes<LANES>(mine, Max());
-        uint64_t has = __ballot(mine == bound);
-        if (LANES < 64) has = has >> (lane - sub) & ((1ull << (LANES & 63)) - 1);
-        if (sub == (int)__builtin_ctzll(has)) {   // of equal ones, one lane's at a time
-            bool done = false;
+        const uint64_t has = __ballot(mine == bound);
+        if (mine == bound && !(has & lower)) {   // of equal ones, one lane's at a time
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const bool it = !done && most[q] == bound;
-                if (it) most[q] = NEG;
-                done |= it;
-            }
+            for (int q = 0; q < 4; ++q) most[q] = most[q] == bound ? NEG : most[q];
         }
     }
     // ---- candidates, in the order of their experts
     bound = a.bias ? bound - 2.0f * eps - 0x1p-22f * fabsf(bound) : bound;
+    bound = fmaxf(bound, -0x1.fffffep+127f);   // closed ones are below every number
     uint32_t mask = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (key[i] >= bound && key[i] > NEG) mask |= 1u << i;
+    for (int i = 0; i < PER; ++i) mask |= key[i] >= bound ? 1u << i : 0;
     int count = __popc(mask), upto = count;
     upto = dpp_add<0x111, 0xf>(upto);
     upto = dpp_add<0x112, 0xf>(upto);
@@ -331,9 +423,12 @@ __global__ __launch_bounds__(256) void k_select(SelectArgs a, int vector) {
     wave_sync();
     int rank = 0;
     const int longest = LANES == 64 ? total : (int)all_lanes<64>((float)total, Max());
-    for (int i = 0; i < min(longest, LANES); ++i) {
-        const double other = cand_key[i];
-        rank += i < total && (other > choice || (other == choice && i < sub));
+    for (int i = 0; i < min(longest, LANES); i += 4) {
+        double other[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) other[j] = cand_key[i + j];   // LANES are a multiple
+#pragma unroll
+        for (int j = 0; j < 4; ++j) rank += i + j < total && (other[j] > choice || (other[j] == choice && i + j < sub));
     }
     bool chosen = mine >= 0 && rank < a.top_k;
     // ---- tokens to be done over, one after the other
@@ -366,11 +461,12 @@ __global__ __launch_bounds__(256) void k_select(SelectArgs a, int vector) {
 template <class T, int LANES, int PER>
 hipError_t launch_shape(const SelectArgs &a, hipStream_t st) {
     constexpr int TOK = 64 / LANES;
-    const size_t room = select_room(LANES, a.experts);
-    int waves = a.tokens > 256 * TOK ? 4 : 1;
+    const size_t room = select_room(LANES, a.experts, a.topk_group < a.groups && !group_span(a.experts / a.groups, PER));
+    const int waves = a.tokens > 256 * TOK ? 4 : 1;
     const int64_t groups = (a.tokens + TOK - 1) / TOK;
     constexpr int N = sizeof(T) == 4 ? 4 : PER < 8 ? 4 : 8;
-    const bool vector = a.experts % N == 0 && a.stride % N == 0 && reinterpret_cast<uintptr_t>(a.logits) % (N * sizeof(T)) == 0;
+    const bool vector = a.experts % N == 0 && a.stride % N == 0 && reinterpret_cast<uintptr_t>(a.logits) % (N * sizeof(T)) == 0 &&
+                        reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
     const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_select<T, LANES, PER>), room * waves);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((k_select<T, LANES, PER>), dim3((uint32_t)((groups + waves - 1) / waves)), dim3(64 * waves), room * waves, st, a,
