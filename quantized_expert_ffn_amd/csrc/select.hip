@@ -155,14 +155,7 @@ __device__ __forceinline__ int select_slow(const SelectArgs &a, const float *log
                     at = e;
                 }
             }
-        for (int o = 32; o; o >>= 1) {
-            const double oc = __shfl_xor(c, o);
-            const int oa = __shfl_xor(at, o);
-            if (oc > c || (oc == c && oa < at)) {
-                c = oc;
-                at = oa;
-            }
-        }
+        at = (int)all_lanes<64>(c == all_lanes<64>(c, Max()) ? (float)at : 1024.0f, Min());
         if ((at & 63) == lane) mine |= 1u << (at >> 6);
         if (lane == k) chosen = at;
     }
@@ -340,18 +333,44 @@ __global__ __launch_bounds__(256) void k_select(SelectArgs a, int vector) {
                 }
         }
         // its number, and the lane that has another's
-        const int self = span ? sub / span : sub, apart = span ? span : 1;
-        const float mine = a.top2 && size > 1 ? first + second : first;
-        int before = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const float other = __shfl(mine, lane - sub + g * apart);
-            before += other > mine || (other == mine && g < self);
-        }
-        const bool there = self < a.groups, in = there && before < a.topk_group;
+        const int shift = span ? __builtin_ctz(span) : 0, self = sub >> shift;
+        const bool two = a.top2 && size > 1, there = self < a.groups;
+        const float mine = two ? first + second : first;
+        bool in;
+        auto stand = [&](auto v) {
+            int before = 0;
+            for (int g = 0; g < a.groups; ++g) {
+                const auto other = __shfl(v, lane - sub + (g << shift));
+                before += other > v || (other == v && g < self);
+            }
+            in = there && before < a.topk_group;
+        };
+        stand(mine);
         if (approximate) {
             const float least = all_lanes<LANES>(in ? mine : -NEG, Min()), next = all_lanes<LANES>(there && !in ? mine : NEG, Max());
             // sums of two are off by 2 eps and their own rounding
             slow = !(least - next > 4.0f * eps + 0x1p-22f * (fabsf(least) + fabsf(next)));
+            if (span && __ballot(slow)) {   // scores in binary64, of the experts that could be a group's best
+                const float from = two ? second : first, least_seen = from - 2.0f * eps - 0x1p-22f * fabsf(from);
+                uint32_t open = 0;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) open |= seen[i] >= least_seen && seen[i] > NEG ? 1u << i : 0;
+                double f = -__builtin_inf(), t = f;
+                while (open) {
+                    const int e = e0 + __builtin_ctz(open);
+                    open &= open - 1;
+                    const double v = score64(a, logit[place(e)], top, inv_sum) + bias_of(a, e);
+                    t = fmax(t, fmin(f, v));
+                    f = fmax(f, v);
+                }
+                for (int o = 1; o < span; o += o) {
+                    const double of = __shfl_xor(f, o), ot = __shfl_xor(t, o);
+                    t = fmax(fmax(t, ot), fmin(f, of));
+                    f = fmax(f, of);
+                }
+                stand(two ? f + t : f);
+                slow = false;
+            }
         }
         if (span) {
 #pragma unroll
