@@ -11,6 +11,10 @@
 namespace coli {
 namespace {
 
+#ifndef ROT
+#define ROT 1
+#endif
+
 typedef int32_t i32x4v __attribute__((ext_vector_type(4)));
 
 // Where chunks behind the end of a row read.
@@ -22,13 +26,17 @@ __device__ __forceinline__ float finish(int32_t sum, float st, float so, float b
     return has_bias ? v + bias : v;
 }
 
+// Lane's place in a 1 KiB load: eight rows of eight chunks, swizzled so that
+// sixteen rows' same chunk lies in sixteen groups of banks.
+__device__ __forceinline__ int swz(int r) { return 4 * ((r >> 1) & 1) + 2 * ((r >> 2) & 1) + ((r >> 3) & 1); }
+
 // ---------------------------------------------------------------- few tokens
 // The weights pass once from memory to registers: a wavefront takes 16 MT
-// channels and every W-th run of four steps of 64 along k, and a workgroup's W
-// wavefronts add their sums in LDS.  Tokens (16 NT) come from the L2.
-template <class T, int MT, int NT, int W>
+// channels and every W-th run of U steps of 64 along k, DEPTH - 1 runs ahead of
+// their products, and a workgroup's W wavefronts add their sums in LDS.  Tokens
+// (16 NT) come from the L2.
+template <class T, int MT, int NT, int W, int U, int DEPTH>
 __global__ __launch_bounds__(64 * W) void k_w8_few(W8LinearArgs a) {
-    constexpr int U = 4;
     __shared__ i32x4v part[W][MT * NT][64];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, kc = 16 * (lane >> 4);
     const int o0 = blockIdx.x * 16 * MT;
@@ -42,34 +50,49 @@ __global__ __launch_bounds__(64 * W) void k_w8_few(W8LinearArgs a) {
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = i32x4v{0, 0, 0, 0};
-    for (int k = wave * 64 * U; k < a.k; k += W * 64 * U) {
-        i32x4v av[U][MT], bv[U][NT];
-        if (k + 64 * U <= a.k) {
+    constexpr int RUN = 64 * U, STRIDE = W * RUN;
+    i32x4v av[DEPTH][U][MT], bv[DEPTH][U][NT];
+    auto fetch = [&](int d, int k) {   // a whole run, or nothing
+        if (k + RUN > a.k) return;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    av[u][i] = __builtin_nontemporal_load(reinterpret_cast<const i32x4v *>(wp[i] + k + 64 * u));
+            for (int i = 0; i < MT; ++i) av[d][u][i] = __builtin_nontemporal_load(reinterpret_cast<const i32x4v *>(wp[i] + k + 64 * u));
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) bv[u][j] = *reinterpret_cast<const i32x4v *>(xp[j] + k + 64 * u);
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const bool in = k + 64 * u + kc < a.k;
-#pragma unroll
-                for (int i = 0; i < MT; ++i) av[u][i] = in ? *reinterpret_cast<const i32x4v *>(wp[i] + k + 64 * u) : i32x4v{0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < NT; ++j) bv[u][j] = in ? *reinterpret_cast<const i32x4v *>(xp[j] + k + 64 * u) : i32x4v{0, 0, 0, 0};
-            }
-        }
+            for (int j = 0; j < NT; ++j) bv[d][u][j] = *reinterpret_cast<const i32x4v *>(xp[j] + k + 64 * u);
+    };
+    auto multiply = [&](int d) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[u][i], bv[u][j], acc[i][j], 0, 0, 0);
+                for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[d][u][i], bv[d][u][j], acc[i][j], 0, 0, 0);
+    };
+    const int whole = a.k / RUN * RUN;
+    int k = wave * RUN;
+#pragma unroll
+    for (int d = 0; d < DEPTH - 1; ++d) fetch(d, k + d * STRIDE);
+    for (; k < whole; k += DEPTH * STRIDE)
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            fetch((d + DEPTH - 1) % DEPTH, k + (d + DEPTH - 1) * STRIDE);
+            if (k + d * STRIDE < whole) multiply(d);
+        }
+    // what is left of a run, a step a wavefront
+    for (k = whole + 64 * wave; k < a.k; k += 64 * W) {
+        const bool in = k + kc < a.k;
+        i32x4v bt[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) bt[j] = in ? *reinterpret_cast<const i32x4v *>(xp[j] + k) : i32x4v{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const i32x4v at = in ? *reinterpret_cast<const i32x4v *>(wp[i] + k) : i32x4v{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(at, bt[j], acc[i][j], 0, 0, 0);
+        }
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -87,6 +110,122 @@ __global__ __launch_bounds__(64 * W) void k_w8_few(W8LinearArgs a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             if (o + r < a.n_out) out[o + r] = (T)finish(sum[r], st, a.w_scale[o + r], a.bias ? a.bias[o + r] : 0.0f, a.bias != nullptr);
+    }
+}
+
+// ---------------------------------------------------------------- some tokens
+// All tokens by 32 FM channels a workgroup, so that weights pass once and many
+// workgroups share them out.  Steps of NW / 4 lines of 128 along k go through a
+// ring of LDS stages, and each of the NW wavefronts multiplies 32 of every
+// step; their sums meet in LDS at the end, 32 x 32 tiles at a time.
+template <class T_, int FM_, int FN_, int NW_, int STAGES_, int WGS_>
+struct Split {
+    using T = T_;
+    static constexpr int FM = FM_, FN = FN_, NW = NW_, STAGES = STAGES_, WGS = WGS_, TM = 32 * FM, TN = 32 * FN, STEP = 32 * NW;
+    static constexpr int LINE = (TM + TN) * 128, STAGE = LINE * NW / 4, LOADS = FM + FN;   // 1 KiB loads a wavefront and step
+    static constexpr int OROW = 36 * 4, SUMS = NW * 4096, OUT = 32 * OROW;
+    static constexpr int RING = STAGES * STAGE, LDS = RING > SUMS + OUT ? RING : SUMS + OUT;
+    static_assert(LDS * WGS <= 160 * 1024 && (STAGES - 2) * LOADS < 64, "LDS, loads that are out");
+};
+
+template <class D>
+__global__ __launch_bounds__(64 * D::NW, D::WGS * D::NW / 4) void k_w8_split(W8LinearArgs a, int wide_out) {
+    using T = typename D::T;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 31, hf = lane >> 5;
+    const int o0 = blockIdx.x * D::TM, steps = (a.k + D::STEP - 1) / D::STEP;
+    const int8_t *src[D::LOADS];
+    int chunk[D::LOADS];
+#pragma unroll
+    for (int i = 0; i < D::LOADS; ++i) {
+        constexpr int GROUPS = D::LINE / 1024;
+        const int l = wave * D::LOADS + i, r = l % GROUPS * 8 + (lane >> 3);
+        chunk[i] = l / GROUPS * 128 + (((lane & 7) ^ swz(r)) << 4);
+        src[i] = (r < D::TM ? a.w + (int64_t)min(o0 + r, a.n_out - 1) * a.k : a.x + (int64_t)min(r - D::TM, a.tokens - 1) * a.x_stride) + chunk[i];
+    }
+    // Rows are often a power of two apart, or nearly so, and the lines of a step then lie in few channels of the L2: each
+    // workgroup of an XCD begins elsewhere along k, and goes round.
+    const int turn = ROT ? (int)((int64_t)(blockIdx.x >> 3) * steps / ((gridDim.x + 7) >> 3)) : 0;
+    int load = turn, load_slot = 0;
+    auto issue = [&] {   // behind the last step nothing is read that counts
+        const int k = load * D::STEP;
+        const uint32_t base = load_slot * D::STAGE + wave * D::LOADS * 1024;
+        if (k + D::STEP <= a.k) {
+#pragma unroll
+            for (int i = 0; i < D::LOADS; ++i) load_to_lds(src[i] + k, base + i * 1024);
+        } else {   // a row that ends inside the step: zeros behind it
+#pragma unroll
+            for (int i = 0; i < D::LOADS; ++i)
+                load_to_lds(k + chunk[i] < a.k ? src[i] + k : reinterpret_cast<const int8_t *>(w8_zeros), base + i * 1024);
+        }
+        load_slot = load_slot == D::STAGES - 1 ? 0 : load_slot + 1;
+        load = load == steps - 1 ? 0 : load + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < D::STAGES - 1; ++i) issue();
+    // this wavefront's 32 of a step: line wave / 4, chunks 2 (wave % 4) + hf
+    const uint32_t at = wave / 4 * D::LINE + (n >> 3) * 1024 + (n & 7) * 128 + (((2 * (wave & 3) + hf) ^ swz(n)) << 4);
+    i32x16 acc[D::FM][D::FN];
+#pragma unroll
+    for (int i = 0; i < D::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < D::FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+    int slot = 0;
+    for (int k = 0; k < steps; ++k) {
+        wait_vm<(D::STAGES - 2) * D::LOADS>();
+        barrier_lds();
+        issue();
+        const uint32_t base = slot * D::STAGE + at;
+        slot = slot == D::STAGES - 1 ? 0 : slot + 1;
+        i32x4 av[D::FM], bv[D::FN];
+#pragma unroll
+        for (int i = 0; i < D::FM; ++i) av[i] = lds_read<i32x4>(base, i * 4096);
+#pragma unroll
+        for (int j = 0; j < D::FN; ++j) bv[j] = lds_read<i32x4>(base, (D::FM + j) * 4096);
+#pragma unroll
+        for (int i = 0; i < D::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < D::FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(av[i], bv[j], acc[i][j], 0, 0, 0);
+    }
+    wait_vm<0>();
+    typedef T four __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int p = 0; p < D::FM * D::FN; ++p) {
+        const int i = p / D::FN, j = p % D::FN;
+        barrier_lds();   // the ring, or the tile before, is done with
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            lds_write((wave * 4 + q) * 1024 + 16 * lane, i32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]});
+        barrier_lds();
+        if (wave < 4) {   // eight of the tile's channels each
+            i32x4 sum = lds_read<i32x4>(wave * 1024 + 16 * lane);
+#pragma unroll
+            for (int w = 1; w < D::NW; ++w) sum += lds_read<i32x4>((w * 4 + wave) * 1024 + 16 * lane);
+            const float st = a.x_scale[min(32 * j + n, a.tokens - 1)];
+            f32x4 v;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int o = min(o0 + 32 * i + 8 * wave + 4 * hf + k, a.n_out - 1);
+                v[k] = finish(sum[k], st, a.w_scale[o], a.bias ? a.bias[o] : 0.0f, a.bias != nullptr);
+            }
+            lds_write(D::SUMS + n * D::OROW + 32 * wave + 16 * hf, v);
+        }
+        barrier_lds();
+        if (wave < 4) {   // tokens' runs of 32 channels, eight lanes each
+            const int r = 8 * wave + (lane >> 3), t = 32 * j + r, o = o0 + 32 * i + 4 * (lane & 7);
+            const f32x4 v = lds_read<f32x4>(D::SUMS + r * D::OROW + 16 * (lane & 7));
+            if (t < a.tokens) {
+                T *dst = static_cast<T *>(a.out) + (int64_t)t * a.o_stride + o;
+                if (wide_out && o + 4 <= a.n_out) {
+                    *reinterpret_cast<four *>(dst) = four{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (o + k < a.n_out) dst[k] = (T)v[k];
+                }
+            }
+        }
     }
 }
 
@@ -108,10 +247,6 @@ struct Tile {
     static constexpr int LDS = L_SCALE + 8 * TM;
     static_assert(LA >= 1 && LB >= 1 && OUT <= STAGE && LDS * WGS <= 160 * 1024, "LDS");
 };
-
-// Lane's place in a 1 KiB load: eight rows of eight chunks, swizzled so that
-// sixteen rows' same chunk lies in sixteen groups of banks.
-__device__ __forceinline__ int swz(int r) { return 4 * ((r >> 1) & 1) + 2 * ((r >> 2) & 1) + ((r >> 3) & 1); }
 
 // Work items to XCDs: workgroups go to the eight XCDs in turn; each XCD takes
 // a contiguous run of items.
@@ -147,35 +282,34 @@ __global__ __launch_bounds__(64 * D::NW, D::NW * D::WGS / 4) void k_w8_tiles(W8L
             wp[i] = a.w + (int64_t)min(load_mt * D::TM + r, a.n_out - 1) * a.k + chunk(r);
         }
     };
-    auto issue = [&] {
-        if (load_mt >= mt_end) return;
+    // A step's loads in four parts, which stand between products: together they would hold the wavefronts up.  Behind the last
+    // step they read its lines once more.
+    auto issue = [&](int part) {
         const uint32_t base = load_slot * D::STAGE;
         const int k = load_k * 128;
-        if (k + 128 <= a.k) {
+        constexpr int ALL = D::LA + D::LB;
 #pragma unroll
-            for (int i = 0; i < D::LA; ++i) load_to_lds(wp[i] + k, base + (wave * D::LA + i) * 1024);
-#pragma unroll
-            for (int i = 0; i < D::LB; ++i) load_to_lds(xp[i] + k, base + D::ASTAGE + (wave * D::LB + i) * 1024);
-        } else {   // the last step of a row that ends inside a line: zeros behind it
-            const int8_t *zero = reinterpret_cast<const int8_t *>(w8_zeros);
-#pragma unroll
-            for (int i = 0; i < D::LA; ++i)
-                load_to_lds(k + chunk((wave * D::LA + i) * 8 + (lane >> 3)) < a.k ? wp[i] + k : zero, base + (wave * D::LA + i) * 1024);
-#pragma unroll
-            for (int i = 0; i < D::LB; ++i)
-                load_to_lds(k + chunk((wave * D::LB + i) * 8 + (lane >> 3)) < a.k ? xp[i] + k : zero,
-                            base + D::ASTAGE + (wave * D::LB + i) * 1024);
+        for (int l = 0; l < ALL; ++l) {
+            if (l * 4 / ALL != part) continue;
+            const bool of_w = l < D::LA;
+            const int g = of_w ? wave * D::LA + l : wave * D::LB + l - D::LA;
+            const int8_t *src = (of_w ? wp[of_w ? l : 0] : xp[of_w ? 0 : l - D::LA]) + k;
+            if (k + 128 > a.k && k + chunk(8 * g + (lane >> 3)) >= a.k) src = reinterpret_cast<const int8_t *>(w8_zeros);
+            load_to_lds(src, base + (of_w ? 0 : D::ASTAGE) + g * 1024);
         }
+        if (part < 3) return;
         load_slot = load_slot == D::STAGES - 1 ? 0 : load_slot + 1;
         if (++load_k == steps) {
             load_k = 0;
-            ++load_mt;
+            load_mt = min(load_mt + 1, mt_end - 1);
             aim();
         }
     };
     aim();
 #pragma unroll
-    for (int i = 0; i < D::STAGES - 1; ++i) issue();
+    for (int i = 0; i < D::STAGES - 1; ++i)
+#pragma unroll
+        for (int part = 0; part < 4; ++part) issue(part);
     // Matrix step e of a stage takes k = 32 e + 16 hf + 0..15 of both sides.
     uint32_t aa[4], ba[4];
 #pragma unroll
@@ -204,26 +338,31 @@ __global__ __launch_bounds__(64 * D::NW, D::NW * D::WGS / 4) void k_w8_tiles(W8L
         for (int k = 0; k < steps; ++k) {
             if (ready > 0)
                 --ready;
-            else if (D::STAGES > 2 && (mt + 1 < mt_end || k + 1 < steps))
-                wait_vm<(D::STAGES - 2) * (D::LA + D::LB)>();
             else
-                wait_vm<0>();
+                wait_vm<(D::STAGES - 2) * (D::LA + D::LB)>();
             barrier_lds();
-            issue();
             base = slot * D::STAGE;
             slot = slot == D::STAGES - 1 ? 0 : slot + 1;
+            i32x4 av[2][D::FM], bv[2][D::FN];
+            auto read = [&](int e) {
+#pragma unroll
+                for (int j = 0; j < D::FN; ++j) bv[e & 1][j] = lds_read<i32x4>(base + ba[e], j * 4096);
+#pragma unroll
+                for (int i = 0; i < D::FM; ++i) av[e & 1][i] = lds_read<i32x4>(base + aa[e], i * 4096);
+            };
+            read(0);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                i32x4 av[D::FM], bv[D::FN];
-#pragma unroll
-                for (int j = 0; j < D::FN; ++j) bv[j] = lds_read<i32x4>(base + ba[e], j * 4096);
-#pragma unroll
-                for (int i = 0; i < D::FM; ++i) av[i] = lds_read<i32x4>(base + aa[e], i * 4096);
+                __builtin_amdgcn_sched_barrier(0);
+                if (e < 3) read(e + 1);
 #pragma unroll
                 for (int i = 0; i < D::FM; ++i)
 #pragma unroll
-                    for (int j = 0; j < D::FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(av[i], bv[j], acc[i][j], 0, 0, 0);
+                    for (int j = 0; j < D::FN; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(av[e & 1][i], bv[e & 1][j], acc[i][j], 0, 0, 0);
+                issue(e);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
         // The loads that are out, before the stores: a later count of loads must not wait for those.
         wait_vm<0>();
@@ -284,9 +423,19 @@ hipError_t tiles(const W8LinearArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <class T, int MT, int NT, int W>
+template <class D>
+hipError_t split(const W8LinearArgs &a, hipStream_t st) {
+    const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_w8_split<D>), D::LDS);
+    if (e != hipSuccess) return e;
+    constexpr int64_t four = 4 * sizeof(typename D::T);
+    const int wide_out = reinterpret_cast<uintptr_t>(a.out) % four == 0 && a.o_stride * (int64_t)sizeof(typename D::T) % four == 0;
+    hipLaunchKernelGGL(k_w8_split<D>, dim3((a.n_out + D::TM - 1) / D::TM), dim3(64 * D::NW), D::LDS, st, a, wide_out);
+    return hipGetLastError();
+}
+
+template <class T, int MT, int NT, int W, int U, int DEPTH>
 hipError_t few(const W8LinearArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL((k_w8_few<T, MT, NT, W>), dim3((a.n_out + 16 * MT - 1) / (16 * MT)), dim3(64 * W), 0, st, a);
+    hipLaunchKernelGGL((k_w8_few<T, MT, NT, W, U, DEPTH>), dim3((a.n_out + 16 * MT - 1) / (16 * MT)), dim3(64 * W), 0, st, a);
     return hipGetLastError();
 }
 
@@ -298,9 +447,9 @@ hipError_t launch_w8_linear(const W8LinearArgs &a, int dtype, hipStream_t st) {
 #ifdef FORCE
         return FORCE(a, st);
 #else
-        if (a.tokens <= 16) return few<T, 1, 1, 8>(a, st);
-        if (a.tokens <= 32) return few<T, 1, 2, 8>(a, st);
-        if (a.tokens <= 64) return few<T, 2, 4, 8>(a, st);
+        if (a.tokens <= 16) return few<T, 1, 1, 8, 4, 2>(a, st);
+        if (a.tokens <= 32) return few<T, 1, 2, 8, 2, 2>(a, st);
+        if (a.tokens <= 64) return few<T, 2, 4, 8, 2, 2>(a, st);
         if (a.tokens <= 256) return tiles<Tile<T, 128, 64, 4, 4, 3, 2>>(a, st);
         if (a.tokens <= 1024) return tiles<Tile<T, 128, 128, 4, 2, 2, 2>>(a, st);
         return tiles<Tile<T, 256, 256, 8, 2, 2, 1>>(a, st);
