@@ -30,89 +30,6 @@ __device__ __forceinline__ float finish(int32_t sum, float st, float so, float b
 // sixteen rows' same chunk lies in sixteen groups of banks.
 __device__ __forceinline__ int swz(int r) { return 4 * ((r >> 1) & 1) + 2 * ((r >> 2) & 1) + ((r >> 3) & 1); }
 
-// ---------------------------------------------------------------- few tokens
-// The weights pass once from memory to registers: a wavefront takes 16 MT
-// channels and every W-th run of U steps of 64 along k, DEPTH - 1 runs ahead of
-// their products, and a workgroup's W wavefronts add their sums in LDS.  Tokens
-// (16 NT) come from the L2.
-template <class T, int MT, int NT, int W, int U, int DEPTH>
-__global__ __launch_bounds__(64 * W) void k_w8_few(W8LinearArgs a) {
-    __shared__ i32x4v part[W][MT * NT][64];
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), n = lane & 15, kc = 16 * (lane >> 4);
-    const int o0 = blockIdx.x * 16 * MT;
-    const int8_t *wp[MT], *xp[NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) wp[i] = a.w + (int64_t)min(o0 + 16 * i + n, a.n_out - 1) * a.k + kc;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) xp[j] = a.x + (int64_t)min(16 * j + n, a.tokens - 1) * a.x_stride + kc;
-    i32x4v acc[MT][NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = i32x4v{0, 0, 0, 0};
-    constexpr int RUN = 64 * U, STRIDE = W * RUN;
-    i32x4v av[DEPTH][U][MT], bv[DEPTH][U][NT];
-    auto fetch = [&](int d, int k) {   // a whole run, or nothing
-        if (k + RUN > a.k) return;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) av[d][u][i] = __builtin_nontemporal_load(reinterpret_cast<const i32x4v *>(wp[i] + k + 64 * u));
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) bv[d][u][j] = *reinterpret_cast<const i32x4v *>(xp[j] + k + 64 * u);
-    };
-    auto multiply = [&](int d) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[d][u][i], bv[d][u][j], acc[i][j], 0, 0, 0);
-    };
-    const int whole = a.k / RUN * RUN;
-    int k = wave * RUN;
-#pragma unroll
-    for (int d = 0; d < DEPTH - 1; ++d) fetch(d, k + d * STRIDE);
-    for (; k < whole; k += DEPTH * STRIDE)
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            fetch((d + DEPTH - 1) % DEPTH, k + (d + DEPTH - 1) * STRIDE);
-            if (k + d * STRIDE < whole) multiply(d);
-        }
-    // what is left of a run, a step a wavefront
-    for (k = whole + 64 * wave; k < a.k; k += 64 * W) {
-        const bool in = k + kc < a.k;
-        i32x4v bt[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) bt[j] = in ? *reinterpret_cast<const i32x4v *>(xp[j] + k) : i32x4v{0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const i32x4v at = in ? *reinterpret_cast<const i32x4v *>(wp[i] + k) : i32x4v{0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(at, bt[j], acc[i][j], 0, 0, 0);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
-    __syncthreads();
-    for (int p = wave; p < MT * NT; p += W) {
-        i32x4v sum = part[0][p][lane];
-#pragma unroll
-        for (int w = 1; w < W; ++w) sum += part[w][p][lane];
-        const int t = 16 * (p % NT) + n, o = o0 + 16 * (p / NT) + 4 * (lane >> 4);
-        if (t >= a.tokens) continue;
-        const float st = a.x_scale[t];
-        T *out = static_cast<T *>(a.out) + (int64_t)t * a.o_stride;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (o + r < a.n_out) out[o + r] = (T)finish(sum[r], st, a.w_scale[o + r], a.bias ? a.bias[o + r] : 0.0f, a.bias != nullptr);
-    }
-}
-
 // ---------------------------------------------------------------- some tokens
 // All tokens by 32 FM channels a workgroup, so that weights pass once and many
 // workgroups share them out.  Steps of NW / 4 lines of 128 along k go through a
@@ -282,22 +199,22 @@ __global__ __launch_bounds__(64 * D::NW, D::NW * D::WGS / 4) void k_w8_tiles(W8L
             wp[i] = a.w + (int64_t)min(load_mt * D::TM + r, a.n_out - 1) * a.k + chunk(r);
         }
     };
-    // A step's loads in four parts, which stand between products: together they would hold the wavefronts up.  Behind the last
-    // step they read its lines once more.
+    // A step's loads in three parts, which stand between products: together they would hold the wavefronts up.  Behind the
+    // last step they read its lines once more.
     auto issue = [&](int part) {
         const uint32_t base = load_slot * D::STAGE;
         const int k = load_k * 128;
         constexpr int ALL = D::LA + D::LB;
 #pragma unroll
         for (int l = 0; l < ALL; ++l) {
-            if (l * 4 / ALL != part) continue;
+            if (l * 3 / ALL != part) continue;
             const bool of_w = l < D::LA;
             const int g = of_w ? wave * D::LA + l : wave * D::LB + l - D::LA;
             const int8_t *src = (of_w ? wp[of_w ? l : 0] : xp[of_w ? 0 : l - D::LA]) + k;
             if (k + 128 > a.k && k + chunk(8 * g + (lane >> 3)) >= a.k) src = reinterpret_cast<const int8_t *>(w8_zeros);
             load_to_lds(src, base + (of_w ? 0 : D::ASTAGE) + g * 1024);
         }
-        if (part < 3) return;
+        if (part < 2) return;
         load_slot = load_slot == D::STAGES - 1 ? 0 : load_slot + 1;
         if (++load_k == steps) {
             load_k = 0;
@@ -309,7 +226,8 @@ __global__ __launch_bounds__(64 * D::NW, D::NW * D::WGS / 4) void k_w8_tiles(W8L
 #pragma unroll
     for (int i = 0; i < D::STAGES - 1; ++i)
 #pragma unroll
-        for (int part = 0; part < 4; ++part) issue(part);
+        for (int part = 0; part < 3; ++part) issue(part);
+    issue(0);
     // Matrix step e of a stage takes k = 32 e + 16 hf + 0..15 of both sides.
     uint32_t aa[4], ba[4];
 #pragma unroll
@@ -323,9 +241,21 @@ __global__ __launch_bounds__(64 * D::NW, D::NW * D::WGS / 4) void k_w8_tiles(W8L
     for (int j = 0; j < D::FN; ++j) st[j] = a.x_scale[min(t0 + (wn * D::FN + j) * 32 + n, a.tokens - 1)];
 #pragma unroll
     for (int j = 0; j < D::FN; ++j) arrived(st[j]);
+    // A step's four products a tile: operands are read one ahead, so that those of step 3 are in registers before it.  There
+    // the barrier stands, for the next step's lines to have arrived and this one's stage to be free, and step 3's products
+    // cover the first reads behind it.
     int slot = 0, ready = 0;   // steps whose loads are known to have arrived
+    uint32_t base = 0;
+    i32x4 av[2][D::FM], bv[2][D::FN];
+    auto read = [&](int e) {
+#pragma unroll
+        for (int j = 0; j < D::FN; ++j) bv[e & 1][j] = lds_read<i32x4>(base + ba[e], j * 4096);
+#pragma unroll
+        for (int i = 0; i < D::FM; ++i) av[e & 1][i] = lds_read<i32x4>(base + aa[e], i * 4096);
+    };
     wait_vm<0>();
-    ready = D::STAGES - 1;
+    barrier_lds();
+    read(0);
     for (; mt < mt_end; ++mt) {
         i32x16 acc[D::FM][D::FN];
 #pragma unroll
@@ -334,46 +264,46 @@ __global__ __launch_bounds__(64 * D::NW, D::NW * D::WGS / 4) void k_w8_tiles(W8L
             for (int j = 0; j < D::FN; ++j)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
-        uint32_t base = 0;
+        auto multiply = [&](int e) {
+#pragma unroll
+            for (int i = 0; i < D::FM; ++i)
+#pragma unroll
+                for (int j = 0; j < D::FN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(av[e & 1][i], bv[e & 1][j], acc[i][j], 0, 0, 0);
+        };
+        uint32_t spent = 0;
         for (int k = 0; k < steps; ++k) {
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+                __builtin_amdgcn_sched_barrier(0);
+                read(e + 1);
+                multiply(e);
+                if (e < 2) issue(e + 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
             if (ready > 0)
                 --ready;
             else
                 wait_vm<(D::STAGES - 2) * (D::LA + D::LB)>();
             barrier_lds();
-            base = slot * D::STAGE;
+            spent = base;
             slot = slot == D::STAGES - 1 ? 0 : slot + 1;
-            i32x4 av[2][D::FM], bv[2][D::FN];
-            auto read = [&](int e) {
-#pragma unroll
-                for (int j = 0; j < D::FN; ++j) bv[e & 1][j] = lds_read<i32x4>(base + ba[e], j * 4096);
-#pragma unroll
-                for (int i = 0; i < D::FM; ++i) av[e & 1][i] = lds_read<i32x4>(base + aa[e], i * 4096);
-            };
+            base = slot * D::STAGE;
             read(0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                __builtin_amdgcn_sched_barrier(0);
-                if (e < 3) read(e + 1);
-#pragma unroll
-                for (int i = 0; i < D::FM; ++i)
-#pragma unroll
-                    for (int j = 0; j < D::FN; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(av[e & 1][i], bv[e & 1][j], acc[i][j], 0, 0, 0);
-                issue(e);
-            }
+            multiply(3);
+            if (k + 1 < steps) issue(0);
             __builtin_amdgcn_sched_barrier(0);
         }
         // The loads that are out, before the stores: a later count of loads must not wait for those.
         wait_vm<0>();
-        ready = D::STAGES - 1;
+        ready = D::STAGES - 2;
         for (int i = tid; i < D::TM; i += 64 * D::NW) {
             const int o = min(mt * D::TM + i, a.n_out - 1);
             lds_write<float>(D::L_SCALE + 4 * i, a.w_scale[o]);
             lds_write<float>(D::L_SCALE + 4 * D::TM + 4 * i, a.bias ? a.bias[o] : 0.0f);
         }
         barrier_lds();
-        const uint32_t at = base + wave * 32 * D::OROW;
+        const uint32_t at = spent + wave * 32 * D::OROW;
         constexpr int VEC = 16 / sizeof(T), PER = 32 * D::OF / VEC;   // channels of 16 bytes, lanes a token's run of them
         typedef T vec __attribute__((ext_vector_type(VEC)));
         typedef T four __attribute__((ext_vector_type(4)));
@@ -407,7 +337,8 @@ __global__ __launch_bounds__(64 * D::NW, D::NW * D::WGS / 4) void k_w8_tiles(W8L
                     }
                 }
             }
-        barrier_lds();   // the scales are read
+        barrier_lds();   // the scales are read, and the stage is free
+        issue(0);
     }
 }
 
@@ -433,12 +364,6 @@ hipError_t split(const W8LinearArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <class T, int MT, int NT, int W, int U, int DEPTH>
-hipError_t few(const W8LinearArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL((k_w8_few<T, MT, NT, W, U, DEPTH>), dim3((a.n_out + 16 * MT - 1) / (16 * MT)), dim3(64 * W), 0, st, a);
-    return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_w8_linear(const W8LinearArgs &a, int dtype, hipStream_t st) {
@@ -447,11 +372,9 @@ hipError_t launch_w8_linear(const W8LinearArgs &a, int dtype, hipStream_t st) {
 #ifdef FORCE
         return FORCE(a, st);
 #else
-        if (a.tokens <= 16) return few<T, 1, 1, 8, 4, 2>(a, st);
-        if (a.tokens <= 32) return few<T, 1, 2, 8, 2, 2>(a, st);
-        if (a.tokens <= 64) return few<T, 2, 4, 8, 2, 2>(a, st);
+        if (a.tokens <= 32) return a.n_out <= 2048 ? split<Split<T, 1, 1, 8, 4, 2>>(a, st) : split<Split<T, 1, 1, 4, 9, 2>>(a, st);
+        if (a.tokens <= 64) return split<Split<T, 1, 2, 4, 6, 2>>(a, st);
         if (a.tokens <= 256) return tiles<Tile<T, 128, 64, 4, 4, 3, 2>>(a, st);
-        if (a.tokens <= 1024) return tiles<Tile<T, 128, 128, 4, 2, 2, 2>>(a, st);
         return tiles<Tile<T, 256, 256, 8, 2, 2, 1>>(a, st);
 #endif
     });
