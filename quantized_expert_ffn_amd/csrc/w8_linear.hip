@@ -364,6 +364,20 @@ hipError_t split(const W8LinearArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
+// Channels of a workgroup where all tokens go with them: as few tiles of 32 as
+// let all workgroups run at once, a CU each (96 tokens, 6144 -> 6144: 19.0 us
+// with one, 26.5 with two; -> 12288: 34.2, 28.3 with two, 33.1 with three; ->
+// 24576: 51.1, 48.7, 37.7).  One tile of tokens has two workgroups a CU at any
+// size (32 tokens, 6144 -> 16384: 21.8 us with one, 21.4 with two).  Eight wavefronts where
+// channels are few and the chain along k is what counts (one token, 6144 ->
+// 2048: 6.6 us against 8.2; -> 8192: 11.6 against 11.3).
+template <class T, int FN, int S1, int W1, int S2, int S3>
+hipError_t split_by_channels(const W8LinearArgs &a, hipStream_t st) {
+    if (a.n_out <= 32 * 256) return split<Split<T, 1, FN, 4, S1, W1>>(a, st);
+    if (a.n_out <= 64 * 256) return split<Split<T, 2, FN, 4, S2, 1>>(a, st);
+    return split<Split<T, 3, FN, 4, S3, 1>>(a, st);
+}
+
 }  // namespace
 
 hipError_t launch_w8_linear(const W8LinearArgs &a, int dtype, hipStream_t st) {
@@ -373,8 +387,19 @@ hipError_t launch_w8_linear(const W8LinearArgs &a, int dtype, hipStream_t st) {
         return FORCE(a, st);
 #else
         if (a.tokens <= 32) return a.n_out <= 2048 ? split<Split<T, 1, 1, 8, 4, 2>>(a, st) : split<Split<T, 1, 1, 4, 9, 2>>(a, st);
-        if (a.tokens <= 64) return split<Split<T, 1, 2, 4, 6, 2>>(a, st);
-        if (a.tokens <= 256) return tiles<Tile<T, 128, 64, 4, 4, 3, 2>>(a, st);
+        if (a.tokens <= 64) return split_by_channels<T, 2, 6, 2, 9, 7>(a, st);
+        if (a.tokens <= 96) return split_by_channels<T, 3, 4, 2, 7, 6>(a, st);
+        if (a.tokens <= 128) return split_by_channels<T, 4, 7, 1, 6, 5>(a, st);
+        if (a.tokens <= 160) return split_by_channels<T, 5, 6, 1, 5, 4>(a, st);
+        // More tokens: rounds of workgroups by what one takes, in 42 us at k = 6144: 128 x 64 tiles, two a CU, 1 (0.65 if one
+        // a CU is enough); 256 x 128: 1.15; 256 x 256: 2.1.  512 tokens, 6144 -> 6144: 41.8, 47.4 and 87.5 us; 1024 tokens:
+        // 77.9, 49.4, 86.8; 2048 tokens: 122, 95.9, 88.6; 8192 tokens, -> 16384: 1210, 815, 750.
+        auto tiles_of = [&](int64_t m, int64_t n) { return (a.n_out + m - 1) / m * ((a.tokens + n - 1) / n); };
+        const int64_t small = tiles_of(128, 64);
+        const double c64 = small <= 256 ? 0.65 : (double)((small + 511) / 512);
+        const double c128 = 1.15 * (double)((tiles_of(256, 128) + 255) / 256), c256 = 2.1 * (double)((tiles_of(256, 256) + 255) / 256);
+        if (c64 <= c128 && c64 <= c256) return tiles<Tile<T, 128, 64, 4, 4, 3, 2>>(a, st);
+        if (c128 < c256) return tiles<Tile<T, 256, 128, 8, 4, 3, 1>>(a, st);
         return tiles<Tile<T, 256, 256, 8, 2, 2, 1>>(a, st);
 #endif
     });
