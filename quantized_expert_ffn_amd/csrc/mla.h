@@ -85,20 +85,24 @@ hipError_t launch_mla_decode_parts(const MlaDecodeArgs &a, const coli_mla_dims &
 struct MlaSharedArgs {
     MlaCache c;                   // the prefix's pages
     const void *q_lat, *q_pe;
-    const int32_t *kv_lens;       // the sequences' own tokens
+    const int32_t *kv_lens, *own_table;   // the sequences' own tokens, and their pages
     void *out;
     float *lse;
     uint32_t *status;
+    int64_t *plan;                // how the work is shared out
     float *part;                  // partial results over the prefix
     const float *own, *full;      // of the sequences' own tokens (MlaParts), or null
-    int32_t batch, n_q, heads, prefix, max_kv;
+    int32_t own_width, batch, n_q, heads, prefix, max_kv, shares;
+    int32_t whole;                // blocks of rows are of one sequence, and take its own tokens too
     MlaParts p;
     float scale;
 };
+// The sizes of a call and where its workspace's part is.
+MlaSharedArgs mla_shared_args(const coli_mla_dims &d, void *part, int batch, int n_q, int prefix, int max_kv);
 hipError_t launch_mla_shared(const MlaSharedArgs &a, const coli_mla_dims &d, hipStream_t st);
 hipError_t launch_mla_shared_join(const MlaSharedArgs &a, const coli_mla_dims &d, hipStream_t st);
 // Bytes of the prefix's partial results.
-size_t mla_shared_part_bytes(const coli_mla_dims &d, int64_t rows, int prefix);
+size_t mla_shared_part_bytes(const coli_mla_dims &d, int batch, int n_q, int prefix, int max_kv);
 
 struct MlaPrefillArgs {
     const void *q, *k_nope, *k_pe, *v;

@@ -98,7 +98,7 @@ SharedLayout shared_layout(const coli_mla_dims *d, int batch, int n_q, int prefi
     const MlaParts p = mla_decode_parts(*d, batch, n_q, max_kv);
     l.full = WS_HEAD + mla_decode_part_bytes(*d, batch, n_q, max_kv);
     l.prefix = l.full + 4 * (size_t)p.slot * p.blocks * batch;
-    l.total = l.prefix + mla_shared_part_bytes(*d, (int64_t)batch * n_q * d->n_heads, prefix_len);
+    l.total = l.prefix + mla_shared_part_bytes(*d, batch, n_q, prefix_len, max_kv);
     return l;
 }
 
@@ -292,22 +292,17 @@ int coli_mla_decode_shared(const coli_mla_dims *d, int32_t batch, int32_t n_q, c
     a.max_kv = max_kv;
     a.scale = d->softmax_scale;
     if (prefix_len == 0) return launched(launch_mla_decode(a, *d, st), "decode");
-    MlaSharedArgs s{};
+    MlaSharedArgs s = mla_shared_args(*d, base + at.prefix, batch, n_q, prefix_len, max_kv);
     s.c = cache(d, pages, kv_scale, n_pages, prefix_table, prefix_width);
     s.q_lat = q_lat;
     s.q_pe = q_pe;
     s.kv_lens = kv_lens;
+    s.own_table = table;
+    s.own_width = table_width;
     s.out = out;
     s.lse = lse;
     s.status = a.status;
-    s.part = reinterpret_cast<float *>(base + at.prefix);
-    s.batch = batch;
-    s.n_q = n_q;
-    s.heads = d->n_heads;
-    s.prefix = prefix_len;
-    s.max_kv = max_kv;
-    s.scale = d->softmax_scale;
-    if (max_kv > 0) {
+    if (max_kv > 0 && !s.whole) {
         s.own = a.part;
         s.full = a.full;
         s.p = mla_decode_parts(*d, batch, n_q, max_kv);

@@ -41,20 +41,49 @@ struct Shd {
     static_assert(LDS <= 160 * 1024, "the LDS of a CU");
 };
 
-// Work is shared out evenly in units of one tile of one block of rows.
+// Work is shared out evenly in units of one tile of one block of rows, blocks
+// in order.  Where blocks are of one sequence each (`whole`), its own tokens are
+// further tiles behind the prefix's, and blocks differ in length by sequence;
+// else all blocks have the prefix's tiles and the own tokens are apart.  A group
+// is the blocks of one length.
+//
+// A share that passes from one block to the next costs about as much as CROSS
+// tiles: queries to load, a pipeline to fill and one more result to write (64
+// blocks of 257 to 288 tiles: 206 us; each in four parts: 170).  Where that is
+// no worse, every block is cut into `parts` of its own, one a workgroup.
+constexpr int CROSS = 8;
 struct Units {
-    int64_t units;
-    int tiles, shares;
-    __host__ __device__ int64_t first(int g) const { return units * g / shares; }
+    int64_t total;
+    int shares, parts;   // parts: 0, or of each block
+    __device__ int64_t first(int g) const { return total * g / shares; }
     // the workgroup that has a unit
-    __host__ __device__ int owner(int64_t unit) const { return (int)(((unit + 1) * shares - 1) / units); }
+    __device__ int owner(int64_t unit) const { return (int)(((unit + 1) * shares - 1) / total); }
 };
-Units shd_units(int64_t rows, int prefix) {
-    Units u;
-    u.tiles = (prefix + SHD_TILE - 1) / SHD_TILE;
-    u.units = (rows + SHD_ROWS - 1) / SHD_ROWS * u.tiles;
-    u.shares = (int)(u.units < 256 ? u.units : 256);
-    return u;
+__host__ __device__ inline int tiles_of(int tokens) { return (tokens + SHD_TILE - 1) / SHD_TILE; }
+__host__ __device__ inline int64_t blocks_of(int64_t rows) { return (rows + SHD_ROWS - 1) / SHD_ROWS; }
+__host__ __device__ inline bool whole_blocks(int64_t rows_of_sequence) { return rows_of_sequence % SHD_ROWS == 0; }
+
+// Most workgroups, each of which takes a CU.
+int shd_shares(int64_t rows, int prefix, int max_kv) {
+    const int64_t units = blocks_of(rows) * ((int64_t)tiles_of(prefix) + tiles_of(max_kv));
+    return (int)(units < 256 ? units : 256);
+}
+
+// Behind the plan, the groups' first units and the parts of a block, come the
+// partial results.
+size_t shd_plan_bytes(int batch) { return (8 * ((size_t)batch + 2) + 255) & ~(size_t)255; }
+
+__device__ __forceinline__ int64_t wave_scan64(int64_t v) {
+    const int lane = threadIdx.x & 63;
+    for (int o = 1; o < 64; o += o) {
+        const int64_t u = __shfl_up(v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    return (int64_t)(uint32_t)uniform((int)v) | (int64_t)uniform((int)(v >> 32)) << 32;
 }
 
 // A product whose sum stays in ordinary registers, beside accumulators that
@@ -98,16 +127,65 @@ __device__ __forceinline__ void acc_settled() { asm volatile("s_nop 15\n\ts_nop 
 
 __device__ __forceinline__ int shd_swz(int t) { return 4 * ((t >> 1) & 1) + 2 * ((t >> 2) & 1) + ((t >> 3) & 1); }
 
-// The tokens of the prefix that a query row sees: all, unless its sequence has
-// fewer tokens of its own than new ones.
+// The tokens that a query row sees of its sequence's own, 0 or fewer where it
+// ends in the prefix.
 __device__ __forceinline__ int shd_seen(const MlaSharedArgs &a, int64_t row) {
     const int per = a.n_q * a.heads, b = (int)(row / per), j = (int)(row - (int64_t)b * per) / a.heads;
-    const int len = mla_len(a.kv_lens, b, a.max_kv, a.status);
-    return max(0, a.prefix + min(0, len - a.n_q + 1 + j));
+    return mla_len(a.kv_lens, b, a.max_kv, a.status) - a.n_q + 1 + j;
+}
+
+// The units a call has, those of workgroup g, and the group that they begin in.
+struct Place {
+    Units u;
+    int64_t unit, end, group_first;
+    int group;
+};
+__device__ __forceinline__ Place shd_units(const MlaSharedArgs &a, int groups, int blocks, int g) {
+    const int lane = threadIdx.x & 63, prefix = tiles_of(a.prefix);
+    auto tiles_at = [&](int b) { return b < groups ? prefix + (a.whole ? tiles_of(mla_len(a.kv_lens, b, a.max_kv, a.status)) : 0) : 0; };
+    Place p{};
+    int longest = 0;
+    for (int b = 0; b < groups; b += 64) {
+        const int t = tiles_at(b + lane);
+        p.u.total += uniform64(__shfl(wave_scan64((int64_t)t * blocks), 63));
+        for (int o = 32, v = t; o; o >>= 1) longest = max(longest, v = max(v, __shfl_xor(v, o)));
+    }
+    longest = uniform(longest);
+    p.u.shares = (int)min(p.u.total, (int64_t)a.shares);
+    const int parts = (int)(p.u.shares / ((int64_t)groups * blocks));
+    if (parts > 0 && parts <= prefix && (longest + parts - 1) / parts <= p.u.total / p.u.shares + CROSS) p.u.parts = parts;
+    int64_t base = 0;
+    p.group = -1;
+    p.unit = p.u.first(min(g, p.u.shares));
+    p.end = p.u.first(min(g + 1, p.u.shares));
+    for (int b = 0; b < groups; b += 64) {
+        const int64_t mine = (int64_t)tiles_at(b + lane) * blocks, incl = wave_scan64(mine);
+        if (g == 0 && threadIdx.x < 64 && b + lane < groups) a.plan[b + lane] = base + incl - mine;
+        const uint64_t hit = __ballot(b + lane < groups && base + incl > p.unit);
+        if (p.group < 0 && hit) {
+            const int l = __builtin_ctzll(hit);
+            p.group = uniform(b + l);
+            p.group_first = base + uniform64(__shfl(incl - mine, l));
+        }
+        base += uniform64(__shfl(incl, 63));
+    }
+    if (g == 0 && threadIdx.x == 0) {
+        a.plan[groups] = base;
+        a.plan[groups + 1] = p.u.parts;
+    }
+    if (p.u.parts) {
+        const int blk = g / parts, part = g - blk * parts;
+        p.group = blk / blocks;
+        p.group_first = 0;
+        const int64_t tiles = p.group < groups ? uniform(tiles_at(p.group)) : 0, at = (blk - p.group * blocks) * tiles;
+        p.unit = at + tiles * part / parts;
+        p.end = at + tiles * (part + 1) / parts;
+    }
+    return p;
 }
 
 template <class D>
-__global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u) {
+__global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a) {
     using T = typename D::T;
     constexpr int RANK = D::RANK, CT = D::CT, KS = D::KS;
     constexpr bool FP8 = D::FP8;
@@ -116,8 +194,15 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int n = lane & 31, hf = lane >> 5, g = blockIdx.x;
     const int64_t rows = (int64_t)a.batch * a.n_q * a.heads;
-    int64_t unit = u.first(g);
-    const int64_t end = u.first(g + 1);
+    const int groups = a.whole ? a.batch : 1, prefix_tiles = tiles_of(a.prefix);
+    const int blocks = (int)(a.whole ? a.n_q * a.heads / SHD_ROWS : blocks_of(rows));   // of a group
+    const Place mine = shd_units(a, groups, blocks, g);
+    int64_t unit = mine.unit, group_first = mine.group_first;
+    const int64_t end = mine.end;
+    int group = mine.group;
+    // the segment's own tokens, if it has any here: how many, the tile they begin with, their pages
+    int own_len = 0, own_from = INT32_MAX;
+    const int32_t *own_row = a.own_table;
     const float scale = a.scale * LOG2E;
     const uint32_t page_inv = 0xffffffffu / (uint32_t)a.c.page;
     bool bad_page = false;
@@ -134,21 +219,24 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
     auto slot_in_ring = [](int tile) { return (uint32_t)tile % (uint32_t)D::RING; };
     auto base_of = [&](int tile) { return slot_in_ring(tile) * D::TILE; };
     auto scale_of = [&](int tile) { return 4 * slot_in_ring(tile) * SHD_TILE; };
-    struct Place {
+    struct Where {
         int page, in;
     };
-    auto place = [&](int tile) {
-        const int t = min(tile * SHD_TILE + lt, a.prefix - 1), pi = div_by(t, a.c.page, page_inv);
-        return Place{pi, t - pi * a.c.page};
+    auto place = [&](int tile) {   // behind a part's end: its last token again
+        const bool own = tile >= own_from;
+        const int start = (own ? tile - own_from : tile) * SHD_TILE, last = (own ? own_len : a.prefix) - 1;
+        const int t = min(start + lt, last), pi = div_by(t, a.c.page, page_inv);
+        return Where{pi, t - pi * a.c.page};
     };
-    auto slot_of = [&](int id, const Place &p) {
+    auto table_of = [&](int tile) { return tile >= own_from ? own_row : a.c.table; };
+    auto slot_of = [&](int id, const Where &p) {
         const bool bad = (uint32_t)id >= (uint32_t)a.c.n_pages;
         bad_page |= bad;
         return (int64_t)(bad ? 0 : id) * a.c.page + p.in;
     };
     // page ids go to LDS two tiles before the rows do
     const uint32_t id_at = D::L_ID + wave * 256;
-    auto issue_id = [&](int tile) { load_word_to_lds(a.c.table + place(tile).page, id_at + (tile & 3) * 1024); };
+    auto issue_id = [&](int tile) { load_word_to_lds(table_of(tile) + place(tile).page, id_at + (tile & 3) * 1024); };
     // plain rows go to their place in the ring, codes to one of two buffers
     constexpr int OPS = FP8 ? D::LINES + 1 : D::LINES;   // loads of a tile
     auto raw_of = [&](int tile) { return (uint32_t)(D::L_RAW + ((tile & 1) * 4 + wave) * D::RAW); };
@@ -230,10 +318,15 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
     };
 
     while (unit < end) {
-        const int blk = (int)(unit / u.tiles), lo = (int)(unit - (int64_t)blk * u.tiles);
-        const int hi = (int)min((int64_t)u.tiles, lo + end - unit);
+        own_len = a.whole ? uniform(mla_len(a.kv_lens, group, a.max_kv, a.status)) : 0;
+        own_from = own_len > 0 ? prefix_tiles : INT32_MAX;
+        own_row = a.own_table + (int64_t)group * a.own_width;
+        const int tiles = prefix_tiles + tiles_of(own_len);
+        const int in_group = (int)((unit - group_first) / tiles), lo = (int)(unit - group_first - (int64_t)in_group * tiles);
+        const int hi = (int)min((int64_t)tiles, lo + end - unit);
+        const int64_t blk = (int64_t)group * blocks + in_group;
         unit += hi - lo;
-        const int64_t row = (int64_t)blk * SHD_ROWS + 32 * wave + n, wave_row = (int64_t)blk * SHD_ROWS + 32 * wave;
+        const int64_t row = blk * SHD_ROWS + 32 * wave + n, wave_row = blk * SHD_ROWS + 32 * wave;
         const bool works = wave_row < rows;
         const int64_t at_row = row < rows ? row : rows - 1;
         issue_id(lo);
@@ -246,16 +339,22 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
             qf[s] = *reinterpret_cast<const x8<T> *>(s < RANK / 16
                                                          ? static_cast<const T *>(a.q_lat) + at_row * RANK + 16 * s + 8 * hf
                                                          : static_cast<const T *>(a.q_pe) + at_row * MLA_ROPE + 16 * (s - RANK / 16) + 8 * hf);
+        // Tokens that a row sees of its own and of the prefix; the least of a wavefront's rows and of the block's.
         const int seen = shd_seen(a, at_row);
         int wave_seen = seen;
         for (int o = 16; o; o >>= 1) wave_seen = min(wave_seen, __shfl_xor(wave_seen, o));
         wave_seen = uniform(wave_seen);
-        int block_seen = a.prefix;   // the least of the block's rows
-        for (int64_t r = (int64_t)blk * SHD_ROWS + lane; r < min((int64_t)(blk + 1) * SHD_ROWS, rows); r += 64)
-            block_seen = min(block_seen, shd_seen(a, r));
+        int block_seen = INT32_MAX;
+        for (int64_t r = blk * SHD_ROWS + lane; r < min((blk + 1) * SHD_ROWS, rows); r += 64) block_seen = min(block_seen, shd_seen(a, r));
         for (int o = 32; o; o >>= 1) block_seen = min(block_seen, __shfl_xor(block_seen, o));
         block_seen = uniform(block_seen);
-        const int partly = block_seen < a.prefix ? block_seen : INT32_MAX;   // tiles that end behind it
+        // Of tile t, the first token that some row does not see though it exists; SHD_TILE if there is none.
+        auto hidden = [&](int t) {
+            const bool own = t >= prefix_tiles;
+            const int least = own ? block_seen : a.prefix + min(0, block_seen), all = own ? own_len : a.prefix;
+            const int from = max(0, least - (own ? t - prefix_tiles : t) * SHD_TILE);
+            return least < all && from < SHD_TILE ? from : SHD_TILE;
+        };
 #pragma unroll
         for (int s = 0; s < KS; ++s) arrived(qf[s]);
         wait_vm<0>();
@@ -328,10 +427,11 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
             if constexpr (STEADY) issue_scale(x);
             issue_id(tile + 4);
             __builtin_amdgcn_sched_barrier(0);
-            const int t0 = tile * SHD_TILE;
-            if (t0 + SHD_TILE > wave_seen) {
+            const bool own = tile >= prefix_tiles;
+            const int t0 = (own ? tile - prefix_tiles : tile) * SHD_TILE;
+            if (t0 + SHD_TILE > (own ? wave_seen : a.prefix + min(0, wave_seen))) {
                 settled(s);
-                int rem = seen - t0 - 4 * hf;
+                int rem = (own ? seen : a.prefix + min(0, seen)) - t0 - 4 * hf;
                 arrived(rem);   // a branch, not selects that every tile would pay for
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
@@ -439,14 +539,14 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
             // plain rows: tile i + 1 has come, i + 2 is out; codes: those of tile i + 2 have come
             wait_vm<FP8 ? 1 : OPS + 1>();
             barrier_lds();   // tile i + 1 is there, and every wavefront is done with tile i - 1
-            if ((i + 1) * SHD_TILE > partly) clear(i, max(0, block_seen - i * SHD_TILE));
+            if (const int from = hidden(i); from < SHD_TILE) clear(i, from);
             score(i + 1, std::true_type());
             values(i, std::true_type());
             take();
         }
-        if ((i + 1) * SHD_TILE > partly) {
+        if (const int from = hidden(i); from < SHD_TILE) {
             barrier_lds();
-            clear(i, max(0, block_seen - i * SHD_TILE));
+            clear(i, from);
         }
         values(i, std::false_type());
         wait_vm<0>();
@@ -458,7 +558,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
         if (works) {
             const float half_off = FP8 && l != 0.0f ? __builtin_amdgcn_exp2f(0.5f * (mv - m)) : 1.0f;
             const float by = l == 0.0f ? 0.0f : half_off / l;
-            float *dst = a.part + (int64_t)(g + blk) * D::SLOT, *at = dst + wave * CT * 1024 + 4 * lane;
+            float *dst = a.part + (g + blk) * D::SLOT, *at = dst + wave * CT * 1024 + 4 * lane;
 #pragma unroll
             for (int c = 0; c < CT; ++c) {
 #pragma unroll
@@ -472,6 +572,10 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
             }
             if (hf == 0) *reinterpret_cast<float2 *>(dst + SHD_ROWS * RANK + 2 * (32 * wave + n)) = make_float2(m, l);
         }
+        if (hi == tiles && in_group + 1 == blocks) {
+            group_first += (int64_t)blocks * tiles;
+            ++group;
+        }
     }
     if (bad_page) raise_status(a.status, ST_BADPAGE);
 }
@@ -481,7 +585,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_shared(MlaSharedArgs a, Units u)
 // wavefront has 32 rows by 8 COLS columns.  W > 1: a workgroup's wavefronts take every
 // W-th partial each of one such piece, for few rows in many parts.
 template <class T, int RANK, int W, int COLS>
-__global__ __launch_bounds__(W > 1 ? 64 * W : 256) void k_mla_shared_join(MlaSharedArgs a, Units u) {
+__global__ __launch_bounds__(W > 1 ? 64 * W : 256) void k_mla_shared_join(MlaSharedArgs a) {
     constexpr int SLOT = SHD_ROWS * RANK + 2 * SHD_ROWS, PIECES = RANK / 8 / COLS;
     constexpr float NEG = -__builtin_inff();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 31;
@@ -533,16 +637,27 @@ __global__ __launch_bounds__(W > 1 ? 64 * W : 256) void k_mla_shared_join(MlaSha
         }
     };
     {
-        const int64_t blk = row / SHD_ROWS, unit = blk * u.tiles;
-        const int r = (int)(row - blk * SHD_ROWS), g0 = u.owner(unit), g1 = u.owner(unit + u.tiles - 1);
+        // the block's units, from the plan: a piece's rows are of one block
+        const int64_t blk = uniform((int)(id / PIECES * 32 / SHD_ROWS));
+        const int group = a.whole ? (int)(blk / (a.n_q * a.heads / SHD_ROWS)) : 0;
+        const int groups = a.whole ? a.batch : 1, parts = (int)a.plan[groups + 1];
+        int64_t g0 = blk * parts, g1 = g0 + parts - 1;
+        if (!parts) {
+            const int64_t blocks = a.whole ? a.n_q * a.heads / SHD_ROWS : blocks_of(rows), total = a.plan[groups];
+            const Units u{total, (int)min(total, (int64_t)a.shares), 0};
+            const int64_t tiles = (a.plan[group + 1] - a.plan[group]) / blocks, unit = a.plan[group] + (blk - group * blocks) * tiles;
+            g0 = u.owner(unit);
+            g1 = u.owner(unit + tiles - 1);
+        }
+        const int r = (int)(row - blk * SHD_ROWS);
         const int col = (r / 32 * (RANK / 8) + piece * COLS) * 256 + 4 * lane, stat = SHD_ROWS * RANK + 2 * r;
-        add(part, g1 - g0 + 1, [&](int i, const float *&base, const float *&stats) {
+        add(part, (int)(g1 - g0) + 1, [&](int i, const float *&base, const float *&stats) {
             const float *slot = a.part + (g0 + i + blk) * SLOT;
             base = slot + col;
             stats = slot + stat;
         });
     }
-    if (a.own) {
+    if (a.own) {   // own tokens apart
         const int per = a.n_q * a.heads, b = (int)(at_row / per), w = (int)(at_row - (int64_t)b * per);
         const int block = w / a.p.rows, r = w - block * a.p.rows;
         const int32_t *plan = reinterpret_cast<const int32_t *>(a.own) + 2 * b;
@@ -601,36 +716,50 @@ hipError_t with_shape(const coli_mla_dims &d, F f) {
 
 constexpr int JOIN_DEEP = 32, JOIN_COLS = 4;
 
-size_t mla_shared_part_bytes(const coli_mla_dims &d, int64_t rows, int prefix) {
+size_t mla_shared_part_bytes(const coli_mla_dims &d, int batch, int n_q, int prefix, int max_kv) {
     // slots are counted by workgroup + block of rows: a bound that grows with each argument
-    const Units u = shd_units(rows, prefix);
-    return 4 * (size_t)(SHD_ROWS * d.rank + 2 * SHD_ROWS) * (size_t)(u.shares + (rows + SHD_ROWS - 1) / SHD_ROWS);
+    const int64_t rows = (int64_t)batch * n_q * d.n_heads;
+    return shd_plan_bytes(batch) +
+           4 * (size_t)(SHD_ROWS * d.rank + 2 * SHD_ROWS) * (size_t)(shd_shares(rows, prefix, max_kv) + blocks_of(rows));
+}
+
+MlaSharedArgs mla_shared_args(const coli_mla_dims &d, void *part, int batch, int n_q, int prefix, int max_kv) {
+    MlaSharedArgs a{};
+    a.plan = static_cast<int64_t *>(part);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(part) + shd_plan_bytes(batch));
+    a.batch = batch;
+    a.n_q = n_q;
+    a.heads = d.n_heads;
+    a.prefix = prefix;
+    a.max_kv = max_kv;
+    a.scale = d.softmax_scale;
+    a.whole = whole_blocks((int64_t)n_q * d.n_heads);
+    a.shares = shd_shares((int64_t)batch * n_q * d.n_heads, prefix, a.whole ? max_kv : 0);
+    return a;
 }
 
 hipError_t launch_mla_shared(const MlaSharedArgs &a, const coli_mla_dims &d, hipStream_t st) {
-    const Units u = shd_units((int64_t)a.batch * a.n_q * a.heads, a.prefix);
     return with_shape(d, [&](auto shape) {
         using D = decltype(shape);
         const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_mla_shared<D>), D::LDS);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(k_mla_shared<D>, dim3(u.shares), dim3(256), D::LDS, st, a, u);
+        hipLaunchKernelGGL(k_mla_shared<D>, dim3(a.shares), dim3(256), D::LDS, st, a);
         return hipGetLastError();
     });
 }
 
 hipError_t launch_mla_shared_join(const MlaSharedArgs &a, const coli_mla_dims &d, hipStream_t st) {
     const int64_t rows = (int64_t)a.batch * a.n_q * a.heads;
-    const Units u = shd_units(rows, a.prefix);
     return with_shape(d, [&](auto shape) {
         using D = decltype(shape);
         const int64_t groups = (rows + 31) / 32, pieces = D::RANK / 8;
         // parts of a row: those of the prefix, and of its own tokens
         if (groups <= JOIN_DEEP)
             hipLaunchKernelGGL((k_mla_shared_join<typename D::T, D::RANK, 16, 1>), dim3((uint32_t)(groups * pieces)), dim3(1024), 0, st,
-                               a, u);
+                               a);
         else
             hipLaunchKernelGGL((k_mla_shared_join<typename D::T, D::RANK, 1, JOIN_COLS>),
-                               dim3((uint32_t)((groups * (pieces / JOIN_COLS) + 3) / 4)), dim3(256), 0, st, a, u);
+                               dim3((uint32_t)((groups * (pieces / JOIN_COLS) + 3) / 4)), dim3(256), 0, st, a);
         return hipGetLastError();
     });
 }

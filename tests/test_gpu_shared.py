@@ -95,6 +95,16 @@ def test_shared_many_rows_and_splits(fp8, prefix, batch, n_q, heads):
     run(gen(batch), prefix, lens, n_q, heads, 512 if heads > 64 else 256, BF, fp8, 16)
 
 
+@pytest.mark.parametrize("dtype,fp8", [(BF, False), (FP, False), (BF, True), (FP, True)])
+@pytest.mark.parametrize("prefix,lens,n_q,heads", [
+    (1, [1], 1, 128), (31, [0, 0, 5], 1, 256), (700, [300, 0, 1, 33, 64], 2, 64), (64, [40] * 70, 1, 128), (9000, [5000, 3], 1, 128),
+    (50, [2, 0, 31, 900], 4, 32), (3, [0, 1, 2, 3, 4], 8, 16), (100, [129, 7], 128, 1), (96, [257, 300, 31], 16, 128)])
+def test_shared_blocks_of_one_sequence(dtype, fp8, prefix, lens, n_q, heads):
+    """Rows of a sequence that fill blocks: its own tokens follow the prefix's there."""
+    say("shared whole", dtype, fp8, prefix, lens, n_q, heads)
+    run(gen(prefix + len(lens)), prefix, lens, n_q, heads, 512 if len(lens) < 6 else 256, dtype, fp8, 48)
+
+
 def test_shared_many_sequences():
     """Own tokens in the plan of more than 64 sequences, whole and in parts."""
     say("shared sequences")
@@ -103,6 +113,7 @@ def test_shared_many_sequences():
     lens[70], lens[140] = 5000, 777
     run(gen(3), 70, lens, 1, 20, 256, FP, False, 16)
     run(gen(3), 70, lens, 2, 32, 256, BF, True, 16)
+    run(gen(3), 70, lens, 2, 64, 256, BF, True, 16)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -114,7 +125,7 @@ def test_shared_peaked_scores(fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("heads,n_q", [(5, 4), (64, 4)])
+@pytest.mark.parametrize("heads,n_q", [(5, 4), (64, 4), (24, 4)])
 @pytest.mark.parametrize("value", [NAN, float("inf")])
 def test_shared_masked_tokens_may_hold_anything(fp8, heads, n_q, value):
     """The last tokens of the prefix are not finite: a query whose sequence begins so late does not see them."""
@@ -134,6 +145,28 @@ def test_shared_masked_tokens_may_hold_anything(fp8, heads, n_q, value):
     for b, m in enumerate(lens):
         clean = max(0, n_q - 1 - m)   # queries that end before the prefix's last token
         assert out[b, :clean].isfinite().all() and lse[b, :clean].isfinite().all() and out[b, clean:].isnan().any(-1).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads,n_q", [(5, 4), (64, 4)])
+def test_shared_unseen_drafts_may_hold_anything(fp8, heads, n_q):
+    """The last own token is not finite: the queries before it do not see it."""
+    for value in (NAN, float("inf")):
+        say("shared poisoned drafts", fp8, heads, n_q, value)
+        page, prefix, rank, lens = 16, 40, 512, [77, 4, 33]
+
+        def poison(pages, scale, table):
+            flat = pages.view(-1, pages.shape[-1])
+            for b, n in enumerate(lens):
+                s = ref.slots_of(table, b, n, page)[-1]
+                if fp8:
+                    flat[s, :rank] = 0x7f
+                    scale[s] = value
+                else:
+                    flat[s] = value
+        out, lse = run(gen(4), prefix, lens, n_q, heads, rank, BF, fp8, page, poison)
+        out, lse = out.view(3, n_q, heads, rank), lse.view(3, n_q, heads)
+        assert out[:, :-1].isfinite().all() and lse[:, :-1].isfinite().all() and out[:, -1].isnan().any(-1).all()
 
 
 def test_shared_queries_that_see_nothing():
