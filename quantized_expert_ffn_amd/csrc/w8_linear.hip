@@ -34,14 +34,15 @@ __device__ __forceinline__ int swz(int r) { return 4 * ((r >> 1) & 1) + 2 * ((r 
 // All tokens by 32 FM channels a workgroup, so that weights pass once and many
 // workgroups share them out.  Steps of NW / 4 lines of 128 along k go through a
 // ring of LDS stages, and each of the NW wavefronts multiplies 32 of every
-// step; their sums meet in LDS at the end, 32 x 32 tiles at a time.
+// step; their sums meet in LDS at the end, BATCH tiles of 32 x 32 at a time.
 template <class T_, int FM_, int FN_, int NW_, int STAGES_, int WGS_>
 struct Split {
     using T = T_;
     static constexpr int FM = FM_, FN = FN_, NW = NW_, STAGES = STAGES_, WGS = WGS_, TM = 32 * FM, TN = 32 * FN, STEP = 32 * NW;
     static constexpr int LINE = (TM + TN) * 128, STAGE = LINE * NW / 4, LOADS = FM + FN;   // 1 KiB loads a wavefront and step
-    static constexpr int OROW = 36 * 4, SUMS = NW * 4096, OUT = 32 * OROW;
-    static constexpr int RING = STAGES * STAGE, LDS = RING > SUMS + OUT ? RING : SUMS + OUT;
+    static constexpr int OROW = 36 * 4, SUMS = NW * 4096, OUT = 32 * OROW;   // of a 32 x 32 tile's join
+    static constexpr int ROOM = 160 * 1024 / WGS / (SUMS + OUT), TILES = FM * FN < 4 ? FM * FN : 4, BATCH = TILES < ROOM ? TILES : ROOM;
+    static constexpr int RING = STAGES * STAGE, JOIN = BATCH * (SUMS + OUT), LDS = RING > JOIN ? RING : JOIN;
     static_assert(LDS * WGS <= 160 * 1024 && (STAGES - 2) * LOADS < 64, "LDS, loads that are out");
 };
 
@@ -108,30 +109,38 @@ __global__ __launch_bounds__(64 * D::NW, D::WGS * D::NW / 4) void k_w8_split(W8L
     wait_vm<0>();
     typedef T four __attribute__((ext_vector_type(4)));
 #pragma unroll
-    for (int p = 0; p < D::FM * D::FN; ++p) {
-        const int i = p / D::FN, j = p % D::FN;
-        barrier_lds();   // the ring, or the tile before, is done with
+    for (int p0 = 0; p0 < D::FM * D::FN; p0 += D::BATCH) {
+        constexpr int ALL = D::FM * D::FN;
+        const int count = p0 + D::BATCH < ALL ? D::BATCH : ALL - p0;
+        barrier_lds();   // the ring, or the tiles before, are done with
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            lds_write((wave * 4 + q) * 1024 + 16 * lane, i32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]});
+        for (int x = 0; x < D::BATCH; ++x) {
+            if (p0 + x >= ALL) continue;
+            const i32x16 &c = acc[(p0 + x) / D::FN][(p0 + x) % D::FN];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                lds_write(x * D::SUMS + (wave * 4 + q) * 1024 + 16 * lane, i32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]});
+        }
         barrier_lds();
-        if (wave < 4) {   // eight of the tile's channels each
-            i32x4 sum = lds_read<i32x4>(wave * 1024 + 16 * lane);
+        for (int task = wave; task < 4 * count; task += D::NW) {   // eight of a tile's channels
+            const int x = task >> 2, q = task & 3, i = (p0 + x) / D::FN, j = (p0 + x) % D::FN;
+            i32x4 sum = lds_read<i32x4>(x * D::SUMS + q * 1024 + 16 * lane);
 #pragma unroll
-            for (int w = 1; w < D::NW; ++w) sum += lds_read<i32x4>((w * 4 + wave) * 1024 + 16 * lane);
+            for (int w = 1; w < D::NW; ++w) sum += lds_read<i32x4>(x * D::SUMS + (w * 4 + q) * 1024 + 16 * lane);
             const float st = a.x_scale[min(32 * j + n, a.tokens - 1)];
             f32x4 v;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int o = min(o0 + 32 * i + 8 * wave + 4 * hf + k, a.n_out - 1);
+                const int o = min(o0 + 32 * i + 8 * q + 4 * hf + k, a.n_out - 1);
                 v[k] = finish(sum[k], st, a.w_scale[o], a.bias ? a.bias[o] : 0.0f, a.bias != nullptr);
             }
-            lds_write(D::SUMS + n * D::OROW + 32 * wave + 16 * hf, v);
+            lds_write(D::BATCH * D::SUMS + x * D::OUT + n * D::OROW + 32 * q + 16 * hf, v);
         }
         barrier_lds();
-        if (wave < 4) {   // tokens' runs of 32 channels, eight lanes each
-            const int r = 8 * wave + (lane >> 3), t = 32 * j + r, o = o0 + 32 * i + 4 * (lane & 7);
-            const f32x4 v = lds_read<f32x4>(D::SUMS + r * D::OROW + 16 * (lane & 7));
+        for (int task = wave; task < 4 * count; task += D::NW) {   // eight tokens' runs of 32 channels, eight lanes each
+            const int x = task >> 2, i = (p0 + x) / D::FN, j = (p0 + x) % D::FN, r = 8 * (task & 3) + (lane >> 3);
+            const int t = 32 * j + r, o = o0 + 32 * i + 4 * (lane & 7);
+            const f32x4 v = lds_read<f32x4>(D::BATCH * D::SUMS + x * D::OUT + r * D::OROW + 16 * (lane & 7));
             if (t < a.tokens) {
                 T *dst = static_cast<T *>(a.out) + (int64_t)t * a.o_stride + o;
                 if (wide_out && o + 4 <= a.n_out) {
