@@ -11,12 +11,6 @@
 namespace coli {
 namespace {
 
-#ifndef ROT
-#define ROT 1
-#endif
-
-typedef int32_t i32x4v __attribute__((ext_vector_type(4)));
-
 // Where chunks behind the end of a row read.
 __device__ const uint4 w8_zeros[8] = {};
 
@@ -62,7 +56,7 @@ __global__ __launch_bounds__(64 * D::NW, D::WGS * D::NW / 4) void k_w8_split(W8L
     }
     // Rows are often a power of two apart, or nearly so, and the lines of a step then lie in few channels of the L2: each
     // workgroup of an XCD begins elsewhere along k, and goes round.
-    const int turn = ROT ? (int)((int64_t)(blockIdx.x >> 3) * steps / ((gridDim.x + 7) >> 3)) : 0;
+    const int turn = (int)((int64_t)(blockIdx.x >> 3) * steps / ((gridDim.x + 7) >> 3));
     int load = turn, load_slot = 0;
     auto issue = [&] {   // behind the last step nothing is read that counts
         const int k = load * D::STEP;
@@ -392,9 +386,6 @@ hipError_t split_by_channels(const W8LinearArgs &a, hipStream_t st) {
 hipError_t launch_w8_linear(const W8LinearArgs &a, int dtype, hipStream_t st) {
     return w8_with_type(dtype, [&](auto t) {
         using T = decltype(t);
-#ifdef FORCE
-        return FORCE(a, st);
-#else
         if (a.tokens <= 32) return a.n_out <= 2048 ? split<Split<T, 1, 1, 8, 4, 2>>(a, st) : split<Split<T, 1, 1, 4, 9, 2>>(a, st);
         if (a.tokens <= 64) return split_by_channels<T, 2, 6, 2, 9, 7>(a, st);
         if (a.tokens <= 96) return split_by_channels<T, 3, 4, 2, 7, 6>(a, st);
@@ -410,7 +401,6 @@ hipError_t launch_w8_linear(const W8LinearArgs &a, int dtype, hipStream_t st) {
         if (c64 <= c128 && c64 <= c256) return tiles<Tile<T, 128, 64, 4, 4, 3, 2>>(a, st);
         if (c128 < c256) return tiles<Tile<T, 256, 128, 8, 4, 3, 1>>(a, st);
         return tiles<Tile<T, 256, 256, 8, 2, 2, 1>>(a, st);
-#endif
     });
 }
 

