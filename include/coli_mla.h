@@ -144,8 +144,9 @@ size_t coli_mla_shared_workspace_bytes(const coli_mla_dims *dims, int32_t batch,
 /*
  * coli_mla_decode for sequences that begin with the same cached tokens:
  * sequence b is the prefix_len tokens of prefix_table, then kv_lens[b] tokens
- * of its own in its pages of table.  The prefix is read once for the rows of
- * all sequences.  The n_q new tokens are the last of the whole sequence:
+ * of its own in its pages of table.  The prefix is read once for every 128
+ * rows of all sequences, or by each sequence for itself where that is faster.
+ * The n_q new tokens are the last of the whole sequence:
  * query j sees its first prefix_len + kv_lens[b] - n_q + 1 + j tokens (a
  * sequence of fewer own tokens than n_q has some of them in the prefix), and
  * one that sees none gets zeros and lse = -inf.
@@ -160,6 +161,12 @@ int coli_mla_decode_shared(const coli_mla_dims *dims, int32_t batch, int32_t n_q
                            int32_t prefix_width, int32_t prefix_len, const int32_t *table, int32_t table_width,
                            const int32_t *kv_lens, int32_t max_kv, void *out, float *lse, void *ws, size_t ws_bytes,
                            void *stream);
+
+/* Test hook: how later coli_mla_decode_shared calls in this process read the
+ * prefix: 0 whichever is faster (default), 1 once for blocks of rows of all
+ * sequences, 2 each sequence for itself (where prefix_len + max_kv is a length
+ * that coli_mla_decode takes).  Results differ by rounding alone. */
+int coli_mla_debug_shared_path(int32_t path);
 
 /*
  * Keys and values of every head out of the paged latents, for a ragged

@@ -407,7 +407,7 @@ def coli_moe_roof_mfma_i8(iters: int, sink, stream=None):
 from .mla import (  # noqa: E402,F401
     COLI_BF16, COLI_F32, COLI_FP16, COLI_KV_E4M3, COLI_KV_PLAIN, COLI_MLA_MAX_BATCH, COLI_MLA_MAX_LENGTH, COLI_MLA_MAX_ROWS,
     COLI_MLA_MAX_SHARED_ROWS, COLI_MLA_ROPE, COLI_ROPE_HALVES, COLI_ROPE_PAIRS, MLA_EXPORTS, coli_mla_append, coli_mla_decode,
-    coli_mla_decode_shared, coli_mla_dims, coli_mla_expand, coli_mla_prefill, coli_mla_project, coli_mla_row_bytes,
+    coli_mla_debug_shared_path, coli_mla_decode_shared, coli_mla_dims, coli_mla_expand, coli_mla_prefill, coli_mla_project, coli_mla_row_bytes,
     coli_mla_shared_workspace_bytes, coli_mla_workspace_bytes, make_mla_dims)
 from . import mla  # noqa: E402
 

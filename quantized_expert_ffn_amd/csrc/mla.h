@@ -61,10 +61,13 @@ struct MlaDecodeArgs {
     uint32_t *status;
     float *part;                  // partial results (workspace)
     float *full;                  // and those of whole sequences, where only partial results are wanted
-    int32_t batch, n_q, heads, max_kv;
+    const int32_t *prefix_table;  // pages of tokens that come before every sequence's own (launch_mla_decode_prefix)
+    int32_t batch, n_q, heads, max_kv, prefix;
     float scale;
 };
 hipError_t launch_mla_decode(const MlaDecodeArgs &a, const coli_mla_dims &d, hipStream_t st);
+// The same where sequences begin with a.prefix > 0 tokens that they share, which each reads for itself.
+hipError_t launch_mla_decode_prefix(const MlaDecodeArgs &a, const coli_mla_dims &d, hipStream_t st);
 // Bytes of partial results a decode call needs behind the status page.
 size_t mla_decode_part_bytes(const coli_mla_dims &d, int batch, int n_q, int max_kv);
 
@@ -97,6 +100,8 @@ struct MlaSharedArgs {
     MlaParts p;
     float scale;
 };
+// Whether a call's sequences read the prefix each for itself: where that is faster (path 0), never (1), wherever lengths fit (2).
+bool mla_prefix_by_sequence(const coli_mla_dims &d, int batch, int n_q, int prefix, int max_kv, int path);
 // The sizes of a call and where its workspace's part is.
 MlaSharedArgs mla_shared_args(const coli_mla_dims &d, void *part, int batch, int n_q, int prefix, int max_kv);
 hipError_t launch_mla_shared(const MlaSharedArgs &a, const coli_mla_dims &d, hipStream_t st);

@@ -84,6 +84,9 @@ int check_shared(const coli_mla_dims *d, int32_t batch, int32_t n_q, int32_t pre
     return COLI_OK;
 }
 
+// coli_mla_debug_shared_path
+int g_shared_path = 0;
+
 // Where a shared decode's workspace holds what: the status page, the own
 // tokens' partial results, those of whole sequences, the prefix's.
 struct SharedLayout {
@@ -96,7 +99,8 @@ SharedLayout shared_layout(const coli_mla_dims *d, int batch, int n_q, int prefi
         return l;
     }
     const MlaParts p = mla_decode_parts(*d, batch, n_q, max_kv);
-    l.full = WS_HEAD + mla_decode_part_bytes(*d, batch, n_q, max_kv);
+    const int64_t longest = (int64_t)prefix_len + max_kv;   // of a call whose sequences read the prefix each for itself
+    l.full = WS_HEAD + mla_decode_part_bytes(*d, batch, n_q, (int)(longest < COLI_MLA_MAX_LENGTH ? longest : COLI_MLA_MAX_LENGTH));
     l.prefix = l.full + 4 * (size_t)p.slot * p.blocks * batch;
     l.total = l.prefix + mla_shared_part_bytes(*d, batch, n_q, prefix_len, max_kv);
     return l;
@@ -292,6 +296,11 @@ int coli_mla_decode_shared(const coli_mla_dims *d, int32_t batch, int32_t n_q, c
     a.max_kv = max_kv;
     a.scale = d->softmax_scale;
     if (prefix_len == 0) return launched(launch_mla_decode(a, *d, st), "decode");
+    if (mla_prefix_by_sequence(*d, batch, n_q, prefix_len, max_kv, g_shared_path)) {
+        a.prefix_table = prefix_table;
+        a.prefix = prefix_len;
+        return launched(launch_mla_decode_prefix(a, *d, st), "decode");
+    }
     MlaSharedArgs s = mla_shared_args(*d, base + at.prefix, batch, n_q, prefix_len, max_kv);
     s.c = cache(d, pages, kv_scale, n_pages, prefix_table, prefix_width);
     s.q_lat = q_lat;
@@ -310,6 +319,12 @@ int coli_mla_decode_shared(const coli_mla_dims *d, int32_t batch, int32_t n_q, c
     }
     if ((rc = launched(launch_mla_shared(s, *d, st), "shared decode"))) return rc;
     return launched(launch_mla_shared_join(s, *d, st), "join");
+}
+
+int coli_mla_debug_shared_path(int32_t path) {
+    if (path < 0 || path > 2) return fail(COLI_EINVAL, "path must be 0, 1 or 2");
+    g_shared_path = path;
+    return COLI_OK;
 }
 
 int coli_mla_expand(const coli_mla_dims *d, int32_t batch, int32_t n_rows, const void *pages,

@@ -116,7 +116,11 @@ __device__ __forceinline__ int dec_swz(int t) {
 //
 // PARTS: whole sequences too leave a partial result, in a slot of their own at
 // a.full, for a join with what else their queries see.
-template <class D, bool PARTS = false>
+//
+// PREFIX: every sequence is the a.prefix tokens of a.prefix_table, then those of
+// its own in its row of the table; each reads the prefix for itself, out of the
+// L2 after the first.
+template <class D, bool PARTS = false, bool PREFIX = false>
 __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int groups) {
     using T = typename D::T;
     constexpr int RANK = D::RANK, CT = D::CT, KS = D::KS;
@@ -130,7 +134,8 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
     const bool has_rows = wave_row < rows;
 
     // ---- this workgroup's tiles: `total` of them from tile `tile` of sequence `seq`
-    auto tiles_of = [&](int b) { return b < a.batch ? dec_tiles(mla_len(a.kv_lens, b, a.max_kv, a.status)) : 0; };
+    const int prefix = PREFIX ? a.prefix : 0;
+    auto tiles_of = [&](int b) { return b < a.batch ? dec_tiles(prefix + mla_len(a.kv_lens, b, a.max_kv, a.status)) : 0; };
     int tiles = 0, mine = 0, incl = 0;
     for (int b = 0; b < a.batch; b += 64) {
         mine = tiles_of(b + lane);
@@ -173,7 +178,7 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
     int lens_from = seq, lens = 0;   // lane i: the length of sequence lens_from + i
     auto load_lens = [&] {
         lens_from = seq;
-        lens = min(max(a.kv_lens[min(seq + lane, a.batch - 1)], 0), a.max_kv);
+        lens = prefix + min(max(a.kv_lens[min(seq + lane, a.batch - 1)], 0), a.max_kv);
     };
     load_lens();
     int next_seq = seq, next_tile = tile, next_len = __builtin_amdgcn_readlane(lens, 0);
@@ -183,9 +188,10 @@ __global__ __launch_bounds__(256, 1) void k_mla_decode(MlaDecodeArgs a, int grou
     };
     auto page_ids = [&](Page &p) {
         const int t = max(0, min(next_tile * DEC_TILE + lane, next_len - 1));   // behind the end: the last again
-        const int pi = div_by(t, a.c.page, page_inv);
-        p.in = t - pi * a.c.page;
-        p.id = a.c.table[(int64_t)next_seq * a.c.width + pi];
+        const bool own = !PREFIX || t >= prefix;
+        const int in = own ? t - prefix : t, pi = div_by(in, a.c.page, page_inv);
+        p.in = in - pi * a.c.page;
+        p.id = (own ? a.c.table + (int64_t)next_seq * a.c.width : a.prefix_table)[pi];
         if (next_len == 0) p.id = 0;
         const bool cross = (next_tile + 1) * DEC_TILE >= next_len;
         next_tile = cross ? 0 : next_tile + 1;
@@ -725,13 +731,13 @@ int dec_groups(int batch, int rows, int max_kv) {
     return (int)groups;
 }
 
-template <class D>
+template <class D, bool PREFIX = false>
 hipError_t launch(const MlaDecodeArgs &a, hipStream_t st) {
-    const int rows = a.n_q * a.heads, groups = dec_groups(a.batch, rows, a.max_kv);
+    const int rows = a.n_q * a.heads, groups = dec_groups(a.batch, rows, a.prefix + a.max_kv);
     const int blocks = (rows + D::ROWS - 1) / D::ROWS;
-    const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_mla_decode<D>), D::LDS);
+    const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_mla_decode<D, false, PREFIX>), D::LDS);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_mla_decode<D>, dim3(groups, blocks), dim3(256), D::LDS, st, a, groups);
+    hipLaunchKernelGGL((k_mla_decode<D, false, PREFIX>), dim3(groups, blocks), dim3(256), D::LDS, st, a, groups);
     if (groups > 1) {
         const int rgs = (rows + 31) / 32, pieces = D::RANK / 8;
         if ((int64_t)a.batch * rgs <= JOIN_DEEP)
@@ -753,10 +759,23 @@ hipError_t launch_parts(const MlaDecodeArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <class T, int RANK, bool FP8>
-hipError_t by_rows(const MlaDecodeArgs &a, hipStream_t st) {
-    return dec_rows(a.n_q * a.heads) == 32 ? launch<Dec<T, RANK, FP8, 1>>(a, st)
-                                           : launch<Dec<T, RANK, FP8, 2>>(a, st);
+// Calls f with the kernel's shape for a call's rows and dims.
+template <class F>
+hipError_t with_shape(const MlaDecodeArgs &a, const coli_mla_dims &d, F f) {
+    return mla_with_type(d.dtype, [&](auto t) {
+        using T = decltype(t);
+        const bool few = dec_rows(a.n_q * a.heads) == 32;
+        auto go = [&](auto rank, auto fp8) {
+            constexpr int R = decltype(rank)::value;
+            constexpr bool F8 = decltype(fp8)::value;
+            return few ? f(Dec<T, R, F8, 1>()) : f(Dec<T, R, F8, 2>());
+        };
+        using std::integral_constant;
+        const integral_constant<int, 512> wide;
+        const integral_constant<int, 256> narrow;
+        if (d.kv_format == COLI_KV_E4M3) return d.rank == 512 ? go(wide, std::true_type()) : go(narrow, std::true_type());
+        return d.rank == 512 ? go(wide, std::false_type()) : go(narrow, std::false_type());
+    });
 }
 
 }  // namespace
@@ -783,29 +802,15 @@ MlaParts mla_decode_parts(const coli_mla_dims &d, int batch, int n_q, int max_kv
 }
 
 hipError_t launch_mla_decode_parts(const MlaDecodeArgs &a, const coli_mla_dims &d, hipStream_t st) {
-    return mla_with_type(d.dtype, [&](auto t) {
-        using T = decltype(t);
-        const bool few = dec_rows(a.n_q * a.heads) == 32;
-        auto go = [&](auto rank, auto fp8) {
-            constexpr int R = decltype(rank)::value;
-            constexpr bool F = decltype(fp8)::value;
-            return few ? launch_parts<Dec<T, R, F, 1>>(a, st) : launch_parts<Dec<T, R, F, 2>>(a, st);
-        };
-        using std::integral_constant;
-        integral_constant<int, 512> wide;
-        integral_constant<int, 256> narrow;
-        if (d.kv_format == COLI_KV_E4M3) return d.rank == 512 ? go(wide, std::true_type()) : go(narrow, std::true_type());
-        return d.rank == 512 ? go(wide, std::false_type()) : go(narrow, std::false_type());
-    });
+    return with_shape(a, d, [&](auto shape) { return launch_parts<decltype(shape)>(a, st); });
+}
+
+hipError_t launch_mla_decode_prefix(const MlaDecodeArgs &a, const coli_mla_dims &d, hipStream_t st) {
+    return with_shape(a, d, [&](auto shape) { return launch<decltype(shape), true>(a, st); });
 }
 
 hipError_t launch_mla_decode(const MlaDecodeArgs &a, const coli_mla_dims &d, hipStream_t st) {
-    return mla_with_type(d.dtype, [&](auto t) {
-        using T = decltype(t);
-        const bool fp8 = d.kv_format == COLI_KV_E4M3;
-        if (d.rank == 512) return fp8 ? by_rows<T, 512, true>(a, st) : by_rows<T, 512, false>(a, st);
-        return fp8 ? by_rows<T, 256, true>(a, st) : by_rows<T, 256, false>(a, st);
-    });
+    return with_shape(a, d, [&](auto shape) { return launch<decltype(shape)>(a, st); });
 }
 
 }  // namespace coli

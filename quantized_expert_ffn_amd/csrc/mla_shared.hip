@@ -52,6 +52,11 @@ struct Shd {
 // blocks of 257 to 288 tiles: 206 us; each in four parts: 170).  Where that is
 // no worse, every block is cut into `parts` of its own, one a workgroup.
 constexpr int CROSS = 8;
+// A workgroup has LEAST units or more, if there are as many: a result of 128
+// rows takes 256 KiB to write and the join to read (64 x 1 x 16 rows behind
+// 2047 tokens: 57.9 us with one, 57.6 with two, 52.2 with three, 50.6 with six;
+// 128 rows behind 8192: 45.3, 37.1, 36.0, 38.0).
+constexpr int LEAST = 3;
 struct Units {
     int64_t total;
     int shares, parts;   // parts: 0, or of each block
@@ -61,12 +66,13 @@ struct Units {
 };
 __host__ __device__ inline int tiles_of(int tokens) { return (tokens + SHD_TILE - 1) / SHD_TILE; }
 __host__ __device__ inline int64_t blocks_of(int64_t rows) { return (rows + SHD_ROWS - 1) / SHD_ROWS; }
+__host__ __device__ inline int64_t shares_of(int64_t units) { return (units + LEAST - 1) / LEAST; }
 __host__ __device__ inline bool whole_blocks(int64_t rows_of_sequence) { return rows_of_sequence % SHD_ROWS == 0; }
 
 // Most workgroups, each of which takes a CU.
 int shd_shares(int64_t rows, int prefix, int max_kv) {
     const int64_t units = blocks_of(rows) * ((int64_t)tiles_of(prefix) + tiles_of(max_kv));
-    return (int)(units < 256 ? units : 256);
+    return (int)(shares_of(units) < 256 ? shares_of(units) : 256);
 }
 
 // Behind the plan, the groups' first units and the parts of a block, come the
@@ -151,7 +157,7 @@ __device__ __forceinline__ Place shd_units(const MlaSharedArgs &a, int groups, i
         for (int o = 32, v = t; o; o >>= 1) longest = max(longest, v = max(v, __shfl_xor(v, o)));
     }
     longest = uniform(longest);
-    p.u.shares = (int)min(p.u.total, (int64_t)a.shares);
+    p.u.shares = (int)min(shares_of(p.u.total), (int64_t)a.shares);
     const int parts = (int)(p.u.shares / ((int64_t)groups * blocks));
     if (parts > 0 && parts <= prefix && (longest + parts - 1) / parts <= p.u.total / p.u.shares + CROSS) p.u.parts = parts;
     int64_t base = 0;
@@ -644,7 +650,7 @@ __global__ __launch_bounds__(W > 1 ? 64 * W : 256) void k_mla_shared_join(MlaSha
         int64_t g0 = blk * parts, g1 = g0 + parts - 1;
         if (!parts) {
             const int64_t blocks = a.whole ? a.n_q * a.heads / SHD_ROWS : blocks_of(rows), total = a.plan[groups];
-            const Units u{total, (int)min(total, (int64_t)a.shares), 0};
+            const Units u{total, (int)min(shares_of(total), (int64_t)a.shares), 0};
             const int64_t tiles = (a.plan[group + 1] - a.plan[group]) / blocks, unit = a.plan[group] + (blk - group * blocks) * tiles;
             g0 = u.owner(unit);
             g1 = u.owner(unit + tiles - 1);
@@ -714,7 +720,36 @@ hipError_t with_shape(const coli_mla_dims &d, F f) {
 
 }  // namespace
 
-constexpr int JOIN_DEEP = 32, JOIN_COLS = 4;
+// A join of at most this many groups of 32 rows has sixteen wavefronts a piece
+// (4 groups: 45 us for the whole call against 130; 16: 50 against 62; 32: 61
+// against 58; 64: 72 against 58).
+constexpr int JOIN_DEEP = 16, JOIN_COLS = 4;
+
+// Which is faster, in us by what both measured (rank 512, 100 tokens of their
+// own, sizes in batch x n_q x heads x prefix): tiles of 64 tokens a workgroup
+// where sequences read the prefix apart, blocks of 32 rows if a sequence has no
+// more, else of 64; tiles of 32 tokens a workgroup, and a third launch where
+// blocks are not of one sequence, together.  Apart / together, plain:
+//   4 x 1 x 16 x 8192     22.5 / 39.8     64 x 1 x 16 x 32768   240 / 112
+//   64 x 1 x 16 x 8192    76.5 / 68.8     64 x 1 x 5 x 32768    241 / 71.2
+//   64 x 1 x 64 x 8192     101 / 113      64 x 1 x 64 x 32768   318 / 292
+//   16 x 1 x 128 x 8192   57.6 / 67.9     64 x 1 x 128 x 32768  570 / 517
+// E4M3, whose codes are widened for every 32 rows or 64 in registers there, here through LDS:
+//   64 x 1 x 16 x 8192    87.2 / 76.2     64 x 1 x 16 x 32768   296 / 137
+//   16 x 4 x 64 x 32768    352 / 362      64 x 1 x 128 x 32768  680 / 683
+bool mla_prefix_by_sequence(const coli_mla_dims &d, int batch, int n_q, int prefix, int max_kv, int path) {
+    const int64_t longest = (int64_t)prefix + max_kv;
+    if (longest > COLI_MLA_MAX_LENGTH || batch * longest > COLI_MLA_MAX_TOKENS) return false;
+    if (path) return path == 2;
+    const int rows = n_q * d.n_heads, own = max_kv / 2;
+    const bool fp8 = d.kv_format == COLI_KV_E4M3, few = rows <= 32, whole = whole_blocks(rows);
+    const double size = d.rank == 512 ? 1.0 : 0.6, own_blocks = whole ? (double)batch * rows / SHD_ROWS : 0.0;
+    const double apart = size / (64 * 256) * batch * ((rows + 63) / 64) * ((double)prefix + own);
+    const double together = size / (32 * 256) * ((double)blocks_of((int64_t)batch * rows) * prefix + own_blocks * own);
+    const double t_apart = few ? 13.0 + (fp8 ? 2.2 : 2.0) * apart : 20.0 + (fp8 ? 2.6 : 2.3) * apart;
+    const double t_together = (whole ? 35.0 : 48.0) * (d.rank == 512 ? 1.0 : 0.8) + (fp8 ? 5.0 + 2.5 * together : 1.9 * together);
+    return t_apart <= t_together;
+}
 
 size_t mla_shared_part_bytes(const coli_mla_dims &d, int batch, int n_q, int prefix, int max_kv) {
     // slots are counted by workgroup + block of rows: a bound that grows with each argument

@@ -163,24 +163,23 @@ __device__ __forceinline__ int select_slow(const SelectArgs &a, const float *log
 }
 
 template <class T, int LANES, int PER>
-__global__ __launch_bounds__(256) void k_select(SelectArgs a, int vector) {
+__global__ __launch_bounds__(64) void k_select(SelectArgs a, int vector) {
     constexpr int TOK = 64 / LANES, SUB = PER / 4;   // tokens a wavefront; experts a maximum stands for
     extern __shared__ double lds[];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tok = lane / LANES, sub = lane % LANES;
+    const int lane = threadIdx.x, tok = lane / LANES, sub = lane % LANES;
     const int words = row_words(a.experts), size = a.experts / a.groups;
-    // a wavefront's room: logits [TOK], approximate choices [TOK] (or one token's in binary64 and its groups'), candidates
+    // in LDS: logits [TOK], approximate choices [TOK] (or one token's in binary64 and its groups'), candidates
     const bool groups = a.topk_group < a.groups;
     const int span = group_span(size, PER);
     const size_t room = select_room(LANES, a.experts, groups && !span);
-    char *mem = reinterpret_cast<char *>(lds) + wave * room;
+    char *mem = reinterpret_cast<char *>(lds);
     float *logit = reinterpret_cast<float *>(mem) + tok * words;
     char *second_row = mem + (size_t)TOK * words * 4;
     float *near = reinterpret_cast<float *>(second_row) + tok * words;
     double *cand_key = reinterpret_cast<double *>(mem + room - 64 * 12) + tok * LANES;
     int *cand = reinterpret_cast<int *>(mem + room - 64 * 4) + tok * LANES;
 
-    const int64_t token = ((int64_t)blockIdx.x * (blockDim.x >> 6) + wave) * TOK + tok;
-    if (token - tok >= a.tokens) return;
+    const int64_t token = (int64_t)blockIdx.x * TOK + tok;
     const bool real = token < a.tokens;
     const T *row = static_cast<const T *>(a.logits) + (real ? token : a.tokens - 1) * a.stride;
     const int e0 = sub * PER;
@@ -481,15 +480,12 @@ template <class T, int LANES, int PER>
 hipError_t launch_shape(const SelectArgs &a, hipStream_t st) {
     constexpr int TOK = 64 / LANES;
     const size_t room = select_room(LANES, a.experts, a.topk_group < a.groups && !group_span(a.experts / a.groups, PER));
-    const int waves = a.tokens > 256 * TOK ? 4 : 1;
-    const int64_t groups = (a.tokens + TOK - 1) / TOK;
     constexpr int N = sizeof(T) == 4 ? 4 : PER < 8 ? 4 : 8;
     const bool vector = a.experts % N == 0 && a.stride % N == 0 && reinterpret_cast<uintptr_t>(a.logits) % (N * sizeof(T)) == 0 &&
                         reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
-    const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_select<T, LANES, PER>), room * waves);
+    const hipError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(&k_select<T, LANES, PER>), room);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_select<T, LANES, PER>), dim3((uint32_t)((groups + waves - 1) / waves)), dim3(64 * waves), room * waves, st, a,
-                       (int)vector);
+    hipLaunchKernelGGL((k_select<T, LANES, PER>), dim3((uint32_t)(((int64_t)a.tokens + TOK - 1) / TOK)), dim3(64), room, st, a, (int)vector);
     return hipGetLastError();
 }
 

@@ -30,7 +30,7 @@ COLI_MLA_MAX_SHARED_ROWS = 1 << 20
 
 MLA_EXPORTS = ("coli_mla_row_bytes", "coli_mla_workspace_bytes", "coli_mla_append", "coli_mla_project",
                "coli_mla_decode", "coli_mla_expand", "coli_mla_prefill", "coli_mla_shared_workspace_bytes",
-               "coli_mla_decode_shared")
+               "coli_mla_decode_shared", "coli_mla_debug_shared_path")
 
 _TYPES = {torch.bfloat16: COLI_BF16, torch.float16: COLI_FP16, COLI_BF16: COLI_BF16, COLI_FP16: COLI_FP16}
 _OF = {COLI_BF16: torch.bfloat16, COLI_FP16: torch.float16}
@@ -57,6 +57,7 @@ _sigs = {
     "coli_mla_shared_workspace_bytes": (_SZ, [_D, _I32, _I32, _I32, _I32]),
     "coli_mla_decode_shared": (ctypes.c_int, [_D, _I32, _I32, _P, _P, _P, _P, _I32, _P, _I32, _I32, _P, _I32, _P, _I32, _P,
                                               _P, _P, _SZ, _P]),
+    "coli_mla_debug_shared_path": (ctypes.c_int, [_I32]),
     "coli_mla_expand": (ctypes.c_int, [_D, _I32, _I32, _P, _P, _I32, _P, _I32, _P, _P, _P, _P, _P, _SZ, _P]),
     "coli_mla_prefill": (ctypes.c_int, [_D, _I32, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _P,
                                         _P, _I32, _I32, _P, _P, _P, _SZ, _P]),
@@ -325,6 +326,10 @@ def coli_mla_decode_shared(dims, q_lat, q_pe, pages, kv_scale, prefix_table, pre
         no.workspace(ws)
         no.end()
     _check(rc, "coli_mla_decode_shared")
+
+
+def coli_mla_debug_shared_path(path: int) -> None:
+    _check(_lib.coli_mla_debug_shared_path(int(path)), "coli_mla_debug_shared_path")
 
 
 def coli_mla_expand(dims, pages, kv_scale, table, cu_k, w, kv, k_pe, ws, stream=None):

@@ -26,6 +26,14 @@ def device():
     assert torch.cuda.is_available(), "no GPU visible"
 
 
+@pytest.fixture(params=["together", "apart"], autouse=True)
+def path(request, device):
+    """Both ways to read the prefix: at these sizes the choice between them is always the second."""
+    q().coli_mla_debug_shared_path({"together": 1, "apart": 2}[request.param])
+    yield request.param
+    q().coli_mla_debug_shared_path(0)
+
+
 def norm(x):
     return x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6)
 

@@ -16,6 +16,14 @@ def device():
     assert torch.cuda.is_available(), "no GPU visible"
 
 
+@pytest.fixture(params=["together", "apart"], autouse=True)
+def path(request, device):
+    """Every test with the prefix read once for blocks of rows of all sequences, and by each sequence for itself."""
+    q().coli_mla_debug_shared_path({"together": 1, "apart": 2}[request.param])
+    yield request.param
+    q().coli_mla_debug_shared_path(0)
+
+
 def workspace(d, *sizes):
     ws = torch.zeros(q().coli_mla_shared_workspace_bytes(d, *sizes), dtype=torch.uint8, device="cuda")
     ws[256:] = 0xff   # stale partial results

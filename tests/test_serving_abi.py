@@ -93,6 +93,12 @@ def test_shared_bad_arguments_are_refused():
     assert shared(_dims(kv_format=q.COLI_KV_E4M3)) == q.COLI_EINVAL   # no kv_scale
 
 
+def test_shared_path_is_one_of_three():
+    for path in (-1, 3):
+        assert q._lib.coli_mla_debug_shared_path(path) == q.COLI_EINVAL
+    assert q._lib.coli_mla_debug_shared_path(0) == q.COLI_OK
+
+
 def test_shared_workspace_grows_with_each_size():
     """A workspace serves every smaller call."""
     for heads in (1, 5, 32, 64, 128):
