@@ -29,6 +29,14 @@ __device__ __forceinline__ int swz(int r) { return 4 * ((r >> 1) & 1) + 2 * ((r 
 // workgroups share them out.  Steps of NW / 4 lines of 128 along k go through a
 // ring of LDS stages, and each of the NW wavefronts multiplies 32 of every
 // step; their sums meet in LDS at the end, BATCH tiles of 32 x 32 at a time.
+//
+// What bounds it is the memory's time to answer: weights and tokens on their
+// way, about 64 KiB a CU of either, arrive after 1.2 us, 50 GB/s a CU, of which
+// the tokens' part comes from the L2 over and over.  One token, 6144 -> 16384,
+// 101 MB: 18.9 us, 5.3 TB/s, as a copy; 61 tokens, 16384 -> 6144: 29.8 (192
+// workgroups of 1.5 MB); 133 tokens, 6144 -> 19393: 43.5.  A ring for weights
+// and one for tokens, each loaded by its half of the wavefronts, so that more
+// weights are out: 20.2 -> 22.6, 30.8 -> 50.2 and 43.6 -> 49.2.
 template <class T_, int FM_, int FN_, int NW_, int STAGES_, int WGS_>
 struct Split {
     using T = T_;
@@ -55,7 +63,8 @@ __global__ __launch_bounds__(64 * D::NW, D::WGS * D::NW / 4) void k_w8_split(W8L
         src[i] = (r < D::TM ? a.w + (int64_t)min(o0 + r, a.n_out - 1) * a.k : a.x + (int64_t)min(r - D::TM, a.tokens - 1) * a.x_stride) + chunk[i];
     }
     // Rows are often a power of two apart, or nearly so, and the lines of a step then lie in few channels of the L2: each
-    // workgroup of an XCD begins elsewhere along k, and goes round.
+    // workgroup of an XCD begins elsewhere along k, and goes round (16384 -> 6144, one token: 25.0 us without, 20.6; 61
+    // tokens: 33.7, 30.5; rows of 6144 alike with and without).
     const int turn = (int)((int64_t)(blockIdx.x >> 3) * steps / ((gridDim.x + 7) >> 3));
     int load = turn, load_slot = 0;
     auto issue = [&] {   // behind the last step nothing is read that counts
@@ -154,6 +163,12 @@ __global__ __launch_bounds__(64 * D::NW, D::WGS * D::NW / 4) void k_w8_split(W8L
 // WGS workgroups fit a CU.  Steps of 128 along k, a line of every row, form one
 // stream over a workgroup's tiles, through a ring of LDS stages loaded straight
 // from memory; results pass through the stage used last, to leave in whole lines.
+//
+// What bounds it: 8192 tokens, 6144 -> 16384, 729 us, 2.26 POP/s: matrix
+// products alone, without loads, ran 512 us at the clock that their power left
+// (1.5 to 1.8 GHz); 256 x 256 tiles read 6.4 GB through L2s that hold 79 % of
+// it.  Steps of 64 in four stages, beginning elsewhere along k, and eight
+// wavefronts as 4 x 2 gained nothing.
 template <class T_, int TM_, int TN_, int NW_, int WM_, int STAGES_, int WGS_>
 struct Tile {
     using T = T_;
@@ -390,6 +405,8 @@ hipError_t launch_w8_linear(const W8LinearArgs &a, int dtype, hipStream_t st) {
         if (a.tokens <= 64) return split_by_channels<T, 2, 6, 2, 9, 7>(a, st);
         if (a.tokens <= 96) return split_by_channels<T, 3, 4, 2, 7, 6>(a, st);
         if (a.tokens <= 128) return split_by_channels<T, 4, 7, 1, 6, 5>(a, st);
+        // up to 160, split or in tiles: 160 tokens, 6144 -> 6144, 26.5 us or 27.3; 16384 -> 6144, 54.0 or 60.9; 6144 -> 24576,
+        // 46.4 or 51.3; 64 tokens, 6144 -> 6144, 15.6 or 29.2
         if (a.tokens <= 160) return split_by_channels<T, 5, 6, 1, 5, 4>(a, st);
         // More tokens: rounds of workgroups by what one takes, in 42 us at k = 6144: 128 x 64 tiles, two a CU, 1 (0.65 if one
         // a CU is enough); 256 x 128: 1.15; 256 x 256: 2.1.  512 tokens, 6144 -> 6144: 41.8, 47.4 and 87.5 us; 1024 tokens:
