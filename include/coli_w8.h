@@ -13,8 +13,9 @@
  * Arithmetic: the scale is one division, rounded to binary32; a code is the
  * integer nearest to the exact quotient by that scale, ties to even, in
  * -127 .. 127.  Sums of products are exact (32-bit integers).  A result is
- * (sum * s_t) * s_o, then + bias, each step rounded to binary32, then once to
- * the output's type.  A token with a value that is not finite gets the scale
+ * (sum * s_t) * s_o, then + bias: in binary64, rounded once, for binary32
+ * outputs; for the 16-bit types each step rounded to binary32, then once to the
+ * output's type.  A token with a value that is not finite gets the scale
  * NaN and codes 0, so that its results are NaN and no other token's.
  */
 #ifndef COLI_W8_H

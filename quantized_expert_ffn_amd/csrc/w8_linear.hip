@@ -14,10 +14,18 @@ namespace {
 // Where chunks behind the end of a row read.
 __device__ const uint4 w8_zeros[8] = {};
 
-// A result: three roundings to binary32 of the product, one with a bias.
+// A result.  One for binary32 is formed in 64 bits and rounded once; for the
+// 16-bit types each step is rounded to binary32 first, 2^-24 beside their 2^-11
+// and more, since the tiles' many results would wait for slower instructions.
+template <class T>
 __device__ __forceinline__ float finish(int32_t sum, float st, float so, float bias, bool has_bias) {
-    const float v = (float)sum * st * so;
-    return has_bias ? v + bias : v;
+    if constexpr (sizeof(T) == 4) {
+        const double v = (double)sum * st * so;
+        return (float)(has_bias ? v + bias : v);
+    } else {
+        const float v = (float)sum * st * so;
+        return has_bias ? v + bias : v;
+    }
 }
 
 // Lane's place in a 1 KiB load: eight rows of eight chunks, swizzled so that
@@ -37,6 +45,8 @@ __device__ __forceinline__ int swz(int r) { return 4 * ((r >> 1) & 1) + 2 * ((r 
 // workgroups of 1.5 MB); 133 tokens, 6144 -> 19393: 43.5.  A ring for weights
 // and one for tokens, each loaded by its half of the wavefronts, so that more
 // weights are out: 20.2 -> 22.6, 30.8 -> 50.2 and 43.6 -> 49.2.
+// Nothing loaded for places without a token: 20.3 -> 22.7, 30.8 -> 34.1, 43.5 ->
+// 45.0; rings twice as deep, one workgroup a CU: 30.8 -> 39.3.
 template <class T_, int FM_, int FN_, int NW_, int STAGES_, int WGS_>
 struct Split {
     using T = T_;
@@ -135,7 +145,7 @@ __global__ __launch_bounds__(64 * D::NW, D::WGS * D::NW / 4) void k_w8_split(W8L
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int o = min(o0 + 32 * i + 8 * q + 4 * hf + k, a.n_out - 1);
-                v[k] = finish(sum[k], st, a.w_scale[o], a.bias ? a.bias[o] : 0.0f, a.bias != nullptr);
+                v[k] = finish<T>(sum[k], st, a.w_scale[o], a.bias ? a.bias[o] : 0.0f, a.bias != nullptr);
             }
             lds_write(D::BATCH * D::SUMS + x * D::OUT + n * D::OROW + 32 * q + 16 * hf, v);
         }
@@ -335,7 +345,7 @@ __global__ __launch_bounds__(64 * D::NW, D::NW * D::WGS / 4) void k_w8_tiles(W8L
                     const f32x4 so = lds_read<f32x4>(ch, 32 * q), b = lds_read<f32x4>(ch, 4 * D::TM + 32 * q);
                     four v;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] = (T)finish(acc[i + q / 4][j][4 * (q % 4) + k], st[j], so[k], b[k], a.bias != nullptr);
+                    for (int k = 0; k < 4; ++k) v[k] = (T)finish<T>(acc[i + q / 4][j][4 * (q % 4) + k], st[j], so[k], b[k], a.bias != nullptr);
                     lds_write(at + n * D::OROW + 4 * sizeof(T) * hf, v, 8 * sizeof(T) * q);
                 }
                 const int o = mt * D::TM + (wm * D::FM + i) * 32 + VEC * (lane % PER);
