@@ -750,9 +750,9 @@ constexpr int JOIN_DEEP = 16, JOIN_COLS = 4;
 //   64 x 1 x 16 x 8192    76.5 / 68.8     64 x 1 x 5 x 32768    241 / 71.2
 //   64 x 1 x 64 x 8192     101 / 113      64 x 1 x 64 x 32768   318 / 292
 //   16 x 1 x 128 x 8192   57.6 / 67.9     64 x 1 x 128 x 32768  570 / 517
-// E4M3, whose codes are widened for every 32 rows or 64 in registers there, here through LDS:
+// E4M3, whose codes are widened in registers there, here through LDS:
 //   64 x 1 x 16 x 8192    87.2 / 76.2     64 x 1 x 16 x 32768   296 / 137
-//   16 x 4 x 64 x 32768    352 / 362      64 x 1 x 128 x 32768  680 / 683
+//   16 x 4 x 64 x 32768    347 / 362      64 x 1 x 128 x 32768  676 / 685
 bool mla_prefix_by_sequence(const coli_mla_dims &d, int batch, int n_q, int prefix, int max_kv, int path) {
     const int64_t longest = (int64_t)prefix + max_kv;
     if (longest > COLI_MLA_MAX_LENGTH || batch * longest > COLI_MLA_MAX_TOKENS) return false;
@@ -763,7 +763,7 @@ bool mla_prefix_by_sequence(const coli_mla_dims &d, int batch, int n_q, int pref
     const double apart = size / (64 * 256) * batch * ((rows + 63) / 64) * ((double)prefix + own);
     const double together = size / (32 * 256) * ((double)blocks_of((int64_t)batch * rows) * prefix + own_blocks * own);
     const double t_apart = few ? 13.0 + (fp8 ? 2.2 : 2.0) * apart : 20.0 + (fp8 ? 2.6 : 2.3) * apart;
-    const double t_together = (whole ? 35.0 : 48.0) * (d.rank == 512 ? 1.0 : 0.8) + (fp8 ? 5.0 + 2.5 * together : 1.9 * together);
+    const double t_together = (whole ? 35.0 : 48.0) * (d.rank == 512 ? 1.0 : 0.8) + (fp8 ? 5.0 + 2.6 * together : 1.9 * together);
     return t_apart <= t_together;
 }
 
