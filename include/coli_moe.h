@@ -183,7 +183,10 @@ typedef struct coli_select_dims {
  *   ws        at least 256 bytes, zero-filled once: a workspace of this
  *             library's, of which the call uses the status word
  * Experts are chosen as in 64 bits: two choices that binary32 cannot tell
- * apart are ranked by what they are.  Weights are rounded once.  Non-finite
+ * apart are ranked by what they are in binary64, and those that it does not tell
+ * apart either (sigmoids of logits beyond 37, say) are equal.  A softmax
+ * renormalised without a bias may be ranked by its exponentials, whose sum
+ * cancels.  Weights are rounded once.  Non-finite
  * logits, bias or weights set COLI_ENONFINITE in the status word; indices are
  * distinct and in range all the same.
  */

@@ -3,10 +3,10 @@
 // Experts are to be chosen as in 64 bits, yet a sigmoid in binary64 for each of
 // them would cost more than all else.  Choices are formed in binary32 first,
 // with a bound on their error; experts that could be among the best K by it,
-// hardly more than K, are ranked by choices in binary64.  Without a bias the
-// order is the logits', which binary32 holds.  Where the bound leaves groups
-// undecided, or too many experts (equal ones), the token is done over in
-// binary64 by a whole wavefront.
+// hardly more than K, are ranked by choices in binary64.  Without a bias scores
+// rise with the logits, which binary32 holds, and the bound is on what binary64
+// rounds away (least_equal).  Where the bound leaves groups undecided, or too many
+// experts (equal ones), the token is done over in binary64 by a whole wavefront.
 //
 // What bounds it: a launch where tokens are few (one token, 256 experts in 8
 // groups: 5.8 us, of which 3.8 are a launch's), then instructions (16384 tokens
@@ -113,6 +113,20 @@ __device__ __forceinline__ double score64(const SelectArgs &a, float l, float to
     return a.softmax ? exp((double)l - top) * inv_sum : 1.0 / (1.0 + exp(-(double)l));
 }
 
+// A logit below which no score in binary64 comes up to that of l; next to l itself
+// except far out.  Computed scores of two logits differ as the exact ones do if
+// those are 2^-50 apart: of one where l >= 0 (exponential, sum and quotient are
+// off by 2^-51 in all), of themselves below.  A sigmoid rises by 1 / (2 (1 + e^l))
+// or more up to l, and below 0 by half of itself; an exponential by itself, and
+// its argument, d below the largest, is off by 2^-53 d.  Scores near the
+// least number binary64 holds keep too few bits: nothing is below.  2^-48 leaves
+// room for the roundings here.
+__device__ __forceinline__ float least_equal(const SelectArgs &a, float l, float top) {
+    const float d = top - l;
+    if (a.softmax ? d > 690.0f : l < -700.0f) return -__builtin_inff();
+    return l - 0x1p-48f * (1.0f + (a.softmax ? d : __builtin_amdgcn_exp2f(l * LOG2E)));
+}
+
 __device__ __forceinline__ float bias_of(const SelectArgs &a, int e) {
     const float b = a.bias ? a.bias[e] : 0.0f;
     return finite_f32(b) ? b : 0.0f;
@@ -120,7 +134,7 @@ __device__ __forceinline__ float bias_of(const SelectArgs &a, int e) {
 
 // One token by a whole wavefront, all in binary64: `logit` its logits, `choice`
 // room for as many choices and, behind them, 64 group scores.  Lane k gets the k-th
-// expert.  What a choice is without a bias is left to the logits.
+// expert.
 __device__ __forceinline__ int select_slow(const SelectArgs &a, const float *logit, double *choice, float top, double inv_sum) {
     const int lane = threadIdx.x & 63, size = a.experts / a.groups;
     double *best = choice + a.experts;
@@ -133,7 +147,7 @@ __device__ __forceinline__ int select_slow(const SelectArgs &a, const float *log
         if (lane < a.groups) {
             double first = -__builtin_inf(), second = -__builtin_inf();
             for (int e = lane * size; e < (lane + 1) * size; ++e) {
-                const double c = a.top2 || a.bias ? choice[e] : (double)logit[place(e)];
+                const double c = choice[e];
                 second = fmax(second, fmin(first, c));
                 first = fmax(first, c);
             }
@@ -151,7 +165,7 @@ __device__ __forceinline__ int select_slow(const SelectArgs &a, const float *log
         int at = a.experts;
         for (int i = 0, e = lane; e < a.experts; ++i, e += 64)
             if ((open >> (e / size) & 1) && !(mine >> i & 1)) {
-                const double v = a.bias ? choice[e] : (double)logit[place(e)];
+                const double v = choice[e];
                 if (v > c) {
                     c = v;
                     at = e;
@@ -351,27 +365,36 @@ __global__ __launch_bounds__(64) void k_select(SelectArgs a, int vector) {
             const float least = all_lanes<LANES>(in ? mine : -NEG, Min()), next = all_lanes<LANES>(there && !in ? mine : NEG, Max());
             // sums of two are off by 2 eps and their own rounding
             slow = !(least - next > 4.0f * eps + 0x1p-22f * (fabsf(least) + fabsf(next)));
-            if (span && __ballot(slow)) {   // scores in binary64, of the experts that could be a group's best
-                const float from = two ? second : first, least_seen = from - 2.0f * eps - 0x1p-22f * fabsf(from);
-                uint32_t open = 0;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) open |= seen[i] >= least_seen && seen[i] > NEG ? 1u << i : 0;
-                double f = -__builtin_inf(), t = f;
-                while (open) {
-                    const int e = e0 + __builtin_ctz(open);
-                    open &= open - 1;
-                    const double v = score64(a, logit[place(e)], top, inv_sum) + bias_of(a, e);
-                    t = fmax(t, fmin(f, v));
-                    f = fmax(f, v);
-                }
-                for (int o = 1; o < span; o += o) {
-                    const double of = __shfl_xor(f, o), ot = __shfl_xor(t, o);
-                    t = fmax(fmax(t, ot), fmin(f, of));
-                    f = fmax(f, of);
-                }
-                stand(two ? f + t : f);
-                slow = false;
+        } else {   // logits: equal ones are, others where binary64 tells the scores apart
+            const float least = all_lanes<LANES>(in ? mine : -NEG, Min()), d = top - least;
+            // elsewhere binary32's steps, 2^-24 of a logit, are the wider ones
+            if (__ballot(fabsf(least) < 0x1p-20f * (a.softmax ? 1.0f + d : 1.0f) || (a.softmax ? d > 690.0f : top > 14.0f))) {
+                const float below = all_lanes<LANES>(there && mine < least ? mine : NEG, Max());
+                const float above = all_lanes<LANES>(there && mine > least ? mine : -NEG, Min());
+                slow = below >= least_equal(a, least, top) || least_equal(a, above, top) <= least;
             }
+        }
+        if (span && __ballot(slow)) {   // scores in binary64, of the experts that could be a group's best
+            const float from = two ? second : first;
+            const float least_seen = approximate ? from - 2.0f * eps - 0x1p-22f * fabsf(from) : least_equal(a, from, top);
+            uint32_t open = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) open |= seen[i] >= least_seen && seen[i] > NEG ? 1u << i : 0;
+            double f = -__builtin_inf(), t = f;
+            while (open) {
+                const int e = e0 + __builtin_ctz(open);
+                open &= open - 1;
+                const double v = score64(a, logit[place(e)], top, inv_sum) + bias_of(a, e);
+                t = fmax(t, fmin(f, v));
+                f = fmax(f, v);
+            }
+            for (int o = 1; o < span; o += o) {
+                const double of = __shfl_xor(f, o), ot = __shfl_xor(t, o);
+                t = fmax(fmax(t, ot), fmin(f, of));
+                f = fmax(f, of);
+            }
+            stand(two ? f + t : f);
+            slow = false;
         }
         if (span) {
 #pragma unroll
@@ -409,7 +432,7 @@ __global__ __launch_bounds__(64) void k_select(SelectArgs a, int vector) {
         }
     }
     // ---- candidates, in the order of their experts
-    bound = a.bias ? bound - 2.0f * eps - 0x1p-22f * fabsf(bound) : bound;
+    bound = a.bias ? bound - 2.0f * eps - 0x1p-22f * fabsf(bound) : least_equal(a, bound, top);
     bound = fmaxf(bound, -0x1.fffffep+127f);   // closed ones are below every number
     uint32_t mask = 0;
 #pragma unroll
@@ -431,13 +454,13 @@ __global__ __launch_bounds__(64) void k_select(SelectArgs a, int vector) {
         cand[at] = e0 + i;
     }
     wave_sync();
-    // ---- their scores, and their order by choices in binary64 (without a bias, by logits)
+    // ---- their scores, and their order by choices in binary64
     int mine = sub < min(total, LANES) ? cand[sub] : -1;
     double score = 0.0, choice = -__builtin_inf();
     if (mine >= 0) {
         const float l = logit[place(mine)];
         score = score64(a, l, top, inv_sum);
-        choice = a.bias ? score + bias_of(a, mine) : (double)l;
+        choice = a.bias ? score + bias_of(a, mine) : score;
         cand_key[sub] = choice;
     }
     wave_sync();
