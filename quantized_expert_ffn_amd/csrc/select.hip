@@ -519,10 +519,14 @@ hipError_t launch_shape(const SelectArgs &a, hipStream_t st) {
 hipError_t launch_select(const SelectArgs &a, int dtype, hipStream_t st) {
     auto go = [&](auto t) {
         using T = decltype(t);
-        // Sixteen lanes against a wavefront a token, us: 256 experts in 8 groups, 1024 tokens 6.8 against 6.5, 2048 7.3, 7.2,
-        // 4096 7.9, 9.3, 16384 13.0, 25.0; 64 experts 4.3, 4.4; 4.4, 4.8; 4.5, 6.2; 6.2, 15.6.  Candidates need a lane each,
-        // hence few of K; groups too.
-        if (a.tokens >= 2048 && a.experts <= 256 && a.top_k <= 10 && a.groups <= 16)
+        // Sixteen lanes against a wavefront a token, us: 256 experts in 8 groups of which 4 are kept, K = 8, 1024 tokens 6.8 and
+        // 6.5, 2048 7.3, 7.3, 4096 7.4, 9.5, 16384 11.6, 25.4; 64 experts 4.3, 4.4; 4.4, 4.8; 4.5, 6.2; 6.2, 15.6.  Candidates
+        // need a lane each, hence few of K, and groups too.  The bound is a maximum of four experts each: with few in the kept
+        // groups it lets more than sixteen candidates in, and tokens are done over (K = 8, 32 experts kept: 2048 tokens 42.4,
+        // 7.6, 16384 59.5, 25.5; 64 kept: 7.5, 7.3; 20.7, 25.3; K = 6, 20 kept: 33.9, 8.0; 55.4, 30.0).
+        const int open = a.experts / a.groups * a.topk_group;
+        const bool fit = a.experts <= 64 || open <= 16 || open >= 8 * a.top_k;
+        if (a.tokens >= 2048 && a.experts <= 256 && a.top_k <= 10 && a.groups <= 16 && fit)
             return a.experts <= 64 ? launch_shape<T, 16, 4>(a, st) : launch_shape<T, 16, 16>(a, st);
         return a.experts <= 256 ? launch_shape<T, 64, 4>(a, st) : launch_shape<T, 64, 16>(a, st);
     };
