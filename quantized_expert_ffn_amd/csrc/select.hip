@@ -368,7 +368,7 @@ __global__ __launch_bounds__(64) void k_select(SelectArgs a, int vector) {
         } else {   // logits: equal ones are, others where binary64 tells the scores apart
             const float least = all_lanes<LANES>(in ? mine : -NEG, Min()), d = top - least;
             // elsewhere binary32's steps, 2^-24 of a logit, are the wider ones
-            if (__ballot(fabsf(least) < 0x1p-20f * (a.softmax ? 1.0f + d : 1.0f) || (a.softmax ? d > 690.0f : top > 14.0f))) {
+            if (__ballot(fabsf(least) < 0x1p-20f * (a.softmax ? 1.0f + d : 1.0f) || (a.softmax ? d > 690.0f : top > 14.0f || least < -700.0f))) {
                 const float below = all_lanes<LANES>(there && mine < least ? mine : NEG, Max());
                 const float above = all_lanes<LANES>(there && mine > least ? mine : -NEG, Min());
                 slow = below >= least_equal(a, least, top) || least_equal(a, above, top) <= least;

@@ -59,3 +59,23 @@ def test_select_scores_that_meet(softmax, top2, n, E, K, groups, keep):
             wrong = (got != idx[rows_at]).any(1)
             assert not wrong.any(), (bias is None, sorted(set(rows_at[wrong])), got[wrong][:2], idx[rows_at][wrong][:2])
             assert (np.abs(gw - w[rows_at]) <= 2.0 ** -24 * 1.001 * np.abs(w[rows_at]) + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("top2", [False, True])
+@pytest.mark.parametrize("n", [5, 2050])
+@pytest.mark.parametrize("E,K,groups,keep", [(256, 8, 8, 4), (160, 6, 8, 3), (60, 4, 5, 2), (64, 6, 32, 5)])
+def test_select_scores_of_zero_meet(top2, n, E, K, groups, keep):
+    """Sigmoids below every number of binary64, of logits that rise with the expert: the first groups and experts, with a
+    weight of zero.  Beside them tokens of which a few experts are not so low."""
+    say("select zero", top2, n, E, K, groups, keep)
+    e = torch.arange(E, device="cuda", dtype=torch.float32)
+    few = torch.stack([e * 2 - 2400, e / 4 - 790, torch.where(e % 29 == 28, -e / 8, e - 1800), torch.where(e == E - 1, 3.0, e - 1800)])
+    d = dims(E, K, groups, keep, False, top2, False)
+    idx, w = reference(d, few, None)
+    at = torch.arange(n, device="cuda") % 4
+    rows_at = at.cpu().numpy()
+    for bias in (torch.zeros(E, device="cuda"), None):
+        got, gw = run(d, few[at], bias)
+        wrong = (got != idx[rows_at]).any(1)
+        assert not wrong.any(), (bias is None, sorted(set(rows_at[wrong])), got[wrong][:2], idx[rows_at][wrong][:2])
+        assert (np.abs(gw - w[rows_at]) <= 2.0 ** -24 * 1.001 * np.abs(w[rows_at]) + 2.0 ** -149).all()
