@@ -733,9 +733,11 @@ int dec_groups(int batch, int rows, int max_kv) {
 }
 
 // Where sequences share a prefix a workgroup has DEC_LEAST tiles or more, if
-// there are as many: every part costs the join its reading (8 x 1 x 16 rows
-// behind 2047 tokens: 23.7 us with one, 21.7 with two, 22.1 with three; 128 rows
-// behind 8192: 27.7, 22.4, 23.1; 64 rows behind 200: 13.2, 13.2, 15.1).
+// there are as many: every part costs the join its reading (whole calls, 100
+// tokens of their own, inputs in turn so that no cache holds them: 8 x 1 x 16 rows
+// behind 2047 tokens, 21.1 us with one, 19.5 with two, 19.5 with three; 128 rows
+// behind 8192, 28.9, 23.7, 24.8; 64 rows behind 200, 12.6, 14.4, 15.4; the same
+// inputs over and over: 21.4, 19.9, 20.4; 28.4, 23.1, 23.2; 12.9, 14.7, 16.7).
 constexpr int DEC_LEAST = 2;
 template <class D, bool PREFIX = false>
 hipError_t launch(const MlaDecodeArgs &a, hipStream_t st) {

@@ -17,10 +17,17 @@
 //
 // What bounds it: matrix products at what the card's power allows, then their
 // operands from LDS.  64 x 128 rows over 8192 tokens and up to 1024 of their
-// own, rank 512, binary16: 179 us, 0.85 PFLOP/s, of which the join 14; its
-// products alone, with nothing else in the kernel, ran 107 us (1.37 PFLOP/s).
-// Leaving out any one of softmax, value reads, key reads or loads saved 8 to 12
-// us of it.  E4M3, 64 x 64 rows over 32768: 363 us, of which widening 45.
+// own, rank 512, binary16: 179 to 183 us, 0.83 to 0.85 PFLOP/s, of which the join
+// 14; its products alone, with nothing else in the kernel, ran 107 us (1.37
+// PFLOP/s).  Leaving out any one of softmax, value reads, key reads or loads saved
+// 8 to 12 us of it.  E4M3, 64 x 64 rows over 32768: 364 us, of which widening 45
+// (by default a call of that size has its sequences read apart, 350 us).
+//
+// Weights are rounded to 16 bits before the values' product, since the matrix
+// cores take both sides in the cache's type; their sum is of the weights before
+// that rounding.  Beside a plain form that keeps 32 bits the error against 64 bits
+// is an eighth larger: bf16 1.9e-3 against 1.7e-3 of the largest value, fp16
+// 2.4e-4 against 2.1e-4.
 #include "kernels.h"
 #include "mla_mfma.h"
 
@@ -752,7 +759,13 @@ constexpr int JOIN_DEEP = 16, JOIN_COLS = 4;
 //   16 x 1 x 128 x 8192   57.6 / 67.9     64 x 1 x 128 x 32768  570 / 517
 // E4M3, whose codes are widened in registers there, here through LDS:
 //   64 x 1 x 16 x 8192    87.2 / 76.2     64 x 1 x 16 x 32768   296 / 137
-//   16 x 4 x 64 x 32768    347 / 362      64 x 1 x 128 x 32768  676 / 685
+//   16 x 4 x 64 x 32768    350 / 364      64 x 1 x 128 x 32768  680 / 687
+// Prefixes that no cache holds whole, 100 tokens of their own, E4M3 on the left
+// (both ways come to the same, up to 2 x 128 rows a sequence too), plain on the right:
+//   16 x 1 x 128 x 131072  673 / 685      16 x 1 x 128 x 131072   586 / 528
+//   16 x 1 x 128 x 524288 2625 / 2617     16 x 1 x 128 x 524288  2346 / 2008
+//   64 x 1 x 128 x 131072 2611 / 2613     64 x 1 x 128 x 131072  2251 / 2009
+//   64 x 1 x 16 x 524288  4489 / 1420     64 x 1 x 16 x 524288   3958 / 1120
 bool mla_prefix_by_sequence(const coli_mla_dims &d, int batch, int n_q, int prefix, int max_kv, int path) {
     const int64_t longest = (int64_t)prefix + max_kv;
     if (longest > COLI_MLA_MAX_LENGTH || batch * longest > COLI_MLA_MAX_TOKENS) return false;

@@ -9,11 +9,11 @@
 // experts (equal ones), the token is done over in binary64 by a whole wavefront.
 //
 // What bounds it: a launch where tokens are few (one token, 256 experts in 8
-// groups: 5.8 us, of which 3.8 are a launch's), then instructions (16384 tokens
-// of 256 experts, sigmoid with a bias, 4 of 8 groups: 12.4 us, 1.44 TB/s of
-// logits).  A token has LANES lanes, each PER experts in a row: sixteen lanes
-// where tokens are many, so that what goes across lanes is shared by four of
-// them, a whole wavefront where they are few or the experts too many.
+// groups: 5.9 us, of which 3.8 are a launch's), then instructions (16384 tokens
+// of 256 experts, sigmoid with a bias, 4 of 8 groups: 12.0 to 12.7 us, 1.4 TB/s
+// of logits, 16.8 MB).  A token has LANES lanes, each PER experts in a row:
+// sixteen lanes where tokens are many, so that what goes across lanes is shared by
+// four of them, a whole wavefront where they are few or the experts too many.
 #include <type_traits>
 
 #include "device_common.h"

@@ -41,12 +41,13 @@ __device__ __forceinline__ int swz(int r) { return 4 * ((r >> 1) & 1) + 2 * ((r 
 // What bounds it is the memory's time to answer: weights and tokens on their
 // way, about 64 KiB a CU of either, arrive after 1.2 us, 50 GB/s a CU, of which
 // the tokens' part comes from the L2 over and over.  One token, 6144 -> 16384,
-// 101 MB: 18.9 us, 5.3 TB/s, as a copy; 61 tokens, 16384 -> 6144: 29.8 (192
-// workgroups of 1.5 MB); 133 tokens, 6144 -> 19393: 43.5.  A ring for weights
-// and one for tokens, each loaded by its half of the wavefronts, so that more
-// weights are out: 20.2 -> 22.6, 30.8 -> 50.2 and 43.6 -> 49.2.
-// Nothing loaded for places without a token: 20.3 -> 22.7, 30.8 -> 34.1, 43.5 ->
-// 45.0; rings twice as deep, one workgroup a CU: 30.8 -> 39.3.
+// 101 MB: 18.9 us, 5.3 TB/s, as a copy; 61 tokens, 16384 -> 6144: 29.3 (192
+// workgroups of 1.5 MB); 133 tokens, 6144 -> 19393, binary32: 46.7.  What was
+// tried, beside builds whose binary32 results were still formed in binary32: a
+// ring for weights and one for tokens, each loaded by its half of the wavefronts,
+// so that more weights are out, 20.2 -> 22.6, 30.8 -> 50.2 and 43.6 -> 49.2;
+// nothing loaded for places without a token, 20.3 -> 22.7, 30.8 -> 34.1, 43.5 ->
+// 45.0; rings twice as deep, one workgroup a CU, 30.8 -> 39.3.
 template <class T_, int FM_, int FN_, int NW_, int STAGES_, int WGS_>
 struct Split {
     using T = T_;
@@ -174,7 +175,7 @@ __global__ __launch_bounds__(64 * D::NW, D::WGS * D::NW / 4) void k_w8_split(W8L
 // stream over a workgroup's tiles, through a ring of LDS stages loaded straight
 // from memory; results pass through the stage used last, to leave in whole lines.
 //
-// What bounds it: 8192 tokens, 6144 -> 16384, 729 us, 2.26 POP/s: matrix
+// What bounds it: 8192 tokens, 6144 -> 16384, 739 to 763 us, 2.16 to 2.23 POP/s: matrix
 // products alone, without loads, ran 512 us at the clock that their power left
 // (1.5 to 1.8 GHz); 256 x 256 tiles read 6.4 GB through L2s that hold 79 % of
 // it.  Steps of 64 in four stages, beginning elsewhere along k, and eight
@@ -419,8 +420,9 @@ hipError_t launch_w8_linear(const W8LinearArgs &a, int dtype, hipStream_t st) {
         // 46.4 or 51.3; 64 tokens, 6144 -> 6144, 15.6 or 29.2
         if (a.tokens <= 160) return split_by_channels<T, 5, 6, 1, 5, 4>(a, st);
         // More tokens: rounds of workgroups by what one takes, in 42 us at k = 6144: 128 x 64 tiles, two a CU, 1 (0.65 if one
-        // a CU is enough); 256 x 128: 1.15; 256 x 256: 2.1.  512 tokens, 6144 -> 6144: 41.8, 47.4 and 87.5 us; 1024 tokens:
-        // 77.9, 49.4, 86.8; 2048 tokens: 122, 95.9, 88.6; 8192 tokens, -> 16384: 1210, 815, 750.
+        // a CU is enough); 256 x 128: 1.15; 256 x 256: 2.1.  Inputs in turn, codes evenly spread (which take more power than
+        // activations'): 512 tokens, 6144 -> 6144: 43.7, 49.7 and 89.0 us; 1024 tokens: 80.8, 50.4, 90.6; 2048 tokens: 124,
+        // 101, 92.4; 8192 tokens, -> 16384: 1264, 830, 769.
         auto tiles_of = [&](int64_t m, int64_t n) { return (a.n_out + m - 1) / m * ((a.tokens + n - 1) / n); };
         const int64_t small = tiles_of(128, 64);
         const double c64 = small <= 256 ? 0.65 : (double)((small + 511) / 512);
